@@ -38,6 +38,15 @@ SGEMM_HALF_BF16 = 0
 SGEMM_HALF_FP16 = 1
 HALF_TYPES = {"bf16": SGEMM_HALF_BF16, "fp16": SGEMM_HALF_FP16}
 
+SGEMM_TYPE_BF16 = 0
+SGEMM_TYPE_FP16 = 1
+SGEMM_TYPE_FP32 = 2
+ROW_TYPES = {"bf16": SGEMM_TYPE_BF16, "fp16": SGEMM_TYPE_FP16, "fp32": SGEMM_TYPE_FP32}
+
+SGEMM_ACT_NONE = 0
+SGEMM_ACT_SWIGLU = 1
+ACTS = {"none": SGEMM_ACT_NONE, "swiglu": SGEMM_ACT_SWIGLU}
+
 SGEMM_ROUTE_AUTO = 0
 SGEMM_ROUTE_SMALL = 1
 SGEMM_ROUTE_PAIR = 2
@@ -92,6 +101,18 @@ SIGNATURES = {
     "la_chunk_state": (_i, [_i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p]),
     "la_chunk_output": (_i, [_i, _i, _i, _i, _f, _p, _p, _p, _p, _p, _p, _p]),
     "la_chunk_fused": (_i, [_i, _i, _i, _i, _f, _p, _p, _p, _p, _p, _p, _p, _p]),
+    # include/int8_gemm.h
+    "sgemm_i8_quantize_rows": (_i, [_i, _i, _i, _i, _p, _i, _p, _i, _p, _p]),
+    "sgemm_i8": (_i, [_i, _i, _i, _i, _p, _i, _p, _p, _i, _p, _p, _i, _p]),
+    "sgemm_i8_experts": (_i, [_i, _i, _i, _i, _i, _p, _p, _i, _p, _p, _i, _ll, _p, _p, _i, _p]),
+    # include/expert_layer.h
+    "sgemm_experts_sort": (_i, [_i, _i, _i, _p, _p, _p, _p, _p]),
+    "sgemm_experts_dispatch": (_i, [_i, _i, _i, _i, _i, _p, _i, _p, _p, _p, _i, _p]),
+    "sgemm_experts_dispatch_i8": (_i, [_i, _i, _i, _i, _i, _p, _i, _p, _p, _p, _i, _p, _p]),
+    "sgemm_experts_dispatch_grad": (_i, [_i, _i, _i, _i, _i, _p, _i, _p, _p, _p, _i, _p]),
+    "sgemm_experts_combine": (_i, [_i, _i, _i, _i, _i, _p, _i, _p, _p, _p, _p, _i, _p]),
+    "sgemm_experts_combine_grad": (_i, [_i, _i, _i, _i, _i, _p, _i, _p, _i, _p, _p, _p, _p, _i,
+                                        _p, _p]),
 }
 
 
@@ -327,6 +348,75 @@ def la_chunk_output(BH, T, DK, DV, scale, q, k, v, g, h, o, stream=None) -> int:
 def la_chunk_fused(BH, T, DK, DV, scale, q, k, v, g, h0, o, state_out, stream=None) -> int:
     return _lib.la_chunk_fused(BH, T, DK, DV, scale, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
                                _ptr(h0), _ptr(o), _ptr(state_out), _stream(stream))
+
+
+# ---- 8-bit integer products (include/int8_gemm.h)
+
+def _type(type_) -> int:
+    return ROW_TYPES[type_] if isinstance(type_, str) else type_
+
+
+def sgemm_i8_quantize_rows(type_, act, M, K, X, ldx, Q, ldq, scale, stream=None) -> int:
+    """Q: device buffer of 8-bit integers (a torch int8 tensor or a raw
+    address), scale: M fp32 values."""
+    if isinstance(act, str):
+        act = ACTS[act]
+    return _lib.sgemm_i8_quantize_rows(_type(type_), act, M, K, _ptr(X), ldx, _ptr(Q), ldq,
+                                       _ptr(scale), _stream(stream))
+
+
+def sgemm_i8(type_, M, N, K, A, lda, scaleA, B, ldb, scaleB, C, ldc, stream=None) -> int:
+    return _lib.sgemm_i8(_type(type_), M, N, K, _ptr(A), lda, _ptr(scaleA), _ptr(B), ldb,
+                         _ptr(scaleB), _ptr(C), ldc, _stream(stream))
+
+
+def sgemm_i8_experts(type_, M, N, K, E, offsets, A, lda, scaleA, B, ldb, strideB, scaleB, C, ldc,
+                     stream=None) -> int:
+    return _lib.sgemm_i8_experts(_type(type_), M, N, K, E, _ptr(offsets), _ptr(A), lda,
+                                 _ptr(scaleA), _ptr(B), ldb, strideB, _ptr(scaleB), _ptr(C), ldc,
+                                 _stream(stream))
+
+
+# ---- tokens to experts and back (include/expert_layer.h)
+
+def sgemm_experts_sort(T, k, E, ids, offsets, slots, positions, stream=None) -> int:
+    """ids, offsets, slots, positions: 32-bit integers on the device."""
+    return _lib.sgemm_experts_sort(T, k, E, _ptr(ids), _ptr(offsets), _ptr(slots),
+                                   _ptr(positions), _stream(stream))
+
+
+def sgemm_experts_dispatch(type_, T, k, E, H, x, ldx, positions, offsets, rows, ldr,
+                           stream=None) -> int:
+    return _lib.sgemm_experts_dispatch(_type(type_), T, k, E, H, _ptr(x), ldx, _ptr(positions),
+                                       _ptr(offsets), _ptr(rows), ldr, _stream(stream))
+
+
+def sgemm_experts_dispatch_i8(type_, T, k, E, H, x, ldx, positions, offsets, q, ldq, scale,
+                              stream=None) -> int:
+    return _lib.sgemm_experts_dispatch_i8(_type(type_), T, k, E, H, _ptr(x), ldx,
+                                          _ptr(positions), _ptr(offsets), _ptr(q), ldq,
+                                          _ptr(scale), _stream(stream))
+
+
+def sgemm_experts_dispatch_grad(type_, T, k, E, H, drows, ldr, positions, offsets, dx, ldx,
+                                stream=None) -> int:
+    return _lib.sgemm_experts_dispatch_grad(_type(type_), T, k, E, H, _ptr(drows), ldr,
+                                            _ptr(positions), _ptr(offsets), _ptr(dx), ldx,
+                                            _stream(stream))
+
+
+def sgemm_experts_combine(type_, T, k, E, H, rows, ldr, positions, offsets, weights, out, ldo,
+                          stream=None) -> int:
+    return _lib.sgemm_experts_combine(_type(type_), T, k, E, H, _ptr(rows), ldr, _ptr(positions),
+                                      _ptr(offsets), _ptr(weights), _ptr(out), ldo,
+                                      _stream(stream))
+
+
+def sgemm_experts_combine_grad(type_, T, k, E, H, dout, ldo, rows, ldr, positions, offsets,
+                               weights, drows, ldd, dweights, stream=None) -> int:
+    return _lib.sgemm_experts_combine_grad(_type(type_), T, k, E, H, _ptr(dout), ldo, _ptr(rows),
+                                           ldr, _ptr(positions), _ptr(offsets), _ptr(weights),
+                                           _ptr(drows), ldd, _ptr(dweights), _stream(stream))
 
 
 def check(status: int) -> None:

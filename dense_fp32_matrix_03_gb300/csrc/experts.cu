@@ -1,0 +1,538 @@
+// experts.cu -- tokens sorted by expert and back (include/expert_layer.h):
+// the stable sort, and the row kernels of dispatch, combine and their
+// gradients.
+#include "../../include/expert_layer.h"
+#include "rows.cuh"
+
+namespace sg {
+namespace ex {
+
+using rows::aligned_to;
+using rows::Vec;
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxChoices = 64;   // k
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kGroup = 8;         // choices of a token whose rows are in flight together
+
+// ------------------------------------------------------------------ sort
+//
+// position(s) = (choices of smaller experts) + (earlier choices of the same
+// expert): a counting sort.  The choices are cut into one contiguous segment
+// per warp, in order, over a cluster of CTAs, so that ranks within a segment
+// need no atomics and the order is stable by construction:
+//   1. each warp counts its segment into a histogram of its own (lanes of
+//      equal key found with a warp match, their leader adds their number);
+//   2. a scan over the CTA's warps turns counts into the warp's first rank,
+//      and the CTAs' totals, read through distributed shared memory, into
+//      each expert's first position and each CTA's share of it;
+//   3. each warp walks its segment again and hands out positions.
+// One launch; the choices (4 bytes each) are read twice, the second time
+// from L2.  The bytes are few (12 per choice): what bounds it is the chain
+// of launch, two walks and two cluster barriers.
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return static_cast<int>(r);
+}
+__device__ __forceinline__ int cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return static_cast<int>(r);
+}
+// An int of CTA `rank`'s shared memory, at this CTA's address p.
+__device__ __forceinline__ int cluster_load(const int *p, int rank)
+{
+    uint32_t a, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(a)
+                 : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return static_cast<int>(v);
+}
+
+__device__ __forceinline__ int sort_key(const int *ids, long long i, int S, int E)
+{
+    if (i >= S) return -1;
+    const int e = ids[i];
+    return (e < 0 || e >= E) ? E : e;
+}
+
+__global__ void __launch_bounds__(kSortThreads, 1)
+    sort_kernel(const int *__restrict__ ids, int S, int E, int *__restrict__ offsets,
+                int *__restrict__ slots, int *__restrict__ positions)
+{
+    extern __shared__ int sm[];
+    const int E1 = E + 1;
+    int *hist = sm;                       // [kSortWarps][E1]
+    int *tot = hist + kSortWarps * E1;    // [E1] this CTA's counts
+    int *base = tot + E1;                 // [E1] this CTA's first position of each key
+    __shared__ int wsum[kSortWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = cluster_rank(), ncta = cluster_size();
+    const int segs = ncta * kSortWarps;
+    const long long len = ((static_cast<long long>(S) + segs - 1) / segs + 31) / 32 * 32;
+    const long long lo = (static_cast<long long>(rank) * kSortWarps + warp) * len;
+    const long long hi = min(lo + len, static_cast<long long>(S));
+    int *mine = hist + warp * E1;
+
+    for (int i = tid; i < kSortWarps * E1; i += kSortThreads) hist[i] = 0;
+    __syncthreads();
+    for (long long i = lo; i < hi; i += 32) {
+        const int key = sort_key(ids, i + lane, S, E);
+        const unsigned same = __match_any_sync(0xffffffffu, key);
+        if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int e = tid; e < E1; e += kSortThreads) {
+        int run = 0;
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int n = hist[w * E1 + e];
+            hist[w * E1 + e] = run;
+            run += n;
+        }
+        tot[e] = run;
+    }
+    cluster_barrier();
+    int before = 0, all = 0;  // key tid: in earlier CTAs, in all CTAs
+    if (tid < E) {
+        for (int c = 0; c < ncta; ++c) {
+            const int n = cluster_load(&tot[tid], c);
+            if (c < rank) before += n;
+            all += n;
+        }
+    }
+    // exclusive scan of `all` over the keys (E <= kSortThreads)
+    int inc = all;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int n = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += n;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int ahead = 0, kept = 0;
+    for (int w = 0; w < kSortWarps; ++w) {
+        if (w < warp) ahead += wsum[w];
+        kept += wsum[w];
+    }
+    const int first = ahead + inc - all;
+    if (tid < E) base[tid] = first + before;
+    if (tid == 0) {  // dropped choices: behind the kept ones
+        int n = 0;
+        for (int c = 0; c < rank; ++c) n += cluster_load(&tot[E], c);
+        base[E] = kept + n;
+    }
+    if (rank == 0) {
+        if (tid < E) offsets[tid] = first;
+        if (tid == 0) offsets[E] = kept;
+    }
+    cluster_barrier();  // tot has been read by every CTA; base is written
+    for (long long i = lo; i < hi; i += 32) {
+        const int key = sort_key(ids, i + lane, S, E);
+        const unsigned same = __match_any_sync(0xffffffffu, key);
+        const int before_me = __popc(same & ((1u << lane) - 1u));
+        int p = 0;
+        if (key >= 0) p = base[key] + mine[key] + before_me;
+        __syncwarp();
+        if (key >= 0) {
+            positions[i + lane] = p;
+            slots[p] = static_cast<int>(i) + lane;
+            if (before_me == 0) mine[key] += __popc(same);
+        }
+        __syncwarp();
+    }
+}
+
+// -------------------------------------------------------------- row kernels
+//
+// All move whole rows and compute next to nothing: bound by HBM.  A block
+// takes blockDim.y tokens, blockDim.x threads over a row's vectors, and works
+// token by token: a token's k rows are read (combine) or written (dispatch)
+// together, so its own row moves once and up to kGroup loads per thread are
+// in flight.  p(t,j) is checked against T * k, so a corrupt position cannot
+// reach outside the rows.
+
+struct Args {
+    int T, k, S;              // S = T * k
+    int nvec;                 // vectors in a row
+    const int *positions;
+    const int *total;         // offsets[E]: the kept choices
+    const float *weights;     // may be null: 1
+    const char *tok;          // rows of tokens (x, dout)
+    char *tok_out;            // rows of tokens written (out, dx)
+    const char *row;          // rows by expert read
+    char *row_out;            // rows by expert written
+    float *dweights;
+    long long tok_pitch, row_pitch, row_out_pitch;  // bytes
+};
+
+template <class T, int VB>
+__global__ void __launch_bounds__(256) dispatch_kernel(const Args a)
+{
+    const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (t >= a.T) return;
+    const int total = *a.total;
+    for (int j0 = 0; j0 < a.k; j0 += kGroup) {
+        int p[kGroup];
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j)
+            p[j] = j0 + j < a.k ? a.positions[t * a.k + j0 + j] : -1;
+        for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < a.nvec;
+             v += gridDim.y * blockDim.x) {
+            Vec<T, VB> x, z;
+            x.load(a.tok + t * a.tok_pitch + static_cast<long long>(v) * VB);
+            z.zero();
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                if (p[j] >= 0 && p[j] < a.S)
+                    (p[j] < total ? x : z)
+                        .store(a.row_out + p[j] * a.row_out_pitch +
+                               static_cast<long long>(v) * VB);
+        }
+    }
+}
+
+template <class T, int VB>
+__global__ void __launch_bounds__(256) combine_kernel(const Args a)
+{
+    using V = Vec<T, VB>;
+    const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (t >= a.T) return;
+    const int total = min(*a.total, a.S);
+    for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < a.nvec; v += gridDim.y * blockDim.x) {
+        float acc[V::N];
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) acc[i] = 0.f;
+        for (int j0 = 0; j0 < a.k; j0 += kGroup) {
+            V x[kGroup];
+            float w[kGroup];
+            bool on[kGroup];
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+                on[j] = false;
+                if (j0 + j < a.k) {
+                    const int p = a.positions[t * a.k + j0 + j];
+                    w[j] = a.weights ? a.weights[t * a.k + j0 + j] : 1.f;
+                    on[j] = p >= 0 && p < total;
+                    if (on[j])
+                        x[j].load(a.row + p * a.row_pitch + static_cast<long long>(v) * VB);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                if (on[j]) {
+#pragma unroll
+                    for (int i = 0; i < V::N; ++i) acc[i] = fmaf(w[j], x[j].get(i), acc[i]);
+                }
+        }
+        V o;
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) o.set(i, acc[i]);
+        o.store(a.tok_out + t * a.tok_pitch + static_cast<long long>(v) * VB);
+    }
+}
+
+// DW: dweights wanted (rows is read).  blockDim.x threads of one token sum
+// their products over the row, then over lanes and warps in a fixed order.
+template <class T, int VB, bool DW>
+__global__ void __launch_bounds__(256) combine_grad_kernel(const Args a)
+{
+    using V = Vec<T, VB>;
+    __shared__ float part[8][kGroup];  // one row per warp of the block
+    const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const bool live = t < a.T;
+    const int total = min(*a.total, a.S);
+    const int wid = (threadIdx.y * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+    for (int j0 = 0; j0 < a.k; j0 += kGroup) {
+        float w[kGroup], dw[kGroup];
+        int p[kGroup];
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) {
+            const bool in = live && j0 + j < a.k;
+            p[j] = in ? a.positions[t * a.k + j0 + j] : -1;
+            if (p[j] >= a.S) p[j] = -1;
+            w[j] = in && a.weights ? a.weights[t * a.k + j0 + j] : 1.f;
+            dw[j] = 0.f;
+        }
+        for (int v = threadIdx.x; live && v < a.nvec; v += blockDim.x) {
+            const long long at = static_cast<long long>(v) * VB;
+            V g, x[kGroup];
+            g.load(a.tok + t * a.tok_pitch + at);
+            if (DW) {
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    if (p[j] >= 0 && p[j] < total) x[j].load(a.row + p[j] * a.row_pitch + at);
+            }
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+                if (p[j] < 0) continue;
+                V o;
+                if (p[j] < total) {
+#pragma unroll
+                    for (int i = 0; i < V::N; ++i) {
+                        if (DW) dw[j] = fmaf(x[j].get(i), g.get(i), dw[j]);
+                        o.set(i, w[j] * g.get(i));
+                    }
+                } else {
+                    o.zero();
+                }
+                o.store(a.row_out + p[j] * a.row_out_pitch + at);
+            }
+        }
+        if (DW) {
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+#pragma unroll
+                for (int d = 16; d > 0; d /= 2) dw[j] += __shfl_xor_sync(0xffffffffu, dw[j], d);
+                if (lane == 0) part[wid][j] = dw[j];
+            }
+            __syncthreads();
+            const int warps = blockDim.x >> 5;
+            if (live && threadIdx.x < kGroup && j0 + static_cast<int>(threadIdx.x) < a.k) {
+                float s = 0.f;
+                for (int i = 0; i < warps; ++i) s += part[threadIdx.y * warps + i][threadIdx.x];
+                a.dweights[t * a.k + j0 + threadIdx.x] = s;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// Threads over a row and tokens per block (256 threads, at least a warp per
+// token), and blocks over a row's columns: enough that few tokens still
+// spread over the GPU.
+struct Grid {
+    dim3 grid, block;
+};
+Grid row_grid(int T, int nvec, bool split_columns)
+{
+    const int tx = rows::pow2_threads(nvec, 32, 256), ty = 256 / tx;
+    const unsigned gx = static_cast<unsigned>((static_cast<long long>(T) + ty - 1) / ty);
+    unsigned gy = 1;
+    if (split_columns) {
+        gy = static_cast<unsigned>((nvec + tx - 1) / tx);
+        if (gy > 64) gy = 64;
+    }
+    return {dim3(gx, gy), dim3(static_cast<unsigned>(tx), static_cast<unsigned>(ty))};
+}
+
+enum Op { kDispatch, kCombine, kCombineGrad };
+
+struct Launch {
+    Op op;
+    const Args &a;
+    cudaStream_t st;
+    template <class T, int VB>
+    int run() const
+    {
+        const Grid g = row_grid(a.T, a.nvec, op != kCombineGrad);
+        if (op == kDispatch)
+            dispatch_kernel<T, VB><<<g.grid, g.block, 0, st>>>(a);
+        else if (op == kCombine)
+            combine_kernel<T, VB><<<g.grid, g.block, 0, st>>>(a);
+        else if (a.dweights != nullptr)
+            combine_grad_kernel<T, VB, true><<<g.grid, g.block, 0, st>>>(a);
+        else
+            combine_grad_kernel<T, VB, false><<<g.grid, g.block, 0, st>>>(a);
+        if (cudaGetLastError() != cudaSuccess) return SGEMM_ERR_LAUNCH;
+        note_launch();
+        return SGEMM_OK;
+    }
+};
+
+bool dims_ok(int T, int k, int E)
+{
+    return T >= 0 && k >= 1 && k <= kMaxChoices && E >= 1 && E <= kMaxExperts &&
+           static_cast<long long>(T) * k <= 0x7FFFFFFFLL;
+}
+
+}  // namespace ex
+}  // namespace sg
+
+using namespace sg;
+using ex::Args;
+
+namespace {
+
+bool int_aligned(const void *p) { return rows::aligned_to(p, 4); }
+
+// The checks every row call shares; ok = false: return rc as it is.
+struct Checked {
+    int rc;
+    bool run;
+};
+Checked check_rows(int type, int T, int k, int E, int H, const void *tok, int ld_tok,
+                   const void *row, int ld_row, const int *positions, const int *offsets)
+{
+    if (!rows::valid_type(type) || !ex::dims_ok(T, k, E) || H < 0 || ld_tok < 1 || ld_row < 1 ||
+        ld_tok < H || ld_row < H)
+        return {SGEMM_ERR_INVALID_ARG, false};
+    if (T == 0) return {SGEMM_OK, false};
+    const int es = rows::elem_size(type);
+    if (positions == nullptr || offsets == nullptr || !int_aligned(positions) ||
+        !int_aligned(offsets))
+        return {SGEMM_ERR_INVALID_ARG, false};
+    if (H > 0 && (tok == nullptr || row == nullptr || !rows::aligned_to(tok, es) ||
+                  !rows::aligned_to(row, es)))
+        return {SGEMM_ERR_INVALID_ARG, false};
+    return {SGEMM_OK, true};
+}
+
+Args base_args(int T, int k, int E, const int *positions, const int *offsets)
+{
+    Args a{};
+    a.T = T;
+    a.k = k;
+    a.S = T * k;
+    a.positions = positions;
+    a.total = offsets + E;
+    return a;
+}
+
+bool on_gpu()
+{
+    int num_sms = 0;
+    unsigned int *status = nullptr;
+    return current_sm103(&num_sms, &status);
+}
+
+int combine(int type, int T, int k, int E, int H, const void *rws, int ldr, const int *positions,
+            const int *offsets, const float *weights, void *out, int ldo, void *stream)
+{
+    const Checked c = check_rows(type, T, k, E, H, out, ldo, rws, ldr, positions, offsets);
+    if (!c.run) return c.rc;
+    if (!int_aligned(weights)) return SGEMM_ERR_INVALID_ARG;
+    if (H == 0) return SGEMM_OK;
+    if (!on_gpu()) return SGEMM_ERR_UNSUPPORTED;
+    const long long es = rows::elem_size(type);
+    Args a = base_args(T, k, E, positions, offsets);
+    a.weights = weights;
+    a.row = static_cast<const char *>(rws);
+    a.tok_out = static_cast<char *>(out);
+    a.row_pitch = ldr * es;
+    a.tok_pitch = ldo * es;
+    const int vb = rows::Width().add(rws).add(out).add(a.row_pitch).add(a.tok_pitch).add(H * es).bytes();
+    a.nvec = static_cast<int>(H * es / vb);
+    return rows::with_vec(type, vb, ex::Launch{ex::kCombine, a, static_cast<cudaStream_t>(stream)});
+}
+
+}  // namespace
+
+extern "C" {
+
+int sgemm_experts_sort(int T, int k, int E, const int *ids, int *offsets, int *slots,
+                       int *positions, void *stream)
+{
+    if (!ex::dims_ok(T, k, E) || offsets == nullptr || !int_aligned(offsets))
+        return SGEMM_ERR_INVALID_ARG;
+    const int S = T * k;
+    if (S > 0 && (ids == nullptr || slots == nullptr || positions == nullptr ||
+                  !int_aligned(ids) || !int_aligned(slots) || !int_aligned(positions)))
+        return SGEMM_ERR_INVALID_ARG;
+    if (!on_gpu()) return SGEMM_ERR_UNSUPPORTED;
+    const int smem = (ex::kSortWarps + 2) * (E + 1) * static_cast<int>(sizeof(int));
+    if (!smem_attr_once(reinterpret_cast<const void *>(ex::sort_kernel), smem))
+        return SGEMM_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg{};
+    // one CTA walks up to 4096 choices in four steps per warp and walk
+    const unsigned ncta = S <= 4096 ? 1u : static_cast<unsigned>(ex::kMaxCluster);
+    cfg.gridDim = dim3(ncta);
+    cfg.blockDim = dim3(ex::kSortThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ncta;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, ex::sort_kernel, ids, S, E, offsets, slots, positions) !=
+        cudaSuccess) {
+        cudaGetLastError();
+        return SGEMM_ERR_LAUNCH;
+    }
+    note_launch();
+    return SGEMM_OK;
+}
+
+int sgemm_experts_dispatch(int type, int T, int k, int E, int H, const void *x, int ldx,
+                           const int *positions, const int *offsets, void *rws, int ldr,
+                           void *stream)
+{
+    const Checked c = check_rows(type, T, k, E, H, x, ldx, rws, ldr, positions, offsets);
+    if (!c.run || H == 0) return c.rc;
+    if (!on_gpu()) return SGEMM_ERR_UNSUPPORTED;
+    const long long es = rows::elem_size(type);
+    Args a = base_args(T, k, E, positions, offsets);
+    a.tok = static_cast<const char *>(x);
+    a.row_out = static_cast<char *>(rws);
+    a.tok_pitch = ldx * es;
+    a.row_out_pitch = ldr * es;
+    const int vb =
+        rows::Width().add(x).add(rws).add(a.tok_pitch).add(a.row_out_pitch).add(H * es).bytes();
+    a.nvec = static_cast<int>(H * es / vb);
+    return rows::with_vec(type, vb, ex::Launch{ex::kDispatch, a, static_cast<cudaStream_t>(stream)});
+}
+
+int sgemm_experts_dispatch_grad(int type, int T, int k, int E, int H, const void *drows, int ldr,
+                                const int *positions, const int *offsets, void *dx, int ldx,
+                                void *stream)
+{
+    return combine(type, T, k, E, H, drows, ldr, positions, offsets, nullptr, dx, ldx, stream);
+}
+
+int sgemm_experts_combine(int type, int T, int k, int E, int H, const void *rws, int ldr,
+                          const int *positions, const int *offsets, const float *weights,
+                          void *out, int ldo, void *stream)
+{
+    return combine(type, T, k, E, H, rws, ldr, positions, offsets, weights, out, ldo, stream);
+}
+
+int sgemm_experts_combine_grad(int type, int T, int k, int E, int H, const void *dout, int ldo,
+                               const void *rws, int ldr, const int *positions,
+                               const int *offsets, const float *weights, void *drows, int ldd,
+                               float *dweights, void *stream)
+{
+    const Checked c = check_rows(type, T, k, E, H, dout, ldo, drows, ldd, positions, offsets);
+    if (!c.run) return c.rc;
+    const long long es = rows::elem_size(type);
+    if (!int_aligned(weights) || !int_aligned(dweights)) return SGEMM_ERR_INVALID_ARG;
+    if (dweights != nullptr && H > 0 &&
+        (rws == nullptr || ldr < H || !rows::aligned_to(rws, static_cast<int>(es))))
+        return SGEMM_ERR_INVALID_ARG;
+    if (H == 0 && dweights == nullptr) return SGEMM_OK;
+    if (!on_gpu()) return SGEMM_ERR_UNSUPPORTED;
+    Args a = base_args(T, k, E, positions, offsets);
+    a.weights = weights;
+    a.tok = static_cast<const char *>(dout);
+    a.row_out = static_cast<char *>(drows);
+    a.dweights = dweights;
+    a.tok_pitch = ldo * es;
+    a.row_out_pitch = ldd * es;
+    rows::Width w;
+    w.add(dout).add(drows).add(a.tok_pitch).add(a.row_out_pitch).add(H * es);
+    if (dweights != nullptr) {
+        a.row = static_cast<const char *>(rws);
+        a.row_pitch = ldr * es;
+        w.add(rws).add(a.row_pitch);
+    }
+    // H == 0: pointers may be null; the kernel writes zero dweights only
+    const int vb = H == 0 ? 16 : w.bytes();
+    a.nvec = static_cast<int>(H * es / vb);
+    return rows::with_vec(type, vb,
+                          ex::Launch{ex::kCombineGrad, a, static_cast<cudaStream_t>(stream)});
+}
+
+}  // extern "C"

@@ -1,0 +1,170 @@
+// i8_gemm.cu -- products of 8-bit integers with a scale for each token and
+// channel (include/int8_gemm.h): argument checks and the integer dot-product
+// kernel.
+#include "../../include/int8_gemm.h"
+#include "i8_gemm.h"
+#include "rows.cuh"
+
+namespace sg {
+namespace i8 {
+
+// ------------------------------------------------- integer dot products
+//
+// C tiles of 64 tokens x 64 channels by 256 threads, 4 x 4 each, over steps
+// of 64 k staged in shared memory as words of four 8-bit values (dp4a: four
+// products and an exact 32-bit sum).  Any base and leading dimension: words
+// are read whole where all allow it, byte by byte otherwise; bytes past K
+// read as zero.
+constexpr int kDT = 64, kDK = 64, kDW = kDK / 4;
+
+template <bool WORDS>
+__device__ __forceinline__ uint32_t load4(const signed char *row, int k, int K)
+{
+    if (k >= K) return 0u;
+    if (WORDS && k + 4 <= K) return *reinterpret_cast<const uint32_t *>(row + k);
+    uint32_t w = 0;
+    for (int i = 0; i < 4 && k + i < K; ++i)
+        w |= (static_cast<uint32_t>(row[k + i]) & 255u) << (8 * i);
+    return w;
+}
+
+template <class T, bool WORDS>
+__global__ void __launch_bounds__(256) dot_kernel(const Args a)
+{
+    __shared__ uint32_t As[kDW][kDT + 1], Bs[kDW][kDT + 1];
+    __shared__ Tile tl;
+    const int tid = threadIdx.x;
+    if (tid < 32) {
+        const Tile t = find_tile_warp(a, blockIdx.y, kDT, tid);
+        if (tid == 0) tl = t;
+    }
+    __syncthreads();
+    if (tl.e < 0) return;
+    const int n0 = blockIdx.x * kDT;
+    const signed char *B = a.B + tl.e * a.strideB;
+    int acc[4][4] = {};
+    const int tm = (tid >> 4) * 4, tn = (tid & 15) * 4;
+    for (int k0 = 0; k0 < a.K; k0 += kDK) {
+        for (int i = tid; i < kDT * kDW; i += 256) {
+            const int r = i / kDW, w = i % kDW;
+            As[w][r] = r < tl.rows ? load4<WORDS>(a.A + (tl.row0 + r) * a.lda, k0 + 4 * w, a.K) : 0u;
+            Bs[w][r] = n0 + r < a.N
+                           ? load4<WORDS>(B + static_cast<long long>(n0 + r) * a.ldb, k0 + 4 * w, a.K)
+                           : 0u;
+        }
+        __syncthreads();
+#pragma unroll 4
+        for (int w = 0; w < kDW; ++w) {
+            int x[4], y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = static_cast<int>(As[w][tm + i]);
+                y[i] = static_cast<int>(Bs[w][tn + i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(x[i], y[j], acc[i][j]);
+        }
+        __syncthreads();
+    }
+    const float *sb = a.scaleB + static_cast<long long>(tl.e) * a.N;
+    for (int i = 0; i < 4; ++i) {
+        if (tm + i >= tl.rows) break;
+        const float sa = a.scaleA[tl.row0 + tm + i];
+        T *c = static_cast<T *>(a.C) + (tl.row0 + tm + i) * a.ldc;
+        for (int j = 0; j < 4; ++j)
+            if (n0 + tn + j < a.N)
+                c[n0 + tn + j] =
+                    rows::from_f<T>(static_cast<float>(acc[i][j]) * sa * sb[n0 + tn + j]);
+    }
+}
+
+template <class T>
+int launch_dot(const Args &a, cudaStream_t st)
+{
+    const bool words = rows::aligned_to(a.A, 4) && rows::aligned_to(a.B, 4) && a.lda % 4 == 0 &&
+                       a.ldb % 4 == 0 && a.strideB % 4 == 0;
+    const long long gy = max_tiles(a, kDT), gx = (a.N + kDT - 1LL) / kDT;
+    // grid.y holds 65535 tiles: longer calls go in pieces
+    for (long long y0 = 0; y0 < gy; y0 += 65535) {
+        Args b = a;
+        b.tile0 = static_cast<int>(y0);
+        const dim3 grid(static_cast<unsigned>(gx),
+                        static_cast<unsigned>(gy - y0 < 65535 ? gy - y0 : 65535));
+        if (words)
+            dot_kernel<T, true><<<grid, 256, 0, st>>>(b);
+        else
+            dot_kernel<T, false><<<grid, 256, 0, st>>>(b);
+        if (cudaGetLastError() != cudaSuccess) return SGEMM_ERR_LAUNCH;
+        note_launch();
+    }
+    return SGEMM_OK;
+}
+
+int run(int type, const Args &a, cudaStream_t st)
+{
+    if (type == SGEMM_TYPE_BF16) return launch_dot<__nv_bfloat16>(a, st);
+    if (type == SGEMM_TYPE_FP16) return launch_dot<__half>(a, st);
+    return launch_dot<float>(a, st);
+}
+
+// Checks and enqueues a product; offsets null: one dense group of M rows.
+int product(int type, int M, int N, int K, int E, const int *offsets, const signed char *A,
+            int lda, const float *scaleA, const signed char *B, int ldb, long long strideB,
+            const float *scaleB, void *C, int ldc, void *stream)
+{
+    if (!rows::valid_type(type) || M < 0 || N < 0 || K < 0 || lda < 1 || ldb < 1 || ldc < 1 ||
+        lda < K || ldb < K || ldc < N || K > kMaxK)
+        return SGEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return SGEMM_OK;
+    if (C == nullptr || scaleA == nullptr || scaleB == nullptr ||
+        !rows::aligned_to(C, rows::elem_size(type)) || !rows::aligned_to(scaleA, 4) ||
+        !rows::aligned_to(scaleB, 4))
+        return SGEMM_ERR_INVALID_ARG;
+    if (K > 0 && (A == nullptr || B == nullptr)) return SGEMM_ERR_INVALID_ARG;
+    Args a{};
+    if (!current_sm103(&a.num_sms, &a.status)) return SGEMM_ERR_UNSUPPORTED;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.E = E;
+    a.offsets = offsets;
+    a.A = A;
+    a.B = B;
+    a.lda = lda;
+    a.ldb = ldb;
+    a.strideB = strideB;
+    a.scaleA = scaleA;
+    a.scaleB = scaleB;
+    a.C = C;
+    a.ldc = ldc;
+    return run(type, a, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace i8
+}  // namespace sg
+
+extern "C" {
+
+int sgemm_i8(int type, int M, int N, int K, const signed char *A, int lda, const float *scaleA,
+             const signed char *B, int ldb, const float *scaleB, void *C, int ldc, void *stream)
+{
+    return sg::i8::product(type, M, N, K, 1, nullptr, A, lda, scaleA, B, ldb, 0, scaleB, C, ldc,
+                           stream);
+}
+
+int sgemm_i8_experts(int type, int M, int N, int K, int E, const int *offsets,
+                     const signed char *A, int lda, const float *scaleA, const signed char *B,
+                     int ldb, long long strideB, const float *scaleB, void *C, int ldc,
+                     void *stream)
+{
+    if (E < 1 || E > sg::i8::kMaxExperts || offsets == nullptr ||
+        !sg::rows::aligned_to(offsets, 4) || strideB < 0 ||
+        (E > 1 && N > 0 && strideB < (N - 1LL) * ldb + K))
+        return SGEMM_ERR_INVALID_ARG;
+    return sg::i8::product(type, M, N, K, E, offsets, A, lda, scaleA, B, ldb, strideB, scaleB, C,
+                           ldc, stream);
+}
+
+}  // extern "C"

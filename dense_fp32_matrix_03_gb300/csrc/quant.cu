@@ -1,0 +1,269 @@
+// quant.cu -- rows quantised to 8-bit integers with one scale each
+// (include/int8_gemm.h), plain, of the gated activation, or copied into
+// expert order on the way (include/expert_layer.h).
+//
+// One pass: a row's values are held in registers between the maximum and the
+// rounding, so each is read once and its code written once (a row longer
+// than the block's registers reads its tail a second time, from L2).  The
+// maximum is taken on the bit patterns of the magnitudes, where an infinity
+// or NaN is larger than every finite value and so cannot be missed.
+#include "../../include/expert_layer.h"
+#include "rows.cuh"
+
+namespace sg {
+namespace qz {
+
+using rows::Vec;
+
+constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100
+constexpr int kHeld = 4;                         // vectors per thread kept in registers
+
+struct Args {
+    int M, K;               // rows, values (codes) per row
+    int nvec;               // vectors per row
+    const char *x;
+    long long x_pitch;      // bytes
+    long long up;           // SwiGLU: bytes from the gates to the values
+    signed char *q;
+    long long ldq;
+    float *scale;
+    // expert order: row t goes to positions[t * k + j] for every j
+    const int *positions, *total;
+    int k, S;
+};
+
+// EV codes as one access of EV bytes where QV says q allows it.
+template <int EV, bool QV>
+__device__ __forceinline__ void store_codes(signed char *p, const int (&c)[EV])
+{
+    if constexpr (QV && EV >= 2) {
+        uint32_t w[(EV + 3) / 4] = {};
+#pragma unroll
+        for (int i = 0; i < EV; ++i)
+            w[i / 4] |= (static_cast<uint32_t>(c[i]) & 255u) << (8 * (i % 4));
+        if constexpr (EV == 8)
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        else if constexpr (EV == 4)
+            *reinterpret_cast<uint32_t *>(p) = w[0];
+        else
+            *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(w[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < EV; ++i) p[i] = static_cast<signed char>(c[i]);
+    }
+}
+
+// One vector of the values to quantise, in fp32.
+template <class T, int VB, bool GATED>
+__device__ __forceinline__ void load_values(const Args &a, const char *row, int v,
+                                            float (&f)[Vec<T, VB>::N])
+{
+    Vec<T, VB> g;
+    g.load(row + static_cast<long long>(v) * VB);
+    if constexpr (GATED) {
+        Vec<T, VB> u;
+        u.load(row + a.up + static_cast<long long>(v) * VB);
+#pragma unroll
+        for (int i = 0; i < Vec<T, VB>::N; ++i) {
+            const float x = g.get(i);
+            f[i] = x / (1.f + expf(-x)) * u.get(i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < Vec<T, VB>::N; ++i) f[i] = g.get(i);
+    }
+}
+
+template <class T, int VB, bool GATED, bool EXPERT, bool QV>
+__global__ void __launch_bounds__(256) quantize_kernel(const Args a)
+{
+    constexpr int EV = Vec<T, VB>::N;
+    __shared__ unsigned part[8];
+    const long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const bool live = r < a.M;
+    const char *row = a.x + (live ? r : 0) * a.x_pitch;
+    const int tx = threadIdx.x, nx = blockDim.x, warps = nx >> 5;
+    const int nvec = live ? a.nvec : 0;
+
+    float f[kHeld][EV];
+    unsigned big = 0;
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+        const int v = tx + h * nx;
+        if (v < nvec) load_values<T, VB, GATED>(a, row, v, f[h]);
+    }
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+        if (tx + h * nx < nvec)
+#pragma unroll
+            for (int i = 0; i < EV; ++i)
+                big = max(big, __float_as_uint(f[h][i]) & 0x7FFFFFFFu);
+    for (int v = tx + kHeld * nx; v < nvec; v += nx) {
+        float g[EV];
+        load_values<T, VB, GATED>(a, row, v, g);
+#pragma unroll
+        for (int i = 0; i < EV; ++i) big = max(big, __float_as_uint(g[i]) & 0x7FFFFFFFu);
+    }
+    big = __reduce_max_sync(0xffffffffu, big);
+    if (warps > 1) {
+        if ((tx & 31) == 0) part[threadIdx.y * warps + (tx >> 5)] = big;
+        __syncthreads();
+        for (int w = 0; w < warps; ++w) big = max(big, part[threadIdx.y * warps + w]);
+    }
+    if (!live) return;
+    const float amax = __uint_as_float(big);
+    const bool finite = big < 0x7F800000u, some = amax >= kTiny;
+    const float inv = finite && some ? __fdiv_rn(127.f, amax) : 0.f;
+    const float scale = !finite ? __int_as_float(0x7FFFFFFF)
+                                : (some ? __fdiv_rn(amax, 127.f) : 0.f);
+
+    auto codes = [&](const float (&x)[EV], int (&c)[EV]) {
+#pragma unroll
+        for (int i = 0; i < EV; ++i) c[i] = __float2int_rn(x[i] * inv);  // NaN -> 0
+    };
+    auto put = [&](int v, const int (&c)[EV]) {
+        if constexpr (EXPERT) {
+            const int total = *a.total;
+            int none[EV] = {};
+            for (int j = 0; j < a.k; ++j) {
+                const int p = a.positions[r * a.k + j];
+                if (p < 0 || p >= a.S) continue;
+                signed char *dst = a.q + p * a.ldq + static_cast<long long>(v) * EV;
+                if (p < total)
+                    store_codes<EV, QV>(dst, c);
+                else
+                    store_codes<EV, QV>(dst, none);
+            }
+        } else {
+            store_codes<EV, QV>(a.q + r * a.ldq + static_cast<long long>(v) * EV, c);
+        }
+    };
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+        const int v = tx + h * nx;
+        if (v < nvec) {
+            int c[EV];
+            codes(f[h], c);
+            put(v, c);
+        }
+    }
+    for (int v = tx + kHeld * nx; v < nvec; v += nx) {
+        float g[EV];
+        int c[EV];
+        load_values<T, VB, GATED>(a, row, v, g);
+        codes(g, c);
+        put(v, c);
+    }
+    if constexpr (EXPERT) {
+        for (int j = tx; j < a.k; j += nx) {
+            const int p = a.positions[r * a.k + j];
+            if (p >= 0 && p < a.S) a.scale[p] = p < *a.total ? scale : 0.f;
+        }
+    } else {
+        if (tx == 0) a.scale[r] = scale;
+    }
+}
+
+struct Launch {
+    const Args &a;
+    bool gated, expert;
+    cudaStream_t st;
+    template <class T, int VB, bool GATED, bool EXPERT>
+    int go() const
+    {
+        constexpr int EV = Vec<T, VB>::N;
+        const bool qv = rows::aligned_to(a.q, EV) && a.ldq % EV == 0;
+        const int tx = rows::pow2_threads((a.nvec + kHeld - 1) / kHeld, 32, 256), ty = 256 / tx;
+        const dim3 block(static_cast<unsigned>(tx), static_cast<unsigned>(ty));
+        const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.M) + ty - 1) / ty));
+        if (qv)
+            quantize_kernel<T, VB, GATED, EXPERT, true><<<grid, block, 0, st>>>(a);
+        else
+            quantize_kernel<T, VB, GATED, EXPERT, false><<<grid, block, 0, st>>>(a);
+        if (cudaGetLastError() != cudaSuccess) return SGEMM_ERR_LAUNCH;
+        note_launch();
+        return SGEMM_OK;
+    }
+    template <class T, int VB>
+    int run() const
+    {
+        if (expert) return go<T, VB, false, true>();
+        return gated ? go<T, VB, true, false>() : go<T, VB, false, false>();
+    }
+};
+
+}  // namespace qz
+}  // namespace sg
+
+using namespace sg;
+
+extern "C" {
+
+int sgemm_i8_quantize_rows(int type, int act, int M, int K, const void *X, int ldx,
+                           signed char *Q, int ldq, float *scale, void *stream)
+{
+    const bool gated = act == SGEMM_ACT_SWIGLU;
+    if (!rows::valid_type(type) || (act != SGEMM_ACT_NONE && !gated) || M < 0 || K < 0 ||
+        ldx < 1 || ldq < 1 || ldx < (gated ? 2LL * K : K) || ldq < K)
+        return SGEMM_ERR_INVALID_ARG;
+    if (M == 0) return SGEMM_OK;
+    const long long es = rows::elem_size(type);
+    if (scale == nullptr || !rows::aligned_to(scale, 4)) return SGEMM_ERR_INVALID_ARG;
+    if (K > 0 && (X == nullptr || Q == nullptr || !rows::aligned_to(X, static_cast<int>(es))))
+        return SGEMM_ERR_INVALID_ARG;
+    int num_sms = 0;
+    unsigned int *status = nullptr;
+    if (!current_sm103(&num_sms, &status)) return SGEMM_ERR_UNSUPPORTED;
+    qz::Args a{};
+    a.M = M;
+    a.K = K;
+    a.x = static_cast<const char *>(X);
+    a.x_pitch = ldx * es;
+    a.up = K * es;
+    a.q = Q;
+    a.ldq = ldq;
+    a.scale = scale;
+    const int vb = K == 0 ? 16 : rows::Width().add(X).add(a.x_pitch).add(a.up).bytes();
+    a.nvec = static_cast<int>(K * es / vb);
+    return rows::with_vec(type, vb,
+                          qz::Launch{a, gated, false, static_cast<cudaStream_t>(stream)});
+}
+
+int sgemm_experts_dispatch_i8(int type, int T, int k, int E, int H, const void *x, int ldx,
+                              const int *positions, const int *offsets, signed char *q, int ldq,
+                              float *scale, void *stream)
+{
+    if (!rows::valid_type(type) || T < 0 || k < 1 || k > 64 || E < 1 || E > 1024 ||
+        static_cast<long long>(T) * k > 0x7FFFFFFFLL || H < 0 || ldx < 1 || ldq < 1 || ldx < H ||
+        ldq < H)
+        return SGEMM_ERR_INVALID_ARG;
+    if (T == 0) return SGEMM_OK;
+    const long long es = rows::elem_size(type);
+    if (positions == nullptr || offsets == nullptr || scale == nullptr ||
+        !rows::aligned_to(positions, 4) || !rows::aligned_to(offsets, 4) ||
+        !rows::aligned_to(scale, 4))
+        return SGEMM_ERR_INVALID_ARG;
+    if (H > 0 && (x == nullptr || q == nullptr || !rows::aligned_to(x, static_cast<int>(es))))
+        return SGEMM_ERR_INVALID_ARG;
+    int num_sms = 0;
+    unsigned int *status = nullptr;
+    if (!current_sm103(&num_sms, &status)) return SGEMM_ERR_UNSUPPORTED;
+    qz::Args a{};
+    a.M = T;
+    a.K = H;
+    a.x = static_cast<const char *>(x);
+    a.x_pitch = ldx * es;
+    a.q = q;
+    a.ldq = ldq;
+    a.scale = scale;
+    a.positions = positions;
+    a.total = offsets + E;
+    a.k = k;
+    a.S = T * k;
+    const int vb = H == 0 ? 16 : rows::Width().add(x).add(a.x_pitch).add(H * es).bytes();
+    a.nvec = static_cast<int>(H * es / vb);
+    return rows::with_vec(type, vb,
+                          qz::Launch{a, false, true, static_cast<cudaStream_t>(stream)});
+}
+
+}  // extern "C"

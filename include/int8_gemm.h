@@ -1,0 +1,87 @@
+/*
+ * int8_gemm.h -- matrix products in 8-bit integers with a scale for each
+ * token and each channel, dense and by expert, on one GB300 (part of
+ * libsgemm_gb300.so; status codes as in sgemm.h).
+ *
+ * A linear layer served in 8 bits: the weights are quantised once, the
+ * activations on every call, one scale per row of either.
+ *
+ *   quantise   a_r = max_k |x_rk|,  scale_r = a_r / 127,
+ *              q_rk = round(x_rk * (127 / a_r))   (to nearest, ties to even)
+ *   product    C[m][n] = scaleA[m] * scaleB[n] * sum_k A[m][k] * B[n][k]
+ *
+ * Rows of activations and results have one of three types:
+ *   SGEMM_TYPE_BF16, SGEMM_TYPE_FP16 (as SGEMM_HALF_*), SGEMM_TYPE_FP32.
+ * All matrices are row-major with a leading dimension in elements; every
+ * pointer is a DEVICE pointer owned by the caller.  Calls enqueue on `stream`
+ * and return; nothing is allocated or synchronised.
+ *
+ * Arithmetic: the quantiser works in fp32 (IEEE division and product).  The
+ * product's sum is exact while the sum of |A||B| over k stays within 2^24
+ * (always for K <= 1024); beyond that it is accumulated in fp32 on the
+ * tensor cores, with at most a relative 2^-23 of the running sum lost per 16
+ * values of k.  The scales are applied in fp32 (token first) and the result
+ * is rounded once to its type.
+ *
+ * Errors: SGEMM_ERR_INVALID_ARG (dimensions, leading dimensions, type, NULL
+ * where data is read or written, pointers not aligned to their type) before
+ * anything is launched; SGEMM_ERR_UNSUPPORTED without a compute capability
+ * 10.3 GPU; SGEMM_ERR_LAUNCH if a launch fails; a bounded wait that runs out
+ * is reported by sgemm_poll_error.
+ */
+#ifndef INT8_GEMM_GB300_H
+#define INT8_GEMM_GB300_H
+
+#include <stddef.h>
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define SGEMM_TYPE_BF16 0
+#define SGEMM_TYPE_FP16 1
+#define SGEMM_TYPE_FP32 2
+
+/* What is quantised: the row itself, or the gated activation of a row that
+ * holds K gates and then K values: silu(X[r][k]) * X[r][K + k]. */
+#define SGEMM_ACT_NONE 0
+#define SGEMM_ACT_SWIGLU 1
+
+/* Quantises M rows of K values (2 K with SGEMM_ACT_SWIGLU) of X into
+ * Q (M x K, 8-bit) and scale (M).
+ * ldx >= K (2 K), ldq >= K; columns K .. ldq-1 of Q are not written.
+ *  - A row whose largest magnitude is below 2^-100 (zeros among them) gets
+ *    scale 0 and codes 0.
+ *  - A row that holds an infinity or NaN gets scale NaN and codes 0, so that
+ *    every result made from it is NaN.
+ * For the product's fast path give Q a 16-byte aligned base and a leading
+ * dimension that is a multiple of 16.  M == 0 or K == 0: scale = 0. */
+int sgemm_i8_quantize_rows(int type, int act, int M, int K, const void *X, int ldx,
+                           signed char *Q, int ldq, float *scale, void *stream);
+
+/* C (M x N, `type`) from A (M x K) and B (N x K), lda >= K, ldb >= K,
+ * ldc >= N, K <= 131071.  K == 0 writes zeros times the scales.  Operands whose rows start on
+ * 16-byte boundaries (base and leading dimension) run on the tensor cores;
+ * any other layout runs on the integer dot-product units, with exact 32-bit
+ * integer sums, several times slower for large M.  C may not overlap the
+ * inputs. */
+int sgemm_i8(int type, int M, int N, int K, const signed char *A, int lda, const float *scaleA,
+             const signed char *B, int ldb, const float *scaleB, void *C, int ldc, void *stream);
+
+/* The product of every expert: rows offsets[e] .. offsets[e+1]-1 of A (M rows
+ * in all, sorted by expert, as sgemm_experts_sort orders them) times expert
+ * e's weights B + e * strideB (N x K, ldb), scaled by scaleA[row] and
+ * scaleB[e * N + n], to the same rows of C.  offsets (E + 1 values, DEVICE)
+ * is read on the GPU: the host needs no counts.  Rows from offsets[E] on are
+ * neither read nor written.  1 <= E <= 1024; strideB >= (N-1) * ldb + K; the
+ * tensor cores need strideB a multiple of 16 as well. */
+int sgemm_i8_experts(int type, int M, int N, int K, int E, const int *offsets,
+                     const signed char *A, int lda, const float *scaleA, const signed char *B,
+                     int ldb, long long strideB, const float *scaleB, void *C, int ldc,
+                     void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* INT8_GEMM_GB300_H */
