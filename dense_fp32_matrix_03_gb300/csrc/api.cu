@@ -369,6 +369,19 @@ bool encode_operand16(CUtensorMap *map, const void *base, bool bf16, long long r
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
+bool encode_weights8(CUtensorMap *map, const signed char *base, long long rows, long long K,
+                     long long ld, int E, long long stride, int box_rows)
+{
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(E)};
+    cuuint64_t strides[2];
+    strides[0] = static_cast<cuuint64_t>(ld);
+    strides[1] = E > 1 ? static_cast<cuuint64_t>(stride) : strides[0] * dims[1];
+    cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), 1};
+    return encode3(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, dims, strides, box,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
 bool smem_attr_once(const void *kernel, int bytes)
 {
     int dev = 0;

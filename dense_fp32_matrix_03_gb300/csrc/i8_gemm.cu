@@ -1,8 +1,11 @@
 // i8_gemm.cu -- products of 8-bit integers with a scale for each token and
-// channel (include/int8_gemm.h): argument checks and the integer dot-product
-// kernel.
+// channel (include/int8_gemm.h): argument checks, the choice of the kernel
+// and the integer dot-product kernel (the tensor-core one is i8_tc.cuh).
+#include <cstring>
+
 #include "../../include/int8_gemm.h"
 #include "i8_gemm.h"
+#include "i8_tc.cuh"
 #include "rows.cuh"
 
 namespace sg {
@@ -102,11 +105,36 @@ int launch_dot(const Args &a, cudaStream_t st)
     return SGEMM_OK;
 }
 
-int run(int type, const Args &a, cudaStream_t st)
+// ------------------------------------------------- the kernel for a call
+
+// Whether the tensor-core kernel can read the operands: rows on 16-byte
+// boundaries.
+bool rows_on_16(const Args &a)
 {
-    if (type == SGEMM_TYPE_BF16) return launch_dot<__nv_bfloat16>(a, st);
-    if (type == SGEMM_TYPE_FP16) return launch_dot<__half>(a, st);
-    return launch_dot<float>(a, st);
+    return aligned16(a.A) && aligned16(a.B) && a.lda % 16 == 0 && a.ldb % 16 == 0 &&
+           (a.E == 1 || a.strideB % 16 == 0);
+}
+
+template <class T>
+int run(const Args &a, cudaStream_t st)
+{
+    alignas(64) CUtensorMap tmW;
+    std::memset(&tmW, 0, sizeof(tmW));
+    if (a.K == 0 || !rows_on_16(a) ||
+        !encode_weights8(&tmW, a.B, a.N, a.K, a.ldb, a.E, a.strideB, kCh))
+        return launch_dot<T>(a, st);
+    const bool c_vec = aligned16(a.C) && a.ldc * static_cast<long long>(sizeof(T)) % 16 == 0;
+    const int k_slots = (a.K + kSlotK - 1) / kSlotK;
+    if (a.M / a.E > 128) {
+        const long long tiles = max_tiles(a, Wide::NT) * ((a.N + 2 * kCh - 1) / (2 * kCh));
+        const int pairs = ss_slots(a.num_sms);
+        return launch_tc_i8<Wide, T>(a, tmW, tiles < pairs ? tiles : pairs, 1, c_vec, st);
+    }
+    const long long tiles = max_tiles(a, Narrow::NT) * ((a.N + kCh - 1) / kCh);
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= a.num_sms && k_slots >= 4 * split) split *= 2;
+    const long long clusters = split > 1 || tiles < a.num_sms ? tiles : a.num_sms;
+    return launch_tc_i8<Narrow, T>(a, tmW, clusters, split, c_vec, st);
 }
 
 // Checks and enqueues a product; offsets null: one dense group of M rows.
@@ -139,7 +167,10 @@ int product(int type, int M, int N, int K, int E, const int *offsets, const sign
     a.scaleB = scaleB;
     a.C = C;
     a.ldc = ldc;
-    return run(type, a, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (type == SGEMM_TYPE_BF16) return run<__nv_bfloat16>(a, st);
+    if (type == SGEMM_TYPE_FP16) return run<__half>(a, st);
+    return run<float>(a, st);
 }
 
 }  // namespace i8

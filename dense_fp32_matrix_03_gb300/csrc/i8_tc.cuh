@@ -1,0 +1,636 @@
+// i8_tc.cuh -- products of 8-bit integers with a scale for each token and
+// channel on the tensor cores:
+//   C[m][n] = scaleA[m] * scaleB[n] * sum_k A[m][k] * B[n][k].
+//
+// Arithmetic.  An 8-bit integer is exact in fp16 and the product of two has
+// magnitude at most 2^14, so kind::f16 with fp32 accumulation gives the exact
+// integer sum while the sum of magnitudes stays within 2^24.  On this GPU the
+// 8-bit integer rate of the tensor cores is far below the 16-bit one, so the
+// integers are widened in the kernel: HBM and L2 carry one byte a value, the
+// tensor cores run at their 16-bit rate.  Widening four bytes takes five
+// instructions: x ^ 0x80 is x + 128 as an unsigned byte u, two byte permutes
+// put 0x64 above each u (the fp16 value 1024 + u), and two packed
+// subtractions of 1152 leave x.
+//
+// Roles of the operands.  The weights are the MMA's M side (128 channels per
+// CTA, always full) and the tokens its N side (16 to 256, in steps of 16 or
+// 32), so that few tokens, or an expert's short last tile, cost MMAs of their
+// own size.  Widened weights go to tensor memory (a thread holds a row, as
+// tensor memory wants it) and never to shared memory, whose bandwidth the
+// widened tokens need: per CTA and 128 k at 256 tokens, in units of 128 bytes
+// a clock, 128 (weights in) + 128 (weights read) + 128 (tokens in) + 256
+// (tokens widened) + 256 (MMA reads) of the MMA's 1024 clocks.
+//
+// Data flow, per step of 128 k (a "slot"):
+//   producer   weights, 128 rows of 128 bytes, by TMA into a ring (128-byte
+//              swizzle)
+//   A warps    a row per thread: 8 x 16 bytes -> 64 columns of packed fp16 in
+//              tensor memory (one of four slots)
+//   B warps    16 bytes of a token per thread and load, from global memory one
+//              slot ahead -> 32 bytes of fp16 in shared memory (one of four
+//              slots)
+//   MMA        one thread: 8 MMAs of k = 16
+//   epilogue   tensor memory -> scales -> result type -> staging -> C
+// The order of k inside a slot is permuted (the first eight values of every
+// 16-byte piece, then the second eight), the same way for both operands: a
+// token's 16-byte piece then becomes one 16-byte piece of each of the slot's
+// two 64-k boxes, and the stores of eight neighbouring threads fall on eight
+// different bank groups.
+//
+// Two configurations.
+//   narrow  one CTA, 128 channels x up to 128 tokens, two accumulators.  For
+//           few tokens the weights are what is read, and a cluster of up to
+//           8 CTAs may share a tile, each a part of k: the partial sums meet
+//           in distributed shared memory, in CTA order, without a workspace
+//           or a second launch.
+//   wide    a CTA pair (cta_group::2), 256 channels x up to 256 tokens, each
+//           CTA widening its 128 channels and half the tokens.
+// Every wait is bounded.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "../../include/sgemm.h"
+#include "i8_gemm.h"
+#include "rows.cuh"
+#include "tc_pair.cuh"
+
+namespace sg {
+namespace i8 {
+
+using tc::Ring;
+using tcp::arrive_on;
+using tcp::cta_rank;
+using tcp::drain_cl;
+using tcp::wait_cl;
+using tcp::warp_wait_cl;
+
+constexpr int kCh = 128;     // channels per CTA
+constexpr int kSlotK = 128;  // k per slot
+constexpr int kSlots = 4;    // widened slots: 64 tensor-memory columns each
+constexpr int kWStage = kCh * kSlotK;
+constexpr int kAWarp0 = 4, kEWarp0 = 8, kBWarps = 4;
+constexpr uint32_t kACols = 256;  // first column of the weights' slots
+constexpr uint32_t kSlotCols = kSlotK / 2;
+
+template <int CG_, int NT_, int RING_, int EWARPS_>
+struct Cfg {
+    static constexpr int CG = CG_, NT = NT_, RING = RING_, EWARPS = EWARPS_;
+    static constexpr int NTC = NT / CG;              // tokens per CTA's half
+    static constexpr int BBOX = NTC * 128;           // 64 k of them, widened
+    static constexpr int BSLOT = 2 * BBOX;
+    static constexpr int ACCS = NT <= 128 ? 2 : 1;
+    static constexpr int ECOLS = NT / (EWARPS / 4);  // tokens per epilogue warp
+    static constexpr int BWARP0 = kEWarp0 + EWARPS;
+    static constexpr int THREADS = (BWARP0 + kBWarps) * 32;
+    static constexpr int STAGING = 32 * 32 * 4;      // per epilogue warp
+    static constexpr int NBAR = 2 * RING + 2 * kSlots + 2 * ACCS + 1;
+    static constexpr int OFF_B = RING * kWStage;
+    static constexpr int OFF_STAGE = OFF_B + kSlots * BSLOT;
+    static constexpr int OFF_SCALE = OFF_STAGE + EWARPS * STAGING;
+    static constexpr int OFF_BAR = OFF_SCALE + EWARPS * ECOLS * 4;
+    static constexpr int OFF_TABLE = OFF_BAR + NBAR * 8 + 16;
+    static constexpr int SMEM = OFF_TABLE + (kMaxExperts + 1) * 4 + 1024;
+    static_assert(NTC == 128, "eight token groups of 16 per converter thread");
+    static_assert(ACCS * NT <= static_cast<int>(kACols), "accumulator columns");
+    static_assert(NT * kCh * 4 <= kSlots * BSLOT || CG == 2, "partial sums fit the token slots");
+    static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+};
+using Narrow = Cfg<1, 128, 4, 4>;
+using Wide = Cfg<2, 256, 3, 8>;
+
+// Four bytes (8-bit integers) as four fp16 values.
+__device__ __forceinline__ void widen4(uint32_t x, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t u = x ^ 0x80808080u;
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140);
+    uint32_t b = __byte_perm(u, 0x64646464u, 0x4342);
+    __half2 ha = __hsub2(*reinterpret_cast<__half2 *>(&a), bias);
+    __half2 hb = __hsub2(*reinterpret_cast<__half2 *>(&b), bias);
+    lo = *reinterpret_cast<uint32_t *>(&ha);
+    hi = *reinterpret_cast<uint32_t *>(&hb);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z),
+                 "r"(w)
+                 : "memory");
+}
+// 16 consecutive columns of this warp's 32 tensor-memory lanes.
+__device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15])
+        : "memory");
+}
+// D (+)= A[tensor memory] * B[shared memory]^T, kind::f16.
+template <int CG>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc)
+{
+    if constexpr (CG == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t *bar)
+{
+    if constexpr (CG == 2)
+        tcp::umma_commit_both(bar);
+    else
+        tc::umma_commit(bar);
+}
+// An arrive on the issuing CTA's barrier.
+template <int CG>
+__device__ __forceinline__ void arrive_issuer(uint64_t *bar)
+{
+    if constexpr (CG == 2)
+        arrive_on(bar, 0);
+    else
+        mbar_arrive(bar);
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr, uint32_t rank)
+{
+    uint32_t a;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
+// One output tile: tokens row0 .. row0 + n - 1 of expert e, channels from
+// ch0 on (this CTA's 128); neff: the MMA's N.
+struct Job {
+    int e, n, neff, ch0;
+    long long row0;
+};
+
+// Tile u of the table (first tile of each expert): within an expert, token
+// tiles run fastest, so that CTAs at work together share weights in L2.
+template <class C>
+__device__ __forceinline__ Job job(const Args &a, const int *table, int u, uint32_t half)
+{
+    int lo = 0, hi = a.E;  // largest e with table[e] <= u
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (table[mid] <= u)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    int r0, r1;
+    expert_rows(a, lo, r0, r1);
+    const int mt = (r1 - r0 + C::NT - 1) / C::NT;
+    const int v = u - table[lo];
+    const int ct = v / mt, m = v - ct * mt;
+    Job j;
+    j.e = lo;
+    j.row0 = r0 + static_cast<long long>(m) * C::NT;
+    j.n = min(C::NT, static_cast<int>(r1 - j.row0));
+    constexpr int STEP = 16 * C::CG;
+    j.neff = (j.n + STEP - 1) / STEP * STEP;
+    j.ch0 = (ct * C::CG + static_cast<int>(half)) * kCh;
+    return j;
+}
+
+// tmW: the weights (K, N, E) in boxes of 128 k by 128 channels, 128-byte
+// swizzle.  split: CTAs of the cluster that share a tile's k (narrow only);
+// then each cluster has one tile.  c_vec: C's rows allow 16-byte accesses.
+template <class C, class T>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    i8_kernel(const __grid_constant__ CUtensorMap tmW, const Args a, int split, int c_vec)
+{
+    constexpr int CG = C::CG;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(base + C::OFF_BAR);
+    uint64_t *w_full = bars, *w_empty = w_full + C::RING;
+    uint64_t *ready = w_empty + C::RING;         // issuing CTA's: widened slots
+    uint64_t *slot_empty = ready + kSlots;       // per CTA: commits
+    uint64_t *acc_full = slot_empty + kSlots;    // per CTA: commits
+    uint64_t *acc_empty = acc_full + C::ACCS;    // issuing CTA's: epilogues
+    uint64_t *mma_done = acc_empty + C::ACCS;
+    uint32_t *tmem_base = reinterpret_cast<uint32_t *>(mma_done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_base + 1);
+    int *table = reinterpret_cast<int *>(base + C::OFF_TABLE);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cta_rank();
+    const uint32_t half = CG == 2 ? rank : 0u, krank = CG == 2 ? 0u : rank;
+    const int cluster = CG == 2 ? 2 : split;
+    const int cid = static_cast<int>(blockIdx.x) / cluster;
+    const int ncl = static_cast<int>(gridDim.x) / cluster;
+    const bool issuer = CG == 1 || rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::RING; ++s) {
+            mbar_init(&w_full[s], 1u);
+            mbar_init(&w_empty[s], 4u);
+        }
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(&ready[s], static_cast<uint32_t>(CG * (4 + kBWarps)));
+            mbar_init(&slot_empty[s], 1u);
+        }
+        for (int s = 0; s < C::ACCS; ++s) {
+            mbar_init(&acc_full[s], 1u);
+            mbar_init(&acc_empty[s], static_cast<uint32_t>(CG * C::EWARPS));
+        }
+        mbar_init(mma_done, 1u);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmW);
+    }
+    if (warp == 1) {
+        if constexpr (CG == 2)
+            tcp::tmem_alloc_pair(tmem_base, 512);
+        else
+            tc::tmem_alloc(tmem_base, 512);
+    }
+    if (warp == 2) {  // the tile table
+        const int cts = (a.N + kCh * CG - 1) / (kCh * CG);
+        int sum = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            int lo = 0, hi = 0;
+            if (e0 + lane < a.E) expert_rows(a, e0 + lane, lo, hi);
+            const int n = (hi - lo + C::NT - 1) / C::NT * cts;
+            int inc = n;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int x = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += x;
+            }
+            if (e0 + lane < a.E) table[e0 + lane] = sum + inc - n;
+            sum += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) table[a.E] = sum;
+    }
+    tc::tc_fence_before();
+    tcp::cluster_sync();
+    tc::tc_fence_after();
+    const uint32_t tmem = *tmem_base;
+    const Abort ab{abort_flag, a.status, kWaitLimitCycles};
+    const int tiles = table[a.E];
+    const int k_slots = (a.K + kSlotK - 1) / kSlotK;
+    const int ks_lo = static_cast<int>(static_cast<long long>(k_slots) * krank / split);
+    const int ks_hi = static_cast<int>(static_cast<long long>(k_slots) * (krank + 1) / split);
+    float *part = reinterpret_cast<float *>(base + C::OFF_B);  // split: [token][channel]
+
+    if (warp == 0) {
+        // ---------------------------------------------------- weights' producer
+        if (lane == 0) {
+            Ring<C::RING> rr;
+            long long issued = 0;
+            bool ok = true;
+            for (int u = cid; ok && u < tiles; u += ncl) {
+                const Job j = job<C>(a, table, u, half);
+                for (int ks = ks_lo; ks < ks_hi; ++ks) {
+                    if (!mbar_wait(&w_empty[rr.s], rr.ph ^ 1u, ab, kStatusWaitEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&w_full[rr.s], kWStage);
+                    tma_load_3d(base + rr.s * kWStage, &tmW, &w_full[rr.s], ks * kSlotK, j.ch0,
+                                j.e);
+                    ++issued;
+                    rr.next();
+                }
+            }
+            if (!ok || *abort_flag) {  // let loads in flight land before the CTA exits
+                Ring<C::RING> d;
+                for (long long i = 0; i < issued; ++i) {
+                    if (i + C::RING >= issued) mbar_drain(&w_full[d.s], d.ph, ab.limit);
+                    d.next();
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------- MMA issuer
+        if (issuer && lane == 0) {
+            Ring<kSlots> sr;
+            Ring<C::ACCS> acc;
+            bool ok = true, any = false;
+            const uint64_t bdesc = tc::kmajor_sw128_desc(smem_u32(base + C::OFF_B));
+            for (int u = cid; ok && u < tiles; u += ncl) {
+                const Job j = job<C>(a, table, u, half);
+                const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(j.neff >> 3) << 17) |
+                                       (static_cast<uint32_t>((kCh * CG) >> 4) << 24);
+                if (!wait_cl(&acc_empty[acc.s], acc.ph ^ 1u, ab, kStatusWaitAcc)) break;
+                tc::tc_fence_after();
+                const uint32_t d = tmem + static_cast<uint32_t>(acc.s * C::NT);
+                for (int ks = ks_lo; ks < ks_hi; ++ks) {
+                    if (!wait_cl(&ready[sr.s], sr.ph, ab, kStatusWaitConv)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::tc_fence_after();
+                    const uint32_t at = tmem + kACols + static_cast<uint32_t>(sr.s) * kSlotCols;
+                    const uint64_t bt = bdesc + static_cast<uint64_t>(sr.s * (C::BSLOT >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_ts<CG>(d, at + 8 * kk,
+                                   bt + static_cast<uint64_t>((kk >> 2) * (C::BBOX >> 4) +
+                                                              2 * (kk & 3)),
+                                   idesc, ks > ks_lo || kk > 0 ? 1u : 0u);
+                    any = true;
+                    commit<CG>(&slot_empty[sr.s]);
+                    sr.next();
+                }
+                if (!ok) break;
+                commit<CG>(&acc_full[acc.s]);
+                acc.next();
+            }
+            if (any) {
+                commit<CG>(mma_done);
+                drain_cl(mma_done, 0, ab.limit);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= kAWarp0 && warp < kAWarp0 + 4) {
+        // ---------------------------------------------------- weights: widen into tensor memory
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t tl = tmem + kACols + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        Ring<C::RING> rr;
+        Ring<kSlots> sr;
+        bool ok = true;
+        for (int u = cid; ok && u < tiles; u += ncl) {
+            for (int ks = ks_lo; ks < ks_hi; ++ks) {
+                if (!warp_wait(&w_full[rr.s], rr.ph, ab, kStatusWaitFull, lane) ||
+                    !warp_wait_cl(&slot_empty[sr.s], sr.ph ^ 1u, ab, kStatusWaitMma)) {
+                    ok = false;
+                    break;
+                }
+                tc::tc_fence_after();
+                const uint32_t src = smem_u32(base + rr.s * kWStage) + row * 128;
+                const uint32_t dst = tl + static_cast<uint32_t>(sr.s) * kSlotCols;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t x[16], y[16];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint4 v = lds128(src + (((4 * h + c) ^ (row & 7)) << 4));
+                        widen4(v.x, x[4 * c], x[4 * c + 1]);
+                        widen4(v.y, x[4 * c + 2], x[4 * c + 3]);
+                        widen4(v.z, y[4 * c], y[4 * c + 1]);
+                        widen4(v.w, y[4 * c + 2], y[4 * c + 3]);
+                    }
+                    tmem_put16(dst + 16 * h, x);
+                    tmem_put16(dst + 32 + 16 * h, y);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&w_empty[rr.s]);
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_issuer<CG>(&ready[sr.s]);
+                rr.next();
+                sr.next();
+            }
+        }
+    } else if (warp >= C::BWARP0) {
+        // ---------------------------------------------------- tokens: widen into shared memory
+        const int t = static_cast<int>(threadIdx.x) - C::BWARP0 * 32;
+        const int c = t & 7, r16 = t >> 3;
+        const uint32_t off = static_cast<uint32_t>(r16 * 128 + ((c ^ (r16 & 7)) << 4));
+        Ring<kSlots> sr;
+        bool ok = true;
+        for (int u = cid; ok && u < tiles; u += ncl) {
+            const Job j = job<C>(a, table, u, half);
+            const int per = j.neff / CG, groups = per >> 4;  // this CTA's tokens, 16 at a time
+            const int first = static_cast<int>(half) * per + r16;
+            const signed char *src = a.A + (j.row0 + first) * a.lda + 16 * c;
+            auto load = [&](int g, int ks) -> uint4 {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                const int k = ks * kSlotK + 16 * c;
+                if (first + 16 * g < j.n && k < a.K) {
+                    const signed char *p = src + 16LL * g * a.lda + ks * kSlotK;
+                    if (k + 16 <= a.K) {
+                        v = *reinterpret_cast<const uint4 *>(p);
+                    } else {  // the row's last bytes: nothing past K is read
+                        uint32_t w[4] = {0u, 0u, 0u, 0u};
+                        for (int i = 0; i < a.K - k; ++i) {
+                            const uint32_t b = (static_cast<uint32_t>(p[i]) & 255u) << (8 * (i & 3));
+                            if (i < 4)
+                                w[0] |= b;
+                            else if (i < 8)
+                                w[1] |= b;
+                            else if (i < 12)
+                                w[2] |= b;
+                            else
+                                w[3] |= b;
+                        }
+                        v = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                return v;
+            };
+            uint4 r[8];
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+                if (g < groups) r[g] = load(g, ks_lo);
+            for (int ks = ks_lo; ks < ks_hi; ++ks) {
+                if (!warp_wait_cl(&slot_empty[sr.s], sr.ph ^ 1u, ab, kStatusWaitMma)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = smem_u32(base + C::OFF_B + sr.s * C::BSLOT) + off;
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    if (g >= groups) break;
+                    uint32_t w[8];
+                    widen4(r[g].x, w[0], w[1]);
+                    widen4(r[g].y, w[2], w[3]);
+                    widen4(r[g].z, w[4], w[5]);
+                    widen4(r[g].w, w[6], w[7]);
+                    sts128(dst + g * 2048, w[0], w[1], w[2], w[3]);
+                    sts128(dst + g * 2048 + C::BBOX, w[4], w[5], w[6], w[7]);
+                    if (ks + 1 < ks_hi) r[g] = load(g, ks + 1);
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_issuer<CG>(&ready[sr.s]);
+                sr.next();
+            }
+        }
+    } else if (warp >= kEWarp0) {
+        // ---------------------------------------------------- epilogue
+        const int q = warp & 3, w = warp - kEWarp0;
+        const int col0 = (w >> 2) * C::ECOLS;  // this warp's first token of the tile
+        T *stage = reinterpret_cast<T *>(base + C::OFF_STAGE + w * C::STAGING);
+        float *sa = reinterpret_cast<float *>(base + C::OFF_SCALE) + w * C::ECOLS;
+        constexpr int VPR = 2 * static_cast<int>(sizeof(T));  // 16-byte pieces of 32 values
+        Ring<C::ACCS> acc;
+        for (int u = cid; u < tiles; u += ncl) {
+            const Job j = job<C>(a, table, u, half);
+            const int ch = j.ch0 + q * 32 + lane;
+            float sb = 0.f;
+            if (split == 1) {
+                for (int i = lane; i < C::ECOLS; i += 32)
+                    sa[i] = col0 + i < j.n ? a.scaleA[j.row0 + col0 + i] : 0.f;
+                if (ch < a.N) sb = a.scaleB[static_cast<long long>(j.e) * a.N + ch];
+                __syncwarp();
+            }
+            int got = 1;
+            if (lane == 0) got = wait_cl(&acc_full[acc.s], acc.ph, ab, kStatusWaitAcc, true);
+            if (!__shfl_sync(0xffffffffu, got, 0)) break;
+            drain_cl(&acc_full[acc.s], acc.ph, ab.limit);
+            tc::tc_fence_after();
+            const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) +
+                                static_cast<uint32_t>(acc.s * C::NT + col0);
+            const int n = min(j.n - col0, C::ECOLS);
+            const bool vec = c_vec != 0 && j.ch0 + q * 32 + 32 <= a.N;
+#pragma unroll 1
+            for (int c0 = 0; c0 < n; c0 += 32) {
+                float v[32];
+                tc::tmem_ld32(tb + c0, v);
+                if (split > 1) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        part[(col0 + c0 + i) * kCh + q * 32 + lane] = v[i];
+                    continue;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 s = *reinterpret_cast<const float4 *>(sa + c0 + i);
+                    v[i] = v[i] * s.x * sb;
+                    v[i + 1] = v[i + 1] * s.y * sb;
+                    v[i + 2] = v[i + 2] * s.z * sb;
+                    v[i + 3] = v[i + 3] * s.w * sb;
+                }
+                T *crow = static_cast<T *>(a.C) + (j.row0 + col0 + c0) * a.ldc;
+                if (vec) {
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) stage[i * 32 + lane] = rows::from_f<T>(v[i]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < VPR; ++i) {
+                        const int x = i * 32 + lane, r = x / VPR, p = x % VPR;
+                        if (c0 + r < n)
+                            *reinterpret_cast<uint4 *>(crow + r * a.ldc + j.ch0 + q * 32 +
+                                                       p * (16 / sizeof(T))) =
+                                reinterpret_cast<const uint4 *>(stage)[x];
+                    }
+                } else if (ch < a.N) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (c0 + i < n) crow[i * a.ldc + ch] = rows::from_f<T>(v[i]);
+                }
+            }
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_issuer<CG>(&acc_empty[acc.s]);
+            acc.next();
+        }
+    }
+
+    if (CG == 1 && split > 1) {
+        // ---- partial sums of the cluster's CTAs, added in CTA order; CTA r
+        // takes tokens r, r + split, ...: a warp a token, four channels a lane
+        __syncwarp();
+        tcp::cluster_sync();
+        if (cid < tiles && *abort_flag == 0) {
+            const Job j = job<C>(a, table, cid, 0);
+            const int ch = j.ch0 + 4 * lane;
+            float sb[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sb[i] = ch + i < a.N ? a.scaleB[static_cast<long long>(j.e) * a.N + ch + i] : 0.f;
+            for (int t = static_cast<int>(krank) + warp * split; t < j.n;
+                 t += split * (C::THREADS / 32)) {
+                const uint32_t at = smem_u32(part + t * kCh + 4 * lane);
+                float4 s = cluster_load4(at, 0);
+                for (int r = 1; r < split; ++r) {
+                    const float4 x = cluster_load4(at, static_cast<uint32_t>(r));
+                    s.x += x.x;
+                    s.y += x.y;
+                    s.z += x.z;
+                    s.w += x.w;
+                }
+                const float sc = a.scaleA[j.row0 + t];
+                const float o[4] = {s.x * sc * sb[0], s.y * sc * sb[1], s.z * sc * sb[2],
+                                    s.w * sc * sb[3]};
+                T *cp = static_cast<T *>(a.C) + (j.row0 + t) * a.ldc + ch;
+                if (c_vec != 0 && ch + 4 <= a.N) {
+                    rows::Vec<T, 4 * static_cast<int>(sizeof(T))> x;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x.set(i, o[i]);
+                    x.store(cp);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (ch + i < a.N) cp[i] = rows::from_f<T>(o[i]);
+                }
+            }
+        }
+    }
+
+    // ---- teardown: no CTA leaves while another may touch its shared memory
+    tc::tc_fence_before();
+    __syncwarp();
+    tcp::cluster_sync();
+    if (warp == 1) {
+        tc::tc_fence_after();
+        if constexpr (CG == 2)
+            tcp::tmem_dealloc_pair(tmem, 512);
+        else
+            tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Enqueues the kernel on `clusters` clusters of CG (or split) CTAs.
+template <class C, class T>
+int launch_tc_i8(const Args &a, const CUtensorMap &tmW, long long clusters, int split, bool c_vec,
+                 cudaStream_t st)
+{
+    auto kern = i8_kernel<C, T>;
+    if (!smem_attr_once(reinterpret_cast<const void *>(kern), C::SMEM)) return SGEMM_ERR_LAUNCH;
+    const unsigned size = C::CG == 2 ? 2u : static_cast<unsigned>(split);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters) * size);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, tmW, a, split, c_vec ? 1 : 0) != cudaSuccess) {
+        cudaGetLastError();
+        return SGEMM_ERR_LAUNCH;
+    }
+    note_launch();
+    return SGEMM_OK;
+}
+
+}  // namespace i8
+}  // namespace sg

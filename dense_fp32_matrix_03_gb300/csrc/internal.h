@@ -209,6 +209,10 @@ bool encode_c_tiles(CUtensorMap *map, const float *C, long long M, long long N, 
 // box_rows rows with the 128-byte swizzle.
 bool encode_operand16(CUtensorMap *map, const void *base, bool bf16, long long rows, long long K,
                       long long ld, int Q, long long stride, int box_rows);
+// Tensor map of E matrices of 8-bit values stored rows x K (K-inner, `stride`
+// values apart): boxes of 128 k by box_rows rows with the 128-byte swizzle.
+bool encode_weights8(CUtensorMap *map, const signed char *base, long long rows, long long K,
+                     long long ld, int E, long long stride, int box_rows);
 // Copies Q matrices of 16-bit values into dst as rows x cols K-inner
 // matrices (row pitch ldd, batch stride dstride): dst[r][c] = src[c][r] when
 // trans (src stored cols x rows), else src[r][c] (src row pitch lds).
