@@ -369,7 +369,7 @@ bool encode_operand16(CUtensorMap *map, const void *base, bool bf16, long long r
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-bool encode_weights8(CUtensorMap *map, const signed char *base, long long rows, long long K,
+bool encode_operand8(CUtensorMap *map, const signed char *base, long long rows, long long K,
                      long long ld, int E, long long stride, int box_rows)
 {
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows),

@@ -119,22 +119,25 @@ template <class T>
 int run(const Args &a, cudaStream_t st)
 {
     alignas(64) CUtensorMap tmW;
+    alignas(64) CUtensorMap tmT;
     std::memset(&tmW, 0, sizeof(tmW));
+    std::memset(&tmT, 0, sizeof(tmT));
     if (a.K == 0 || !rows_on_16(a) ||
-        !encode_weights8(&tmW, a.B, a.N, a.K, a.ldb, a.E, a.strideB, kCh))
+        !encode_operand8(&tmW, a.B, a.N, a.K, a.ldb, a.E, a.strideB, kCh) ||
+        !encode_operand8(&tmT, a.A, a.M, a.K, a.lda, 1, 0, kBoxRows))
         return launch_dot<T>(a, st);
     const bool c_vec = aligned16(a.C) && a.ldc * static_cast<long long>(sizeof(T)) % 16 == 0;
     const int k_slots = (a.K + kSlotK - 1) / kSlotK;
     if (a.M / a.E > 128) {
         const long long tiles = max_tiles(a, Wide::NT) * ((a.N + 2 * kCh - 1) / (2 * kCh));
         const int pairs = ss_slots(a.num_sms);
-        return launch_tc_i8<Wide, T>(a, tmW, tiles < pairs ? tiles : pairs, 1, c_vec, st);
+        return launch_tc_i8<Wide, T>(a, tmW, tmT, tiles < pairs ? tiles : pairs, 1, c_vec, st);
     }
     const long long tiles = max_tiles(a, Narrow::NT) * ((a.N + kCh - 1) / kCh);
     int split = 1;
     while (split < 8 && tiles * split * 2 <= a.num_sms && k_slots >= 4 * split) split *= 2;
     const long long clusters = split > 1 || tiles < a.num_sms ? tiles : a.num_sms;
-    return launch_tc_i8<Narrow, T>(a, tmW, clusters, split, c_vec, st);
+    return launch_tc_i8<Narrow, T>(a, tmW, tmT, clusters, split, c_vec, st);
 }
 
 // Checks and enqueues a product; offsets null: one dense group of M rows.

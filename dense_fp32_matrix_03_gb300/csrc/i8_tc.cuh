@@ -22,20 +22,23 @@
 // (tokens widened) + 256 (MMA reads) of the MMA's 1024 clocks.
 //
 // Data flow, per step of 128 k (a "slot"):
-//   producer   weights, 128 rows of 128 bytes, by TMA into a ring (128-byte
-//              swizzle)
+//   producers  weights, 128 rows of 128 bytes, and tokens, in boxes of 32
+//              rows, by TMA into a ring each (128-byte swizzle)
 //   A warps    a row per thread: 8 x 16 bytes -> 64 columns of packed fp16 in
-//              tensor memory (one of four slots)
-//   B warps    16 bytes of a token per thread and load, from global memory one
-//              slot ahead -> 32 bytes of fp16 in shared memory (one of four
-//              slots)
+//              tensor memory
+//   B warps    16 bytes at a time -> 32 bytes of fp16 in shared memory
 //   MMA        one thread: 8 MMAs of k = 16
 //   epilogue   tensor memory -> scales -> result type -> staging -> C
+// A and B warps come in two sets that take alternate slots: a slot's chain of
+// waits, loads, stores and fences is about 1100 clocks long (with one set the
+// weights of a decoding step came at 4.0 TB/s and a 256 x 256 tile's slot took
+// 2490 clocks).
 // The order of k inside a slot is permuted (the first eight values of every
 // 16-byte piece, then the second eight), the same way for both operands: a
 // token's 16-byte piece then becomes one 16-byte piece of each of the slot's
-// two 64-k boxes, and the stores of eight neighbouring threads fall on eight
-// different bank groups.
+// two 64-k boxes, at the byte offset it had itself: rows of 128 bytes and
+// their swizzle are the same before and after, so widening is a walk over
+// offsets, free of bank conflicts.
 //
 // Two configurations.
 //   narrow  one CTA, 128 channels x up to 128 tokens, two accumulators.  For
@@ -67,37 +70,66 @@ using tcp::warp_wait_cl;
 
 constexpr int kCh = 128;     // channels per CTA
 constexpr int kSlotK = 128;  // k per slot
-constexpr int kSlots = 4;    // widened slots: 64 tensor-memory columns each
 constexpr int kWStage = kCh * kSlotK;
-constexpr int kAWarp0 = 4, kEWarp0 = 8, kBWarps = 4;
+constexpr int kBoxRows = 32;                      // tokens per TMA box
+constexpr int kSets = 2;                          // of A and of B warps
+constexpr int kAWarp0 = 4, kBWarp0 = kAWarp0 + 4 * kSets, kEWarp0 = kBWarp0 + 4 * kSets;
 constexpr uint32_t kACols = 256;  // first column of the weights' slots
 constexpr uint32_t kSlotCols = kSlotK / 2;
 
-template <int CG_, int NT_, int RING_, int EWARPS_>
+// SLOTS: widened slots; WRING / TRING: stages of weights / tokens as bytes.
+template <int CG_, int NT_, int SLOTS_, int WRING_, int TRING_, int EWARPS_>
 struct Cfg {
-    static constexpr int CG = CG_, NT = NT_, RING = RING_, EWARPS = EWARPS_;
+    static constexpr int CG = CG_, NT = NT_, SLOTS = SLOTS_, WRING = WRING_, TRING = TRING_,
+                         EWARPS = EWARPS_;
     static constexpr int NTC = NT / CG;              // tokens per CTA's half
+    static constexpr int TSTAGE = NTC * kSlotK;
     static constexpr int BBOX = NTC * 128;           // 64 k of them, widened
     static constexpr int BSLOT = 2 * BBOX;
     static constexpr int ACCS = NT <= 128 ? 2 : 1;
     static constexpr int ECOLS = NT / (EWARPS / 4);  // tokens per epilogue warp
-    static constexpr int BWARP0 = kEWarp0 + EWARPS;
-    static constexpr int THREADS = (BWARP0 + kBWarps) * 32;
-    static constexpr int STAGING = 32 * 32 * 4;      // per epilogue warp
-    static constexpr int NBAR = 2 * RING + 2 * kSlots + 2 * ACCS + 1;
-    static constexpr int OFF_B = RING * kWStage;
-    static constexpr int OFF_STAGE = OFF_B + kSlots * BSLOT;
+    static constexpr int THREADS = (kEWarp0 + EWARPS) * 32;
+    // One accumulator: the epilogue holds the whole tile, packed to 16 bits,
+    // in registers, so that the next tile's MMAs wait for reads of tensor
+    // memory only, not for stores.  Registers move from the other roles to the
+    // epilogue (kReg*, within the 72 per thread of the launch).
+    static constexpr bool HOLD = ACCS == 1;
+    static constexpr int STAGING = 32 * 32 * 2;      // per epilogue warp, 16-bit results
+    static constexpr int NBAR = 2 * WRING + 2 * TRING + 2 * SLOTS + 2 * ACCS + 1;
+    static constexpr int OFF_T = WRING * kWStage;
+    static constexpr int OFF_B = OFF_T + TRING * TSTAGE;
+    static constexpr int OFF_STAGE = OFF_B + SLOTS * BSLOT;
     static constexpr int OFF_SCALE = OFF_STAGE + EWARPS * STAGING;
     static constexpr int OFF_BAR = OFF_SCALE + EWARPS * ECOLS * 4;
     static constexpr int OFF_TABLE = OFF_BAR + NBAR * 8 + 16;
     static constexpr int SMEM = OFF_TABLE + (kMaxExperts + 1) * 4 + 1024;
     static_assert(NTC == 128, "eight token groups of 16 per converter thread");
     static_assert(ACCS * NT <= static_cast<int>(kACols), "accumulator columns");
-    static_assert(NT * kCh * 4 <= kSlots * BSLOT || CG == 2, "partial sums fit the token slots");
+    static_assert(SLOTS * kSlotCols + kACols <= 512, "tensor-memory columns");
+    static_assert(NT * kCh * 4 <= SLOTS * BSLOT || CG == 2, "partial sums fit the token slots");
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
-using Narrow = Cfg<1, 128, 4, 4>;
-using Wide = Cfg<2, 256, 3, 8>;
+#ifndef I8_WIDE
+#define I8_WIDE 2, 256, 3, 3, 3, 8
+#endif
+#ifndef I8_NARROW
+#define I8_NARROW 1, 128, 3, 4, 2, 4
+#endif
+using Narrow = Cfg<I8_NARROW>;
+using Wide = Cfg<I8_WIDE>;
+
+// Registers per thread after a warpgroup's give or take (HOLD, below).
+constexpr int kRegMisc = 56, kRegConv = 56, kRegEpi = 112;
+template <int N>
+__device__ __forceinline__ void give_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void take_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // Four bytes (8-bit integers) as four fp16 values.
 __device__ __forceinline__ void widen4(uint32_t x, uint32_t &lo, uint32_t &hi)
@@ -135,6 +167,48 @@ __device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t (&v)[1
         "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
         "r"(v[15])
         : "memory");
+}
+// Rows 0-15 (lane field of taddr) of 32 columns in the layout of an 8 x 8
+// matrix's registers: v[4 * i + 2 * b + c] is row 8 b + lane / 4, column
+// 8 i + 2 (lane % 4) + c.  Completion: tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+          "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld()
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    if constexpr (sizeof(T) == 4) {
+        return 0u;  // fp32 results are never packed
+    } else {
+        union {
+            T h[2];
+            uint32_t u;
+        } x;
+        x.h[0] = rows::from_f<T>(lo);
+        x.h[1] = rows::from_f<T>(hi);
+        return x.u;
+    }
+}
+// Four 8 x 8 matrices of 16-bit values, each transposed into rows of 16
+// bytes: lane l gives the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void store_transposed(uint32_t addr, const uint32_t (&m)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                     addr),
+                 "r"(m[0]), "r"(m[1]), "r"(m[2]), "r"(m[3])
+                 : "memory");
 }
 // D (+)= A[tensor memory] * B[shared memory]^T, kind::f16.
 template <int CG>
@@ -183,6 +257,18 @@ __device__ __forceinline__ float4 cluster_load4(uint32_t addr, uint32_t rank)
     return v;
 }
 
+// Waits (bounded) for the last loads of a ring that stops early, so that none
+// is in flight when the CTA exits.
+template <int STAGES>
+__device__ __forceinline__ void drain_ring(uint64_t *full, long long issued, const Abort &ab)
+{
+    Ring<STAGES> d;
+    for (long long i = 0; i < issued; ++i) {
+        if (i + STAGES >= issued) mbar_drain(&full[d.s], d.ph, ab.limit);
+        d.next();
+    }
+}
+
 // One output tile: tokens row0 .. row0 + n - 1 of expert e, channels from
 // ch0 on (this CTA's 128); neff: the MMA's N.
 struct Job {
@@ -218,22 +304,26 @@ __device__ __forceinline__ Job job(const Args &a, const int *table, int u, uint3
     return j;
 }
 
-// tmW: the weights (K, N, E) in boxes of 128 k by 128 channels, 128-byte
-// swizzle.  split: CTAs of the cluster that share a tile's k (narrow only);
+// tmW: the weights (K, N, E) in boxes of 128 k by 128 channels, tmT: the
+// tokens (K, M) in boxes of 128 k by 32 rows, both in the 128-byte swizzle.
+// (A box past an expert's last token holds the next expert's: their columns
+// of the result are not stored.)  split: CTAs of the cluster that share a tile's k (narrow only);
 // then each cluster has one tile.  c_vec: C's rows allow 16-byte accesses.
 template <class C, class T>
 __global__ void __launch_bounds__(C::THREADS, 1)
-    i8_kernel(const __grid_constant__ CUtensorMap tmW, const Args a, int split, int c_vec)
+    i8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT,
+              const Args a, int split, int c_vec)
 {
     constexpr int CG = C::CG;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(base + C::OFF_BAR);
-    uint64_t *w_full = bars, *w_empty = w_full + C::RING;
-    uint64_t *ready = w_empty + C::RING;         // issuing CTA's: widened slots
-    uint64_t *slot_empty = ready + kSlots;       // per CTA: commits
-    uint64_t *acc_full = slot_empty + kSlots;    // per CTA: commits
+    uint64_t *w_full = bars, *w_empty = w_full + C::WRING;
+    uint64_t *t_full = w_empty + C::WRING, *t_empty = t_full + C::TRING;
+    uint64_t *ready = t_empty + C::TRING;        // issuing CTA's: widened slots
+    uint64_t *slot_empty = ready + C::SLOTS;     // per CTA: commits
+    uint64_t *acc_full = slot_empty + C::SLOTS;  // per CTA: commits
     uint64_t *acc_empty = acc_full + C::ACCS;    // issuing CTA's: epilogues
     uint64_t *mma_done = acc_empty + C::ACCS;
     uint32_t *tmem_base = reinterpret_cast<uint32_t *>(mma_done + 1);
@@ -249,12 +339,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const bool issuer = CG == 1 || rank == 0;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::RING; ++s) {
+        for (int s = 0; s < C::WRING; ++s) {
             mbar_init(&w_full[s], 1u);
             mbar_init(&w_empty[s], 4u);
         }
-        for (int s = 0; s < kSlots; ++s) {
-            mbar_init(&ready[s], static_cast<uint32_t>(CG * (4 + kBWarps)));
+        for (int s = 0; s < C::TRING; ++s) {
+            mbar_init(&t_full[s], 1u);
+            mbar_init(&t_empty[s], 4u);
+        }
+        for (int s = 0; s < C::SLOTS; ++s) {
+            mbar_init(&ready[s], static_cast<uint32_t>(CG * (4 + 4)));
             mbar_init(&slot_empty[s], 1u);
         }
         for (int s = 0; s < C::ACCS; ++s) {
@@ -265,6 +359,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmT);
     }
     if (warp == 1) {
         if constexpr (CG == 2)
@@ -300,200 +395,239 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int ks_lo = static_cast<int>(static_cast<long long>(k_slots) * krank / split);
     const int ks_hi = static_cast<int>(static_cast<long long>(k_slots) * (krank + 1) / split);
     float *part = reinterpret_cast<float *>(base + C::OFF_B);  // split: [token][channel]
+    static_assert(!C::HOLD || (C::EWARPS == 8 && 4 * kRegMisc + 16 * kRegConv + 8 * kRegEpi <=
+                                                     28 * 72 && kSets == 2),
+                  "the register shares stay within the launch's");
 
-    if (warp == 0) {
-        // ---------------------------------------------------- weights' producer
-        if (lane == 0) {
-            Ring<C::RING> rr;
-            long long issued = 0;
-            bool ok = true;
-            for (int u = cid; ok && u < tiles; u += ncl) {
-                const Job j = job<C>(a, table, u, half);
-                for (int ks = ks_lo; ks < ks_hi; ++ks) {
-                    if (!mbar_wait(&w_empty[rr.s], rr.ph ^ 1u, ab, kStatusWaitEmpty)) {
-                        ok = false;
-                        break;
+    if (warp < kAWarp0) {
+        if constexpr (C::HOLD) give_registers<kRegMisc>();
+        if (warp == 0) {
+            // ---------------------------------------------------- weights' producer
+            if (lane == 0) {
+                Ring<C::WRING> rr;
+                long long issued = 0;
+                bool ok = true;
+                for (int u = cid; ok && u < tiles; u += ncl) {
+                    const Job j = job<C>(a, table, u, half);
+                    for (int ks = ks_lo; ks < ks_hi; ++ks) {
+                        if (!mbar_wait(&w_empty[rr.s], rr.ph ^ 1u, ab, kStatusWaitEmpty)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&w_full[rr.s], kWStage);
+                        tma_load_3d(base + rr.s * kWStage, &tmW, &w_full[rr.s], ks * kSlotK, j.ch0,
+                                    j.e);
+                        ++issued;
+                        rr.next();
                     }
-                    mbar_arrive_expect_tx(&w_full[rr.s], kWStage);
-                    tma_load_3d(base + rr.s * kWStage, &tmW, &w_full[rr.s], ks * kSlotK, j.ch0,
-                                j.e);
-                    ++issued;
-                    rr.next();
+                }
+                if (!ok || *abort_flag) drain_ring<C::WRING>(w_full, issued, ab);
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // ---------------------------------------------------- tokens' producer
+            if (lane == 0) {
+                Ring<C::TRING> rr;
+                long long issued = 0;
+                bool ok = true;
+                for (int u = cid; ok && u < tiles; u += ncl) {
+                    const Job j = job<C>(a, table, u, half);
+                    const int per = j.neff / CG, boxes = (per + kBoxRows - 1) / kBoxRows;
+                    const int first = static_cast<int>(j.row0) + static_cast<int>(half) * per;
+                    for (int ks = ks_lo; ks < ks_hi; ++ks) {
+                        if (!mbar_wait(&t_empty[rr.s], rr.ph ^ 1u, ab, kStatusWaitEmpty)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t *dst = base + C::OFF_T + rr.s * C::TSTAGE;
+                        mbar_arrive_expect_tx(&t_full[rr.s],
+                                              static_cast<uint32_t>(boxes * kBoxRows * kSlotK));
+                        for (int x = 0; x < boxes; ++x)
+                            tma_load_3d(dst + x * kBoxRows * kSlotK, &tmT, &t_full[rr.s], ks * kSlotK,
+                                        first + x * kBoxRows, 0);
+                        ++issued;
+                        rr.next();
+                    }
+                }
+                if (!ok || *abort_flag) drain_ring<C::TRING>(t_full, issued, ab);
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ---------------------------------------------------- MMA issuer
+            if (issuer && lane == 0) {
+                Ring<C::SLOTS> sr;
+                Ring<C::ACCS> acc;
+                bool ok = true, any = false;
+                const uint64_t bdesc = tc::kmajor_sw128_desc(smem_u32(base + C::OFF_B));
+                for (int u = cid; ok && u < tiles; u += ncl) {
+                    const Job j = job<C>(a, table, u, half);
+                    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(j.neff >> 3) << 17) |
+                                           (static_cast<uint32_t>((kCh * CG) >> 4) << 24);
+                    if (!wait_cl(&acc_empty[acc.s], acc.ph ^ 1u, ab, kStatusWaitAcc)) break;
+                    tc::tc_fence_after();
+                    const uint32_t d = tmem + static_cast<uint32_t>(acc.s * C::NT);
+                    for (int ks = ks_lo; ks < ks_hi; ++ks) {
+                        if (!wait_cl(&ready[sr.s], sr.ph, ab, kStatusWaitConv)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::tc_fence_after();
+                        const uint32_t at = tmem + kACols + static_cast<uint32_t>(sr.s) * kSlotCols;
+                        const uint64_t bt = bdesc + static_cast<uint64_t>(sr.s * (C::BSLOT >> 4));
+    #pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_ts<CG>(d, at + 8 * kk,
+                                       bt + static_cast<uint64_t>((kk >> 2) * (C::BBOX >> 4) +
+                                                                  2 * (kk & 3)),
+                                       idesc, ks > ks_lo || kk > 0 ? 1u : 0u);
+                        any = true;
+                        commit<CG>(&slot_empty[sr.s]);
+                        sr.next();
+                    }
+                    if (!ok) break;
+                    commit<CG>(&acc_full[acc.s]);
+                    acc.next();
+                }
+                if (any) {
+                    commit<CG>(mma_done);
+                    drain_cl(mma_done, 0, ab.limit);
                 }
             }
-            if (!ok || *abort_flag) {  // let loads in flight land before the CTA exits
-                Ring<C::RING> d;
-                for (long long i = 0; i < issued; ++i) {
-                    if (i + C::RING >= issued) mbar_drain(&w_full[d.s], d.ph, ab.limit);
-                    d.next();
-                }
-            }
+            __syncwarp();
         }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ---------------------------------------------------- MMA issuer
-        if (issuer && lane == 0) {
-            Ring<kSlots> sr;
-            Ring<C::ACCS> acc;
-            bool ok = true, any = false;
-            const uint64_t bdesc = tc::kmajor_sw128_desc(smem_u32(base + C::OFF_B));
-            for (int u = cid; ok && u < tiles; u += ncl) {
-                const Job j = job<C>(a, table, u, half);
-                const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(j.neff >> 3) << 17) |
-                                       (static_cast<uint32_t>((kCh * CG) >> 4) << 24);
-                if (!wait_cl(&acc_empty[acc.s], acc.ph ^ 1u, ab, kStatusWaitAcc)) break;
-                tc::tc_fence_after();
-                const uint32_t d = tmem + static_cast<uint32_t>(acc.s * C::NT);
-                for (int ks = ks_lo; ks < ks_hi; ++ks) {
-                    if (!wait_cl(&ready[sr.s], sr.ph, ab, kStatusWaitConv)) {
+    } else if (warp < kBWarp0) {
+        if constexpr (C::HOLD) give_registers<kRegConv>();
+        // ---------------------------------------------------- weights: widen into tensor memory
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t tl = tmem + kACols + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t src0 = smem_u32(base) + row * 128 + ((row & 7) << 4);
+        int turn = (warp - kAWarp0) >> 2;  // 0: this set's slot
+        Ring<C::WRING> rr;
+        Ring<C::SLOTS> sr;
+        bool ok = true;
+        for (int u = cid; ok && u < tiles; u += ncl) {
+            for (int ks = ks_lo; ks < ks_hi; ++ks) {
+                if (turn == 0) {
+                    turn = kSets;
+                    if (!warp_wait(&w_full[rr.s], rr.ph, ab, kStatusWaitFull, lane) ||
+                        !warp_wait_cl(&slot_empty[sr.s], sr.ph ^ 1u, ab, kStatusWaitMma)) {
                         ok = false;
                         break;
                     }
                     tc::tc_fence_after();
-                    const uint32_t at = tmem + kACols + static_cast<uint32_t>(sr.s) * kSlotCols;
-                    const uint64_t bt = bdesc + static_cast<uint64_t>(sr.s * (C::BSLOT >> 4));
+                    const uint32_t src = src0 + static_cast<uint32_t>(rr.s * kWStage);
+                    const uint32_t dst = tl + static_cast<uint32_t>(sr.s) * kSlotCols;
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_ts<CG>(d, at + 8 * kk,
-                                   bt + static_cast<uint64_t>((kk >> 2) * (C::BBOX >> 4) +
-                                                              2 * (kk & 3)),
-                                   idesc, ks > ks_lo || kk > 0 ? 1u : 0u);
-                    any = true;
-                    commit<CG>(&slot_empty[sr.s]);
-                    sr.next();
-                }
-                if (!ok) break;
-                commit<CG>(&acc_full[acc.s]);
-                acc.next();
-            }
-            if (any) {
-                commit<CG>(mma_done);
-                drain_cl(mma_done, 0, ab.limit);
-            }
-        }
-        __syncwarp();
-    } else if (warp >= kAWarp0 && warp < kAWarp0 + 4) {
-        // ---------------------------------------------------- weights: widen into tensor memory
-        const int row = (warp & 3) * 32 + lane;
-        const uint32_t tl = tmem + kACols + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        Ring<C::RING> rr;
-        Ring<kSlots> sr;
-        bool ok = true;
-        for (int u = cid; ok && u < tiles; u += ncl) {
-            for (int ks = ks_lo; ks < ks_hi; ++ks) {
-                if (!warp_wait(&w_full[rr.s], rr.ph, ab, kStatusWaitFull, lane) ||
-                    !warp_wait_cl(&slot_empty[sr.s], sr.ph ^ 1u, ab, kStatusWaitMma)) {
-                    ok = false;
-                    break;
-                }
-                tc::tc_fence_after();
-                const uint32_t src = smem_u32(base + rr.s * kWStage) + row * 128;
-                const uint32_t dst = tl + static_cast<uint32_t>(sr.s) * kSlotCols;
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t x[16], y[16];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t x[16], y[16];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint4 v = lds128(src + (((4 * h + c) ^ (row & 7)) << 4));
-                        widen4(v.x, x[4 * c], x[4 * c + 1]);
-                        widen4(v.y, x[4 * c + 2], x[4 * c + 3]);
-                        widen4(v.z, y[4 * c], y[4 * c + 1]);
-                        widen4(v.w, y[4 * c + 2], y[4 * c + 3]);
+                        for (int c = 0; c < 4; ++c) {
+                            const uint4 v = lds128(src ^ static_cast<uint32_t>((4 * h + c) << 4));
+                            widen4(v.x, x[4 * c], x[4 * c + 1]);
+                            widen4(v.y, x[4 * c + 2], x[4 * c + 3]);
+                            widen4(v.z, y[4 * c], y[4 * c + 1]);
+                            widen4(v.w, y[4 * c + 2], y[4 * c + 3]);
+                        }
+                        tmem_put16(dst + 16 * h, x);
+                        tmem_put16(dst + 32 + 16 * h, y);
                     }
-                    tmem_put16(dst + 16 * h, x);
-                    tmem_put16(dst + 32 + 16 * h, y);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&w_empty[rr.s]);
+                    tc::tmem_wait_st();
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_issuer<CG>(&ready[sr.s]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&w_empty[rr.s]);
-                tc::tmem_wait_st();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_issuer<CG>(&ready[sr.s]);
+                --turn;
                 rr.next();
                 sr.next();
             }
         }
-    } else if (warp >= C::BWARP0) {
+    } else if (warp < kEWarp0) {
+        if constexpr (C::HOLD) give_registers<kRegConv>();
         // ---------------------------------------------------- tokens: widen into shared memory
-        const int t = static_cast<int>(threadIdx.x) - C::BWARP0 * 32;
-        const int c = t & 7, r16 = t >> 3;
-        const uint32_t off = static_cast<uint32_t>(r16 * 128 + ((c ^ (r16 & 7)) << 4));
-        Ring<kSlots> sr;
+        const int t = static_cast<int>(threadIdx.x) & 127;
+        int turn = (warp - kBWarp0) >> 2;
+        Ring<C::TRING> rr;
+        Ring<C::SLOTS> sr;
         bool ok = true;
         for (int u = cid; ok && u < tiles; u += ncl) {
             const Job j = job<C>(a, table, u, half);
-            const int per = j.neff / CG, groups = per >> 4;  // this CTA's tokens, 16 at a time
-            const int first = static_cast<int>(half) * per + r16;
-            const signed char *src = a.A + (j.row0 + first) * a.lda + 16 * c;
-            auto load = [&](int g, int ks) -> uint4 {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                const int k = ks * kSlotK + 16 * c;
-                if (first + 16 * g < j.n && k < a.K) {
-                    const signed char *p = src + 16LL * g * a.lda + ks * kSlotK;
-                    if (k + 16 <= a.K) {
-                        v = *reinterpret_cast<const uint4 *>(p);
-                    } else {  // the row's last bytes: nothing past K is read
-                        uint32_t w[4] = {0u, 0u, 0u, 0u};
-                        for (int i = 0; i < a.K - k; ++i) {
-                            const uint32_t b = (static_cast<uint32_t>(p[i]) & 255u) << (8 * (i & 3));
-                            if (i < 4)
-                                w[0] |= b;
-                            else if (i < 8)
-                                w[1] |= b;
-                            else if (i < 12)
-                                w[2] |= b;
-                            else
-                                w[3] |= b;
-                        }
-                        v = make_uint4(w[0], w[1], w[2], w[3]);
+            const int groups = j.neff / CG / 16;  // this CTA's tokens, 16 at a time
+            for (int ks = ks_lo; ks < ks_hi; ++ks) {
+                if (turn == 0) {
+                    turn = kSets;
+                    if (!warp_wait(&t_full[rr.s], rr.ph, ab, kStatusWaitFull, lane) ||
+                        !warp_wait_cl(&slot_empty[sr.s], sr.ph ^ 1u, ab, kStatusWaitMma)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t src =
+                        smem_u32(base + C::OFF_T + rr.s * C::TSTAGE) + 16u * static_cast<uint32_t>(t);
+                    const uint32_t dst =
+                        smem_u32(base + C::OFF_B + sr.s * C::BSLOT) + 16u * static_cast<uint32_t>(t);
+#pragma unroll
+                    for (int g = 0; g < 8; g += 4) {
+                        if (g >= groups) break;
+                        uint4 v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (g + i < groups) v[i] = lds128(src + (g + i) * 2048);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (g + i < groups) {
+                                uint32_t w[8];
+                                widen4(v[i].x, w[0], w[1]);
+                                widen4(v[i].y, w[2], w[3]);
+                                widen4(v[i].z, w[4], w[5]);
+                                widen4(v[i].w, w[6], w[7]);
+                                sts128(dst + (g + i) * 2048, w[0], w[1], w[2], w[3]);
+                                sts128(dst + (g + i) * 2048 + C::BBOX, w[4], w[5], w[6], w[7]);
+                            }
+                    }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&t_empty[rr.s]);
+                        arrive_issuer<CG>(&ready[sr.s]);
                     }
                 }
-                return v;
-            };
-            uint4 r[8];
-#pragma unroll
-            for (int g = 0; g < 8; ++g)
-                if (g < groups) r[g] = load(g, ks_lo);
-            for (int ks = ks_lo; ks < ks_hi; ++ks) {
-                if (!warp_wait_cl(&slot_empty[sr.s], sr.ph ^ 1u, ab, kStatusWaitMma)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t dst = smem_u32(base + C::OFF_B + sr.s * C::BSLOT) + off;
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    if (g >= groups) break;
-                    uint32_t w[8];
-                    widen4(r[g].x, w[0], w[1]);
-                    widen4(r[g].y, w[2], w[3]);
-                    widen4(r[g].z, w[4], w[5]);
-                    widen4(r[g].w, w[6], w[7]);
-                    sts128(dst + g * 2048, w[0], w[1], w[2], w[3]);
-                    sts128(dst + g * 2048 + C::BBOX, w[4], w[5], w[6], w[7]);
-                    if (ks + 1 < ks_hi) r[g] = load(g, ks + 1);
-                }
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive_issuer<CG>(&ready[sr.s]);
+                --turn;
+                rr.next();
                 sr.next();
             }
         }
-    } else if (warp >= kEWarp0) {
+    } else {
+        if constexpr (C::HOLD) take_registers<kRegEpi>();
         // ---------------------------------------------------- epilogue
+        // Lanes of tensor memory are channels, columns tokens; C wants a
+        // token's channels side by side.  fp32: 32 lanes store 128 bytes of a
+        // token's row as they are.  16 bits: chunks of 32 x 32 go through a
+        // transposing matrix store into 64-byte token rows (16-byte pieces
+        // XORed with token / 2 against bank conflicts) and out in 16-byte
+        // pieces.
         const int q = warp & 3, w = warp - kEWarp0;
         const int col0 = (w >> 2) * C::ECOLS;  // this warp's first token of the tile
-        T *stage = reinterpret_cast<T *>(base + C::OFF_STAGE + w * C::STAGING);
+        const uint32_t stage = smem_u32(base + C::OFF_STAGE + w * C::STAGING);
+        const uint32_t st_row = stage + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
         float *sa = reinterpret_cast<float *>(base + C::OFF_SCALE) + w * C::ECOLS;
-        constexpr int VPR = 2 * static_cast<int>(sizeof(T));  // 16-byte pieces of 32 values
         Ring<C::ACCS> acc;
         for (int u = cid; u < tiles; u += ncl) {
             const Job j = job<C>(a, table, u, half);
-            const int ch = j.ch0 + q * 32 + lane;
-            float sb = 0.f;
+            const int chq = j.ch0 + q * 32;        // this warp's first channel
+            const int n = min(j.n - col0, C::ECOLS);
+            const bool vec = sizeof(T) == 2 && c_vec != 0 && chq + 32 <= a.N;
+            float sb[4] = {};  // vec: rows lane / 4 + 8 i; else row lane
             if (split == 1) {
+                const float *sp = a.scaleB + static_cast<long long>(j.e) * a.N;
                 for (int i = lane; i < C::ECOLS; i += 32)
-                    sa[i] = col0 + i < j.n ? a.scaleA[j.row0 + col0 + i] : 0.f;
-                if (ch < a.N) sb = a.scaleB[static_cast<long long>(j.e) * a.N + ch];
+                    sa[i] = i < n ? a.scaleA[j.row0 + col0 + i] : 0.f;
+                if (vec) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sb[i] = sp[chq + 8 * i + (lane >> 2)];
+                } else if (chq + lane < a.N) {
+                    sb[0] = sp[chq + lane];
+                }
                 __syncwarp();
             }
             int got = 1;
@@ -503,44 +637,76 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             tc::tc_fence_after();
             const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) +
                                 static_cast<uint32_t>(acc.s * C::NT + col0);
-            const int n = min(j.n - col0, C::ECOLS);
-            const bool vec = c_vec != 0 && j.ch0 + q * 32 + 32 <= a.N;
+            T *crow = static_cast<T *>(a.C) + (j.row0 + col0) * a.ldc + chq;
+            // a chunk of 32 tokens, scaled and packed: m[4 t + i] is channels
+            // 8 i + lane / 4, tokens 8 t + 2 (lane % 4), + 1
+            auto pack_chunk = [&](int c0, uint32_t (&m)[16]) {
+                uint32_t v[2][16];
+                tmem_ld_16x32(tb + c0, v[0]);
+                tmem_ld_16x32(tb + (16u << 16) + c0, v[1]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const float2 s =
+                        *reinterpret_cast<const float2 *>(sa + c0 + 8 * t + 2 * (lane & 3));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        m[4 * t + i] = pack2<T>(
+                            __uint_as_float(v[i >> 1][4 * t + 2 * (i & 1)]) * s.x * sb[i],
+                            __uint_as_float(v[i >> 1][4 * t + 2 * (i & 1) + 1]) * s.y * sb[i]);
+                }
+            };
+            auto store_chunk = [&](int c0, const uint32_t (&m)[16]) {
+                __syncwarp();  // the staging's last readers are done
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const uint32_t x[4] = {m[4 * t], m[4 * t + 1], m[4 * t + 2], m[4 * t + 3]};
+                    store_transposed(st_row + t * 512, x);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 8 * i + (lane >> 2), p = lane & 3;
+                    const uint4 x = lds128(stage + r * 64 + ((p ^ ((r >> 1) & 3)) << 4));
+                    if (c0 + r < n)
+                        *reinterpret_cast<uint4 *>(crow + (c0 + r) * a.ldc + 8 * p) = x;
+                }
+            };
+            if (C::HOLD && split == 1 && vec) {
+                constexpr int NCH = C::HOLD ? C::ECOLS / 32 : 1;
+                uint32_t m[NCH][16];
+#pragma unroll
+                for (int c = 0; c < NCH; ++c)
+                    if (32 * c < n) pack_chunk(32 * c, m[c]);
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_issuer<CG>(&acc_empty[acc.s]);
+#pragma unroll
+                for (int c = 0; c < NCH; ++c)
+                    if (32 * c < n) store_chunk(32 * c, m[c]);
+                acc.next();
+                continue;
+            }
 #pragma unroll 1
             for (int c0 = 0; c0 < n; c0 += 32) {
+                if (split == 1 && vec) {
+                    uint32_t m[16];
+                    pack_chunk(c0, m);
+                    store_chunk(c0, m);
+                    continue;
+                }
                 float v[32];
                 tc::tmem_ld32(tb + c0, v);
                 if (split > 1) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         part[(col0 + c0 + i) * kCh + q * 32 + lane] = v[i];
-                    continue;
-                }
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 s = *reinterpret_cast<const float4 *>(sa + c0 + i);
-                    v[i] = v[i] * s.x * sb;
-                    v[i + 1] = v[i + 1] * s.y * sb;
-                    v[i + 2] = v[i + 2] * s.z * sb;
-                    v[i + 3] = v[i + 3] * s.w * sb;
-                }
-                T *crow = static_cast<T *>(a.C) + (j.row0 + col0 + c0) * a.ldc;
-                if (vec) {
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) stage[i * 32 + lane] = rows::from_f<T>(v[i]);
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < VPR; ++i) {
-                        const int x = i * 32 + lane, r = x / VPR, p = x % VPR;
-                        if (c0 + r < n)
-                            *reinterpret_cast<uint4 *>(crow + r * a.ldc + j.ch0 + q * 32 +
-                                                       p * (16 / sizeof(T))) =
-                                reinterpret_cast<const uint4 *>(stage)[x];
-                    }
-                } else if (ch < a.N) {
+                } else if (chq + lane < a.N) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (c0 + i < n) crow[i * a.ldc + ch] = rows::from_f<T>(v[i]);
+                        if (c0 + i < n)
+                            crow[(c0 + i) * a.ldc + lane] =
+                                rows::from_f<T>(v[i] * sa[c0 + i] * sb[0]);
                 }
             }
             tc::tc_fence_before();
@@ -606,8 +772,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
 // Enqueues the kernel on `clusters` clusters of CG (or split) CTAs.
 template <class C, class T>
-int launch_tc_i8(const Args &a, const CUtensorMap &tmW, long long clusters, int split, bool c_vec,
-                 cudaStream_t st)
+int launch_tc_i8(const Args &a, const CUtensorMap &tmW, const CUtensorMap &tmT, long long clusters,
+                 int split, bool c_vec, cudaStream_t st)
 {
     auto kern = i8_kernel<C, T>;
     if (!smem_attr_once(reinterpret_cast<const void *>(kern), C::SMEM)) return SGEMM_ERR_LAUNCH;
@@ -624,7 +790,7 @@ int launch_tc_i8(const Args &a, const CUtensorMap &tmW, long long clusters, int 
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, tmW, a, split, c_vec ? 1 : 0) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kern, tmW, tmT, a, split, c_vec ? 1 : 0) != cudaSuccess) {
         cudaGetLastError();
         return SGEMM_ERR_LAUNCH;
     }

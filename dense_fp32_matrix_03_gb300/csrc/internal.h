@@ -211,7 +211,7 @@ bool encode_operand16(CUtensorMap *map, const void *base, bool bf16, long long r
                       long long ld, int Q, long long stride, int box_rows);
 // Tensor map of E matrices of 8-bit values stored rows x K (K-inner, `stride`
 // values apart): boxes of 128 k by box_rows rows with the 128-byte swizzle.
-bool encode_weights8(CUtensorMap *map, const signed char *base, long long rows, long long K,
+bool encode_operand8(CUtensorMap *map, const signed char *base, long long rows, long long K,
                      long long ld, int E, long long stride, int box_rows);
 // Copies Q matrices of 16-bit values into dst as rows x cols K-inner
 // matrices (row pitch ldd, batch stride dstride): dst[r][c] = src[c][r] when
