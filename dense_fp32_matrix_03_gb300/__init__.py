@@ -141,10 +141,12 @@ class _Lazy:
     def __init__(self):
         self._h = None
 
-    def __getattr__(self, name):
+    def __getattr__(self, name):  # only for names not kept yet
         if self._h is None:
             self._h = _load()
-        return getattr(self._h, name)
+        fn = getattr(self._h, name)
+        setattr(self, name, fn)
+        return fn
 
 
 _lib = _Lazy()
@@ -159,22 +161,39 @@ def _ptr(x):
     """Device address of a tensor (data_ptr) or a raw integer address."""
     if x is None:
         return None
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
-    return int(x)
+    except AttributeError:
+        return int(x)
+
+
+_raw_stream = None  # torch's current stream on the current device, as a handle
+
+
+def _current_stream():
+    """Handle of torch's current stream; None (the legacy default stream)
+    without torch or before it uses a GPU."""
+    global _raw_stream
+    if _raw_stream is None:
+        try:
+            import torch
+        except ImportError:
+            return None
+        if not (torch.cuda.is_available() and torch.cuda.is_initialized()):
+            return None
+        try:  # no Stream object per call: small products are launch-bound
+            device, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+            _raw_stream = lambda: raw(device())
+        except AttributeError:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream
+    return _raw_stream()
 
 
 def _stream(s):
     """cudaStream_t of a torch stream, a raw handle, or torch's current stream
     when None (0, the legacy default stream, without torch)."""
     if s is None:
-        try:
-            import torch
-            if torch.cuda.is_available() and torch.cuda.is_initialized():
-                return torch.cuda.current_stream().cuda_stream
-        except ImportError:
-            pass
-        return None
+        return _current_stream() or None
     if hasattr(s, "cuda_stream"):
         return s.cuda_stream
     return int(s) or None

@@ -2,6 +2,7 @@
 // the stable sort, and the row kernels of dispatch, combine and their
 // gradients.
 #include "../../include/expert_layer.h"
+#include "dependent.cuh"
 #include "rows.cuh"
 
 namespace sg {
@@ -84,7 +85,9 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     const long long hi = min(lo + len, static_cast<long long>(S));
     int *mine = hist + warp * E1;
 
+    dependent_release();
     for (int i = tid; i < kSortWarps * E1; i += kSortThreads) hist[i] = 0;
+    dependent_wait();
     __syncthreads();
     for (long long i = lo; i < hi; i += 32) {
         const int key = sort_key(ids, i + lane, S, E);
@@ -180,6 +183,8 @@ struct Args {
 template <class T, int VB>
 __global__ void __launch_bounds__(256) dispatch_kernel(const Args a)
 {
+    dependent_release();
+    dependent_wait();
     const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (t >= a.T) return;
     const int total = *a.total;
@@ -207,6 +212,8 @@ template <class T, int VB>
 __global__ void __launch_bounds__(256) combine_kernel(const Args a)
 {
     using V = Vec<T, VB>;
+    dependent_release();
+    dependent_wait();
     const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (t >= a.T) return;
     const int total = min(*a.total, a.S);
@@ -250,6 +257,8 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const Args a)
 {
     using V = Vec<T, VB>;
     __shared__ float part[8][kGroup];  // one row per warp of the block
+    dependent_release();
+    dependent_wait();
     const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     const bool live = t < a.T;
     const int total = min(*a.total, a.S);
@@ -337,17 +346,11 @@ struct Launch {
     int run() const
     {
         const Grid g = row_grid(a.T, a.nvec, op != kCombineGrad);
-        if (op == kDispatch)
-            dispatch_kernel<T, VB><<<g.grid, g.block, 0, st>>>(a);
-        else if (op == kCombine)
-            combine_kernel<T, VB><<<g.grid, g.block, 0, st>>>(a);
-        else if (a.dweights != nullptr)
-            combine_grad_kernel<T, VB, true><<<g.grid, g.block, 0, st>>>(a);
-        else
-            combine_grad_kernel<T, VB, false><<<g.grid, g.block, 0, st>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return SGEMM_ERR_LAUNCH;
-        note_launch();
-        return SGEMM_OK;
+        auto kern = op == kDispatch              ? dispatch_kernel<T, VB>
+                    : op == kCombine             ? combine_kernel<T, VB>
+                    : a.dweights != nullptr      ? combine_grad_kernel<T, VB, true>
+                                                 : combine_grad_kernel<T, VB, false>;
+        return launch_dependent(kern, g.grid, g.block, 0, 1, st, a);
     }
 };
 
@@ -444,27 +447,11 @@ int sgemm_experts_sort(int T, int k, int E, const int *ids, int *offsets, int *s
     const int smem = (ex::kSortWarps + 2) * (E + 1) * static_cast<int>(sizeof(int));
     if (!smem_attr_once(reinterpret_cast<const void *>(ex::sort_kernel), smem))
         return SGEMM_ERR_LAUNCH;
-    cudaLaunchConfig_t cfg{};
     // one CTA walks up to 4096 choices in four steps per warp and walk
     const unsigned ncta = S <= 4096 ? 1u : static_cast<unsigned>(ex::kMaxCluster);
-    cfg.gridDim = dim3(ncta);
-    cfg.blockDim = dim3(ex::kSortThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ncta;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, ex::sort_kernel, ids, S, E, offsets, slots, positions) !=
-        cudaSuccess) {
-        cudaGetLastError();
-        return SGEMM_ERR_LAUNCH;
-    }
-    note_launch();
-    return SGEMM_OK;
+    return launch_dependent(ex::sort_kernel, dim3(ncta), dim3(ex::kSortThreads),
+                            static_cast<size_t>(smem), ncta, static_cast<cudaStream_t>(stream),
+                            ids, S, E, offsets, slots, positions);
 }
 
 int sgemm_experts_dispatch(int type, int T, int k, int E, int H, const void *x, int ldx,

@@ -1,9 +1,12 @@
 // i8_gemm.cu -- products of 8-bit integers with a scale for each token and
 // channel (include/int8_gemm.h): argument checks, the choice of the kernel
 // and the integer dot-product kernel (the tensor-core one is i8_tc.cuh).
+#include <cmath>
 #include <cstring>
 
 #include "../../include/int8_gemm.h"
+#include "dependent.cuh"
+#include "i8_few.cuh"
 #include "i8_gemm.h"
 #include "i8_tc.cuh"
 #include "rows.cuh"
@@ -37,6 +40,8 @@ __global__ void __launch_bounds__(256) dot_kernel(const Args a)
     __shared__ uint32_t As[kDW][kDT + 1], Bs[kDW][kDT + 1];
     __shared__ Tile tl;
     const int tid = threadIdx.x;
+    dependent_release();
+    dependent_wait();
     if (tid < 32) {
         const Tile t = find_tile_warp(a, blockIdx.y, kDT, tid);
         if (tid == 0) tl = t;
@@ -95,12 +100,9 @@ int launch_dot(const Args &a, cudaStream_t st)
         b.tile0 = static_cast<int>(y0);
         const dim3 grid(static_cast<unsigned>(gx),
                         static_cast<unsigned>(gy - y0 < 65535 ? gy - y0 : 65535));
-        if (words)
-            dot_kernel<T, true><<<grid, 256, 0, st>>>(b);
-        else
-            dot_kernel<T, false><<<grid, 256, 0, st>>>(b);
-        if (cudaGetLastError() != cudaSuccess) return SGEMM_ERR_LAUNCH;
-        note_launch();
+        const int rc = launch_dependent(words ? dot_kernel<T, true> : dot_kernel<T, false>, grid,
+                                        dim3(256), 0, 1, st, b);
+        if (rc != SGEMM_OK) return rc;
     }
     return SGEMM_OK;
 }
@@ -115,6 +117,17 @@ bool rows_on_16(const Args &a)
            (a.E == 1 || a.strideB % 16 == 0);
 }
 
+// Output tiles of nt tokens x ch channels that a call is expected to have:
+// experts share the rows about evenly, and end in half a tile.
+double tiles_expected(const Args &a, int nt, int ch)
+{
+    const double cts = (a.N + ch - 1) / ch;
+    if (a.offsets == nullptr) return (a.M + nt - 1LL) / nt * cts;
+    const int used = a.E < a.M ? a.E : a.M;
+    const double each = static_cast<double>(a.M) / used / nt + 0.5;
+    return used * (each > 1. ? each : 1.) * cts;
+}
+
 template <class T>
 int run(const Args &a, cudaStream_t st)
 {
@@ -126,18 +139,30 @@ int run(const Args &a, cudaStream_t st)
         !encode_operand8(&tmW, a.B, a.N, a.K, a.ldb, a.E, a.strideB, kCh) ||
         !encode_operand8(&tmT, a.A, a.M, a.K, a.lda, 1, 0, kBoxRows))
         return launch_dot<T>(a, st);
-    const bool c_vec = aligned16(a.C) && a.ldc * static_cast<long long>(sizeof(T)) % 16 == 0;
+    const int c_bytes = rows::Width().add(a.C).add(a.ldc * sizeof(T)).bytes();
     const int k_slots = (a.K + kSlotK - 1) / kSlotK;
-    if (a.M / a.E > 128) {
-        const long long tiles = max_tiles(a, Wide::NT) * ((a.N + 2 * kCh - 1) / (2 * kCh));
-        const int pairs = ss_slots(a.num_sms);
-        return launch_tc_i8<Wide, T>(a, tmW, tmT, tiles < pairs ? tiles : pairs, 1, c_vec, st);
+    if (a.E == 1 && a.M <= 16) {
+        if (a.M == 1) return launch_dots<T, 1>(a, st);
+        if (a.M == 2) return launch_dots<T, 2>(a, st);
+        if (a.M <= 4) return launch_dots<T, 4>(a, st);
+        return a.M <= 8 ? launch_few<T, 1, 1, 16, 2>(a, st) : launch_few<T, 2, 1, 16, 2>(a, st);
     }
-    const long long tiles = max_tiles(a, Narrow::NT) * ((a.N + kCh - 1) / kCh);
+    if (a.E > 1 && a.M <= 8LL * a.E) return launch_few<T, 1, 2, 4, 6>(a, st);
+    const int pairs = ss_slots(a.num_sms);
+    const double narrow_tiles = tiles_expected(a, Narrow::NT, kCh);
+    const double wide_tiles = tiles_expected(a, Wide::NT, 2 * kCh);
     int split = 1;
-    while (split < 8 && tiles * split * 2 <= a.num_sms && k_slots >= 4 * split) split *= 2;
+    while (split < 8 && narrow_tiles * split * 2 <= a.num_sms && k_slots >= 4 * split) split *= 2;
+    const double narrow_cost = 0.63 / split * ceil(narrow_tiles * split / a.num_sms);
+    const double wide_cost = (wide_tiles < pairs ? 0.70 : 0.60) * ceil(wide_tiles / pairs);
+    if (wide_cost < narrow_cost) {
+        const long long tiles = max_tiles(a, Wide::NT) * ((a.N + 2 * kCh - 1) / (2 * kCh));
+        return launch_tc_i8<Wide, T>(a, tmW, tmT, tiles < pairs ? tiles : pairs, 1, c_bytes, st);
+    }
+    // a cluster that shares a tile's k has one tile
+    const long long tiles = max_tiles(a, Narrow::NT) * ((a.N + kCh - 1) / kCh);
     const long long clusters = split > 1 || tiles < a.num_sms ? tiles : a.num_sms;
-    return launch_tc_i8<Narrow, T>(a, tmW, tmT, clusters, split, c_vec, st);
+    return launch_tc_i8<Narrow, T>(a, tmW, tmT, clusters, split, c_bytes, st);
 }
 
 // Checks and enqueues a product; offsets null: one dense group of M rows.

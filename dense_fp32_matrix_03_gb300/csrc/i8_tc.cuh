@@ -54,6 +54,7 @@
 #include <cuda_fp16.h>
 
 #include "../../include/sgemm.h"
+#include "dependent.cuh"
 #include "i8_gemm.h"
 #include "rows.cuh"
 #include "tc_pair.cuh"
@@ -113,7 +114,7 @@ struct Cfg {
 #define I8_WIDE 2, 256, 3, 3, 3, 8
 #endif
 #ifndef I8_NARROW
-#define I8_NARROW 1, 128, 3, 4, 2, 4
+#define I8_NARROW 1, 128, 3, 4, 3, 4
 #endif
 using Narrow = Cfg<I8_NARROW>;
 using Wide = Cfg<I8_WIDE>;
@@ -129,6 +130,14 @@ template <int N>
 __device__ __forceinline__ void take_registers()
 {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *m, int c0, int c1, int c2)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
 }
 
 // Four bytes (8-bit integers) as four fp16 values.
@@ -308,11 +317,12 @@ __device__ __forceinline__ Job job(const Args &a, const int *table, int u, uint3
 // tokens (K, M) in boxes of 128 k by 32 rows, both in the 128-byte swizzle.
 // (A box past an expert's last token holds the next expert's: their columns
 // of the result are not stored.)  split: CTAs of the cluster that share a tile's k (narrow only);
-// then each cluster has one tile.  c_vec: C's rows allow 16-byte accesses.
+// then each cluster has one tile.  c_bytes: accesses that C's rows allow
+// (16, 8 or fewer).
 template <class C, class T>
 __global__ void __launch_bounds__(C::THREADS, 1)
     i8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT,
-              const Args a, int split, int c_vec)
+              const Args a, int split, int c_bytes)
 {
     constexpr int CG = C::CG;
     extern __shared__ uint8_t smem_raw[];
@@ -337,6 +347,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int cid = static_cast<int>(blockIdx.x) / cluster;
     const int ncl = static_cast<int>(gridDim.x) / cluster;
     const bool issuer = CG == 1 || rank == 0;
+    const int k_slots = (a.K + kSlotK - 1) / kSlotK;
+    const int ks_lo = static_cast<int>(static_cast<long long>(k_slots) * krank / split);
+    const int ks_hi = static_cast<int>(static_cast<long long>(k_slots) * (krank + 1) / split);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::WRING; ++s) {
@@ -367,6 +380,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         else
             tc::tmem_alloc(tmem_base, 512);
     }
+    // dense: the first tile's weights start on their way into L2 while the
+    // kernel before (the quantiser, as a rule) runs; nothing is read yet
+    dependent_release();
+    if (a.offsets == nullptr && warp == 3 && lane == 0) {
+        const int ch0 = (cid / ((a.M + C::NT - 1) / C::NT) * CG + static_cast<int>(half)) * kCh;
+        for (int ks = ks_lo; ks < ks_hi && ks < ks_lo + 16; ++ks)
+            tma_prefetch_3d(&tmW, ks * kSlotK, ch0, 0);
+    }
+    dependent_wait();
     if (warp == 2) {  // the tile table
         const int cts = (a.N + kCh * CG - 1) / (kCh * CG);
         int sum = 0;
@@ -391,9 +413,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const uint32_t tmem = *tmem_base;
     const Abort ab{abort_flag, a.status, kWaitLimitCycles};
     const int tiles = table[a.E];
-    const int k_slots = (a.K + kSlotK - 1) / kSlotK;
-    const int ks_lo = static_cast<int>(static_cast<long long>(k_slots) * krank / split);
-    const int ks_hi = static_cast<int>(static_cast<long long>(k_slots) * (krank + 1) / split);
     float *part = reinterpret_cast<float *>(base + C::OFF_B);  // split: [token][channel]
     static_assert(!C::HOLD || (C::EWARPS == 8 && 4 * kRegMisc + 16 * kRegConv + 8 * kRegEpi <=
                                                      28 * 72 && kSets == 2),
@@ -616,15 +635,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const Job j = job<C>(a, table, u, half);
             const int chq = j.ch0 + q * 32;        // this warp's first channel
             const int n = min(j.n - col0, C::ECOLS);
-            const bool vec = sizeof(T) == 2 && c_vec != 0 && chq + 32 <= a.N;
-            float sb[4] = {};  // vec: rows lane / 4 + 8 i; else row lane
+            constexpr bool PACK = sizeof(T) == 2;
+            float sb[4] = {};  // 16 bits: rows lane / 4 + 8 i; else row lane
             if (split == 1) {
                 const float *sp = a.scaleB + static_cast<long long>(j.e) * a.N;
                 for (int i = lane; i < C::ECOLS; i += 32)
                     sa[i] = i < n ? a.scaleA[j.row0 + col0 + i] : 0.f;
-                if (vec) {
+                if (PACK) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sb[i] = sp[chq + 8 * i + (lane >> 2)];
+                    for (int i = 0; i < 4; ++i)
+                        if (chq + 8 * i + (lane >> 2) < a.N) sb[i] = sp[chq + 8 * i + (lane >> 2)];
                 } else if (chq + lane < a.N) {
                     sb[0] = sp[chq + lane];
                 }
@@ -664,16 +684,39 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     store_transposed(st_row + t * 512, x);
                 }
                 __syncwarp();
+                T *out = crow + static_cast<long long>(c0) * a.ldc;
+                if (c_bytes == 16 && chq + 32 <= a.N) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 8 * i + (lane >> 2), p = lane & 3;
-                    const uint4 x = lds128(stage + r * 64 + ((p ^ ((r >> 1) & 3)) << 4));
-                    if (c0 + r < n)
-                        *reinterpret_cast<uint4 *>(crow + (c0 + r) * a.ldc + 8 * p) = x;
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 8 * i + (lane >> 2), p = lane & 3;
+                        const uint4 x = lds128(stage + r * 64 + ((p ^ ((r >> 1) & 3)) << 4));
+                        if (c0 + r < n) *reinterpret_cast<uint4 *>(out + r * a.ldc + 8 * p) = x;
+                    }
+                } else if (c_bytes >= 8 && chq + 32 <= a.N) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + (lane >> 3), p = lane & 7;
+                        uint2 x;
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                     : "=r"(x.x), "=r"(x.y)
+                                     : "r"(stage + r * 64 + (((p >> 1) ^ ((r >> 1) & 3)) << 4) +
+                                           8 * (p & 1)));
+                        if (c0 + r < n) *reinterpret_cast<uint2 *>(out + r * a.ldc + 4 * p) = x;
+                    }
+                } else {  // a token's row at a time
+                    for (int r = 0; r < 32 && c0 + r < n; ++r) {
+                        uint16_t x;
+                        asm volatile("ld.shared.u16 %0, [%1];"
+                                     : "=h"(x)
+                                     : "r"(stage + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) +
+                                           2 * (lane & 7)));
+                        if (chq + lane < a.N)
+                            *reinterpret_cast<uint16_t *>(out + r * a.ldc + lane) = x;
+                    }
                 }
             };
-            if (C::HOLD && split == 1 && vec) {
-                constexpr int NCH = C::HOLD ? C::ECOLS / 32 : 1;
+            if (PACK && C::HOLD) {
+                constexpr int NCH = PACK && C::HOLD ? C::ECOLS / 32 : 1;
                 uint32_t m[NCH][16];
 #pragma unroll
                 for (int c = 0; c < NCH; ++c)
@@ -689,7 +732,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
 #pragma unroll 1
             for (int c0 = 0; c0 < n; c0 += 32) {
-                if (split == 1 && vec) {
+                if (PACK && split == 1) {
                     uint32_t m[16];
                     pack_chunk(c0, m);
                     store_chunk(c0, m);
@@ -743,7 +786,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const float o[4] = {s.x * sc * sb[0], s.y * sc * sb[1], s.z * sc * sb[2],
                                     s.w * sc * sb[3]};
                 T *cp = static_cast<T *>(a.C) + (j.row0 + t) * a.ldc + ch;
-                if (c_vec != 0 && ch + 4 <= a.N) {
+                if (c_bytes >= 4 * static_cast<int>(sizeof(T)) && ch + 4 <= a.N) {
                     rows::Vec<T, 4 * static_cast<int>(sizeof(T))> x;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x.set(i, o[i]);
@@ -773,29 +816,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 // Enqueues the kernel on `clusters` clusters of CG (or split) CTAs.
 template <class C, class T>
 int launch_tc_i8(const Args &a, const CUtensorMap &tmW, const CUtensorMap &tmT, long long clusters,
-                 int split, bool c_vec, cudaStream_t st)
+                 int split, int c_bytes, cudaStream_t st)
 {
     auto kern = i8_kernel<C, T>;
     if (!smem_attr_once(reinterpret_cast<const void *>(kern), C::SMEM)) return SGEMM_ERR_LAUNCH;
     const unsigned size = C::CG == 2 ? 2u : static_cast<unsigned>(split);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(clusters) * size);
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = size;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, tmW, tmT, a, split, c_vec ? 1 : 0) != cudaSuccess) {
-        cudaGetLastError();
-        return SGEMM_ERR_LAUNCH;
-    }
-    note_launch();
-    return SGEMM_OK;
+    return launch_dependent(kern, dim3(static_cast<unsigned>(clusters) * size), dim3(C::THREADS),
+                            C::SMEM, size, st, tmW, tmT, a, split, c_bytes);
 }
 
 }  // namespace i8

@@ -8,6 +8,7 @@
 // maximum is taken on the bit patterns of the magnitudes, where an infinity
 // or NaN is larger than every finite value and so cannot be missed.
 #include "../../include/expert_layer.h"
+#include "dependent.cuh"
 #include "rows.cuh"
 
 namespace sg {
@@ -79,6 +80,8 @@ __global__ void __launch_bounds__(256) quantize_kernel(const Args a)
 {
     constexpr int EV = Vec<T, VB>::N;
     __shared__ unsigned part[8];
+    dependent_release();
+    dependent_wait();
     const long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     const bool live = r < a.M;
     const char *row = a.x + (live ? r : 0) * a.x_pitch;
@@ -176,13 +179,9 @@ struct Launch {
         const int tx = rows::pow2_threads((a.nvec + kHeld - 1) / kHeld, 32, 256), ty = 256 / tx;
         const dim3 block(static_cast<unsigned>(tx), static_cast<unsigned>(ty));
         const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.M) + ty - 1) / ty));
-        if (qv)
-            quantize_kernel<T, VB, GATED, EXPERT, true><<<grid, block, 0, st>>>(a);
-        else
-            quantize_kernel<T, VB, GATED, EXPERT, false><<<grid, block, 0, st>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return SGEMM_ERR_LAUNCH;
-        note_launch();
-        return SGEMM_OK;
+        auto kern = qv ? quantize_kernel<T, VB, GATED, EXPERT, true>
+                       : quantize_kernel<T, VB, GATED, EXPERT, false>;
+        return launch_dependent(kern, grid, block, 0, 1, st, a);
     }
     template <class T, int VB>
     int run() const
