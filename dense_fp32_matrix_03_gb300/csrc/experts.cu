@@ -1,6 +1,8 @@
 // experts.cu -- tokens sorted by expert and back (include/expert_layer.h):
 // the stable sort, and the row kernels of dispatch, combine and their
 // gradients.
+#include <atomic>
+
 #include "../../include/expert_layer.h"
 #include "dependent.cuh"
 #include "rows.cuh"
@@ -14,8 +16,13 @@ using rows::Vec;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 64;   // k
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kMaxCluster = 8;
-constexpr int kGroup = 8;         // choices of a token whose rows are in flight together
+constexpr int kSortAhead = 8;     // steps of a warp's walk loaded at once
+// Choices of a token whose rows are in flight together.  Four, on blocks small
+// enough in registers that five or six share a multiprocessor, hide each
+// other's chain of position, row and sum best (65536 rows of 4096 bf16
+// combined, by choices x blocks: 8 x 4 97 us, 4 x 6 95, 4 x 8 (spills) 299,
+// 2 x 8 112; the gradient of 32768 rows of 2048: 8 x 4 66, 4 x 5 48, 2 x 8 61).
+constexpr int kGroup = 4;
 
 // ------------------------------------------------------------------ sort
 //
@@ -24,7 +31,7 @@ constexpr int kGroup = 8;         // choices of a token whose rows are in flight
 // per warp, in order, over a cluster of CTAs, so that ranks within a segment
 // need no atomics and the order is stable by construction:
 //   1. each warp counts its segment into a histogram of its own (lanes of
-//      equal key found with a warp match, their leader adds their number);
+//      equal key found with a warp match, the first adds their number);
 //   2. a scan over the CTA's warps turns counts into the warp's first rank,
 //      and the CTAs' totals, read through distributed shared memory, into
 //      each expert's first position and each CTA's share of it;
@@ -60,11 +67,16 @@ __device__ __forceinline__ int cluster_load(const int *p, int rank)
     return static_cast<int>(v);
 }
 
-__device__ __forceinline__ int sort_key(const int *ids, long long i, int S, int E)
+// The keys of this lane's choices i, i + 32, ... (dropped: E; past the
+// segment: -1), all on their way at once.
+__device__ __forceinline__ void load_keys(int (&key)[kSortAhead], const int *ids, long long i,
+                                          long long hi, int E)
 {
-    if (i >= S) return -1;
-    const int e = ids[i];
-    return (e < 0 || e >= E) ? E : e;
+#pragma unroll
+    for (int c = 0; c < kSortAhead; ++c) key[c] = i + 32 * c < hi ? ids[i + 32 * c] : -1;
+#pragma unroll
+    for (int c = 0; c < kSortAhead; ++c)
+        key[c] = i + 32 * c >= hi ? -1 : (key[c] < 0 || key[c] >= E) ? E : key[c];
 }
 
 __global__ void __launch_bounds__(kSortThreads, 1)
@@ -89,11 +101,16 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     for (int i = tid; i < kSortWarps * E1; i += kSortThreads) hist[i] = 0;
     dependent_wait();
     __syncthreads();
-    for (long long i = lo; i < hi; i += 32) {
-        const int key = sort_key(ids, i + lane, S, E);
-        const unsigned same = __match_any_sync(0xffffffffu, key);
-        if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
-        __syncwarp();
+    for (long long i = lo; i < hi; i += 32 * kSortAhead) {
+        int key[kSortAhead];
+        load_keys(key, ids, i + lane, hi, E);
+#pragma unroll
+        for (int c = 0; c < kSortAhead; ++c) {
+            if (i + 32 * c >= hi) break;
+            const unsigned same = __match_any_sync(0xffffffffu, key[c]);
+            if (key[c] >= 0 && lane == __ffs(same) - 1) mine[key[c]] += __popc(same);
+            __syncwarp();
+        }
     }
     __syncthreads();
     for (int e = tid; e < E1; e += kSortThreads) {
@@ -141,20 +158,66 @@ __global__ void __launch_bounds__(kSortThreads, 1)
         if (tid == 0) offsets[E] = kept;
     }
     cluster_barrier();  // tot has been read by every CTA; base is written
-    for (long long i = lo; i < hi; i += 32) {
-        const int key = sort_key(ids, i + lane, S, E);
-        const unsigned same = __match_any_sync(0xffffffffu, key);
-        const int before_me = __popc(same & ((1u << lane) - 1u));
-        int p = 0;
-        if (key >= 0) p = base[key] + mine[key] + before_me;
-        __syncwarp();
-        if (key >= 0) {
-            positions[i + lane] = p;
-            slots[p] = static_cast<int>(i) + lane;
-            if (before_me == 0) mine[key] += __popc(same);
+    for (long long i = lo; i < hi; i += 32 * kSortAhead) {
+        int key[kSortAhead];
+        load_keys(key, ids, i + lane, hi, E);
+#pragma unroll
+        for (int c = 0; c < kSortAhead; ++c) {
+            if (i + 32 * c >= hi) break;
+            const unsigned same = __match_any_sync(0xffffffffu, key[c]);
+            const int before_me = __popc(same & ((1u << lane) - 1u));
+            int p = 0;
+            if (key[c] >= 0) p = base[key[c]] + mine[key[c]] + before_me;
+            __syncwarp();
+            if (key[c] >= 0) {
+                const int slot = static_cast<int>(i) + 32 * c + lane;
+                positions[slot] = p;
+                slots[p] = slot;
+                if (before_me == 0) mine[key[c]] += __popc(same);
+            }
+            __syncwarp();
         }
-        __syncwarp();
     }
+}
+
+// CTAs of the sort's cluster: one for up to 512 choices (half a step per warp),
+// 8 beyond, 16 from 8192 on where the GPU has room for such a cluster
+// (64 experts: 2048 choices 7.0 us on one, 4104 6.6 us on 8, 65536 20 us on 8
+// and 12 us on 16: what costs is a warp's match of up to 32 different keys and
+// its stores to as many lines).
+unsigned sort_cluster(int S)
+{
+    if (S <= 512) return 1u;
+    static std::atomic<int> widest[64];  // per device: 0 not asked yet
+    int dev = 0;
+    if (S <= 8192 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 8u;
+    int w = widest[dev].load();
+    if (w == 0) {
+        int n = 0;
+        // the largest shared memory any call asks for
+        const int most = (kSortWarps + 2) * (kMaxExperts + 1) * static_cast<int>(sizeof(int));
+        if (cudaFuncSetAttribute(reinterpret_cast<const void *>(sort_kernel),
+                                 cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                 1) == cudaSuccess &&
+            smem_attr_once(reinterpret_cast<const void *>(sort_kernel), most)) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(16);
+            cfg.blockDim = dim3(kSortThreads);
+            cfg.dynamicSmemBytes = static_cast<size_t>(most);
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 16;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, sort_kernel, &cfg) != cudaSuccess) n = 0;
+        }
+        cudaGetLastError();
+        w = n > 0 ? 16 : 8;
+        widest[dev].store(w);
+    }
+    return static_cast<unsigned>(w);
 }
 
 // -------------------------------------------------------------- row kernels
@@ -209,7 +272,7 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const Args a)
 }
 
 template <class T, int VB>
-__global__ void __launch_bounds__(256) combine_kernel(const Args a)
+__global__ void __launch_bounds__(256, 6) combine_kernel(const Args a)
 {
     using V = Vec<T, VB>;
     dependent_release();
@@ -253,7 +316,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const Args a)
 // DW: dweights wanted (rows is read).  blockDim.x threads of one token sum
 // their products over the row, then over lanes and warps in a fixed order.
 template <class T, int VB, bool DW>
-__global__ void __launch_bounds__(256) combine_grad_kernel(const Args a)
+__global__ void __launch_bounds__(256, 5) combine_grad_kernel(const Args a)
 {
     using V = Vec<T, VB>;
     __shared__ float part[8][kGroup];  // one row per warp of the block
@@ -447,8 +510,7 @@ int sgemm_experts_sort(int T, int k, int E, const int *ids, int *offsets, int *s
     const int smem = (ex::kSortWarps + 2) * (E + 1) * static_cast<int>(sizeof(int));
     if (!smem_attr_once(reinterpret_cast<const void *>(ex::sort_kernel), smem))
         return SGEMM_ERR_LAUNCH;
-    // one CTA walks up to 4096 choices in four steps per warp and walk
-    const unsigned ncta = S <= 4096 ? 1u : static_cast<unsigned>(ex::kMaxCluster);
+    const unsigned ncta = ex::sort_cluster(S);
     return launch_dependent(ex::sort_kernel, dim3(ncta), dim3(ex::kSortThreads),
                             static_cast<size_t>(smem), ncta, static_cast<cudaStream_t>(stream),
                             ids, S, E, offsets, slots, positions);

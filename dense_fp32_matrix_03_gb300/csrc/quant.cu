@@ -75,8 +75,29 @@ __device__ __forceinline__ void load_values(const Args &a, const char *row, int 
     }
 }
 
+// A vector of values kept until the maximum is known: as loaded, or, gated,
+// as computed.
+template <class T, int VB, bool GATED>
+struct Held {
+    Vec<T, VB> v;
+    __device__ __forceinline__ void load(const Args &, const char *row, int i)
+    {
+        v.load(row + static_cast<long long>(i) * VB);
+    }
+    __device__ __forceinline__ float get(int i) const { return v.get(i); }
+};
+template <class T, int VB>
+struct Held<T, VB, true> {
+    float f[Vec<T, VB>::N];
+    __device__ __forceinline__ void load(const Args &a, const char *row, int i)
+    {
+        load_values<T, VB, true>(a, row, i, f);
+    }
+    __device__ __forceinline__ float get(int i) const { return f[i]; }
+};
+
 template <class T, int VB, bool GATED, bool EXPERT, bool QV>
-__global__ void __launch_bounds__(256) quantize_kernel(const Args a)
+__global__ void __launch_bounds__(256, GATED ? 3 : 5) quantize_kernel(const Args a)
 {
     constexpr int EV = Vec<T, VB>::N;
     __shared__ unsigned part[8];
@@ -88,19 +109,19 @@ __global__ void __launch_bounds__(256) quantize_kernel(const Args a)
     const int tx = threadIdx.x, nx = blockDim.x, warps = nx >> 5;
     const int nvec = live ? a.nvec : 0;
 
-    float f[kHeld][EV];
+    Held<T, VB, GATED> held[kHeld];
     unsigned big = 0;
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
         const int v = tx + h * nx;
-        if (v < nvec) load_values<T, VB, GATED>(a, row, v, f[h]);
+        if (v < nvec) held[h].load(a, row, v);
     }
 #pragma unroll
     for (int h = 0; h < kHeld; ++h)
         if (tx + h * nx < nvec)
 #pragma unroll
             for (int i = 0; i < EV; ++i)
-                big = max(big, __float_as_uint(f[h][i]) & 0x7FFFFFFFu);
+                big = max(big, __float_as_uint(held[h].get(i)) & 0x7FFFFFFFu);
     for (int v = tx + kHeld * nx; v < nvec; v += nx) {
         float g[EV];
         load_values<T, VB, GATED>(a, row, v, g);
@@ -145,8 +166,11 @@ __global__ void __launch_bounds__(256) quantize_kernel(const Args a)
     for (int h = 0; h < kHeld; ++h) {
         const int v = tx + h * nx;
         if (v < nvec) {
+            float f[EV];
             int c[EV];
-            codes(f[h], c);
+#pragma unroll
+            for (int i = 0; i < EV; ++i) f[i] = held[h].get(i);
+            codes(f, c);
             put(v, c);
         }
     }
