@@ -105,6 +105,16 @@ struct Cfg {
     static constexpr int OFF_TABLE = OFF_BAR + NBAR * 8 + 16;
     static constexpr int SMEM = OFF_TABLE + (kMaxExperts + 1) * 4 + 1024;
     static_assert(NTC == 128, "eight token groups of 16 per converter thread");
+    // A converter set waits at its own steps only, every other one, and a wait
+    // on a phase's parity is sound only if the phase before has completed.
+    // Step n's slot: the set saw the MMAs of step n - 2 - SLOTS done, so those
+    // of n - 2 * SLOTS, the phase before, are.  Step n's stage of a ring of R:
+    // with R even, step n - R was the set's own; else the slot's wait, taken
+    // first, says that the MMAs of step n - SLOTS are done, so step n - R has
+    // been loaded and used if R >= SLOTS.
+    static_assert(kSets == 2 && SLOTS >= 2 && (WRING % 2 == 0 || WRING >= SLOTS) &&
+                      (TRING % 2 == 0 || TRING >= SLOTS),
+                  "no parity wait may be two phases ahead");
     static_assert(ACCS * NT <= static_cast<int>(kACols), "accumulator columns");
     static_assert(SLOTS * kSlotCols + kACols <= 512, "tensor-memory columns");
     static_assert(NT * kCh * 4 <= SLOTS * BSLOT || CG == 2, "partial sums fit the token slots");
@@ -219,23 +229,69 @@ __device__ __forceinline__ void store_transposed(uint32_t addr, const uint32_t (
                  "r"(m[0]), "r"(m[1]), "r"(m[2]), "r"(m[3])
                  : "memory");
 }
-// D (+)= A[tensor memory] * B[shared memory]^T, kind::f16.
+// One slot's MMAs (kind::f16): d (+)= A[tensor memory] * B[shared memory]^T,
+// eight steps of k = 16: A's columns a + 8 i, B's descriptors b0 + 2 i in the
+// slot's first box (b1 in its second).  The first overwrites d unless acc.
+// In the same block it tests, without blocking, whether the barrier at shared
+// address nbar (the next slot's) has completed the phase of parity npar, and
+// returns that: the tensor pipe's queue holds little more than the MMA in
+// flight, so a wait after the issue would leave it idle (measured before:
+// 1330 clocks a slot for 48 tokens, of which the MMAs' own time is 200).
 template <int CG>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t acc)
+__device__ __forceinline__ uint32_t issue_slot(uint32_t d, uint32_t a, uint64_t b0, uint64_t b1,
+                                               uint32_t idesc, uint32_t acc, uint32_t nbar,
+                                               uint32_t npar)
 {
+    uint32_t ready;
     if constexpr (CG == 2)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-            "r"(a), "l"(b), "r"(idesc), "r"(acc)
+            "{\n\t.reg .pred q, p0, p1;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
+            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 q, [%5], %6;\n\t"
+            "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 p1, %4, %4;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%1], [%2], %3, %7, p0;\n\t"
+            "add.u32 a, %2, 8;\n\tadd.s64 b, %3, 2;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "add.u32 a, %2, 16;\n\tadd.s64 b, %3, 4;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "add.u32 a, %2, 24;\n\tadd.s64 b, %3, 6;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "add.u32 a, %2, 32;\n\tadd.s64 b, %8, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "add.u32 a, %2, 40;\n\tadd.s64 b, %8, 2;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "add.u32 a, %2, 48;\n\tadd.s64 b, %8, 4;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "add.u32 a, %2, 56;\n\tadd.s64 b, %8, 6;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "selp.u32 %0, 1, 0, q;\n\t}"
+            : "=r"(ready)
+            : "r"(d), "r"(a), "l"(b0), "r"(acc), "r"(nbar), "r"(npar), "r"(idesc), "l"(b1)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-            "r"(a), "l"(b), "r"(idesc), "r"(acc)
+            "{\n\t.reg .pred q, p0, p1;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
+            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 q, [%5], %6;\n\t"
+            "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 p1, %4, %4;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %7, p0;\n\t"
+            "add.u32 a, %2, 8;\n\tadd.s64 b, %3, 2;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "add.u32 a, %2, 16;\n\tadd.s64 b, %3, 4;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "add.u32 a, %2, 24;\n\tadd.s64 b, %3, 6;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "add.u32 a, %2, 32;\n\tadd.s64 b, %8, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "add.u32 a, %2, 40;\n\tadd.s64 b, %8, 2;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "add.u32 a, %2, 48;\n\tadd.s64 b, %8, 4;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "add.u32 a, %2, 56;\n\tadd.s64 b, %8, 6;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "selp.u32 %0, 1, 0, q;\n\t}"
+            : "=r"(ready)
+            : "r"(d), "r"(a), "l"(b0), "r"(acc), "r"(nbar), "r"(npar), "r"(idesc), "l"(b1)
             : "memory");
+    return ready;
 }
 template <int CG>
 __device__ __forceinline__ void commit(uint64_t *bar)
@@ -485,23 +541,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (!wait_cl(&acc_empty[acc.s], acc.ph ^ 1u, ab, kStatusWaitAcc)) break;
                     tc::tc_fence_after();
                     const uint32_t d = tmem + static_cast<uint32_t>(acc.s * C::NT);
+                    uint32_t seen = 0;  // this slot is already known to be ready
                     for (int ks = ks_lo; ks < ks_hi; ++ks) {
-                        if (!wait_cl(&ready[sr.s], sr.ph, ab, kStatusWaitConv)) {
+                        if (!seen && !wait_cl(&ready[sr.s], sr.ph, ab, kStatusWaitConv)) {
                             ok = false;
                             break;
                         }
                         tc::tc_fence_after();
-                        const uint32_t at = tmem + kACols + static_cast<uint32_t>(sr.s) * kSlotCols;
-                        const uint64_t bt = bdesc + static_cast<uint64_t>(sr.s * (C::BSLOT >> 4));
-    #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            mma_ts<CG>(d, at + 8 * kk,
-                                       bt + static_cast<uint64_t>((kk >> 2) * (C::BBOX >> 4) +
-                                                                  2 * (kk & 3)),
-                                       idesc, ks > ks_lo || kk > 0 ? 1u : 0u);
+                        const uint64_t b0 = bdesc + static_cast<uint64_t>(sr.s * (C::BSLOT >> 4));
+                        Ring<C::SLOTS> nx = sr;
+                        nx.next();
+                        seen = issue_slot<CG>(
+                            d, tmem + kACols + static_cast<uint32_t>(sr.s) * kSlotCols, b0,
+                            b0 + static_cast<uint64_t>(C::BBOX >> 4), idesc, ks > ks_lo ? 1u : 0u,
+                            smem_u32(&ready[nx.s]), nx.ph);
+                        if (ks + 1 == ks_hi) seen = 0;
                         any = true;
                         commit<CG>(&slot_empty[sr.s]);
-                        sr.next();
+                        sr = nx;
                     }
                     if (!ok) break;
                     commit<CG>(&acc_full[acc.s]);
@@ -528,8 +585,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int ks = ks_lo; ks < ks_hi; ++ks) {
                 if (turn == 0) {
                     turn = kSets;
-                    if (!warp_wait(&w_full[rr.s], rr.ph, ab, kStatusWaitFull, lane) ||
-                        !warp_wait_cl(&slot_empty[sr.s], sr.ph ^ 1u, ab, kStatusWaitMma)) {
+                    // the slot before the load (Cfg: the order matters)
+                    if (!warp_wait_cl(&slot_empty[sr.s], sr.ph ^ 1u, ab, kStatusWaitMma) ||
+                        !warp_wait(&w_full[rr.s], rr.ph, ab, kStatusWaitFull, lane)) {
                         ok = false;
                         break;
                     }
@@ -576,8 +634,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int ks = ks_lo; ks < ks_hi; ++ks) {
                 if (turn == 0) {
                     turn = kSets;
-                    if (!warp_wait(&t_full[rr.s], rr.ph, ab, kStatusWaitFull, lane) ||
-                        !warp_wait_cl(&slot_empty[sr.s], sr.ph ^ 1u, ab, kStatusWaitMma)) {
+                    // the slot before the load (Cfg: the order matters)
+                    if (!warp_wait_cl(&slot_empty[sr.s], sr.ph ^ 1u, ab, kStatusWaitMma) ||
+                        !warp_wait(&t_full[rr.s], rr.ph, ab, kStatusWaitFull, lane)) {
                         ok = false;
                         break;
                     }
