@@ -310,16 +310,29 @@ __device__ __forceinline__ void arrive_issuer(uint64_t *bar)
     else
         mbar_arrive(bar);
 }
-__device__ __forceinline__ float4 cluster_load4(uint32_t addr, uint32_t rank)
+// The sum of four floats at this CTA's shared address `addr` over the cluster's
+// CTAs, in their order.
+template <int CTAS>
+__device__ __forceinline__ float4 cluster_sum(uint32_t addr)
 {
-    uint32_t a;
-    float4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
+    float4 v[CTAS];
+#pragma unroll
+    for (int r = 0; r < CTAS; ++r) {
+        uint32_t a;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(r));
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w)
+                     : "r"(a)
+                     : "memory");
+    }
+#pragma unroll
+    for (int r = 1; r < CTAS; ++r) {
+        v[0].x += v[r].x;
+        v[0].y += v[r].y;
+        v[0].z += v[r].z;
+        v[0].w += v[r].w;
+    }
+    return v[0];
 }
 
 // Waits (bounded) for the last loads of a ring that stops early, so that none
@@ -820,28 +833,29 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
     if (CG == 1 && split > 1) {
         // ---- partial sums of the cluster's CTAs, added in CTA order; CTA r
-        // takes tokens r, r + split, ...: a warp a token, four channels a lane
+        // takes tokens r, r + split, ...: a warp a token, four channels a lane.
+        // The scales, and then every CTA's part, are asked for together.
         __syncwarp();
-        tcp::cluster_sync();
-        if (cid < tiles && *abort_flag == 0) {
-            const Job j = job<C>(a, table, cid, 0);
-            const int ch = j.ch0 + 4 * lane;
-            float sb[4];
+        const bool some = cid < tiles;
+        Job j{};
+        float sb[4] = {}, sc = 0.f;
+        const int t0 = static_cast<int>(krank) + warp * split;
+        if (some) {
+            j = job<C>(a, table, cid, 0);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                sb[i] = ch + i < a.N ? a.scaleB[static_cast<long long>(j.e) * a.N + ch + i] : 0.f;
-            for (int t = static_cast<int>(krank) + warp * split; t < j.n;
-                 t += split * (C::THREADS / 32)) {
+                if (j.ch0 + 4 * lane + i < a.N)
+                    sb[i] = a.scaleB[static_cast<long long>(j.e) * a.N + j.ch0 + 4 * lane + i];
+            if (t0 < j.n) sc = a.scaleA[j.row0 + t0];
+        }
+        tcp::cluster_sync();
+        if (some && *abort_flag == 0) {
+            const int ch = j.ch0 + 4 * lane;
+            for (int t = t0; t < j.n; t += split * (C::THREADS / 32)) {
                 const uint32_t at = smem_u32(part + t * kCh + 4 * lane);
-                float4 s = cluster_load4(at, 0);
-                for (int r = 1; r < split; ++r) {
-                    const float4 x = cluster_load4(at, static_cast<uint32_t>(r));
-                    s.x += x.x;
-                    s.y += x.y;
-                    s.z += x.z;
-                    s.w += x.w;
-                }
-                const float sc = a.scaleA[j.row0 + t];
+                const float4 s = split == 8 ? cluster_sum<8>(at)
+                                            : split == 4 ? cluster_sum<4>(at) : cluster_sum<2>(at);
+                if (t != t0) sc = a.scaleA[j.row0 + t];
                 const float o[4] = {s.x * sc * sb[0], s.y * sc * sb[1], s.z * sc * sb[2],
                                     s.w * sc * sb[3]};
                 T *cp = static_cast<T *>(a.C) + (j.row0 + t) * a.ldc + ch;
