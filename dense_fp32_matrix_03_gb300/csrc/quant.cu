@@ -17,6 +17,7 @@ namespace qz {
 using rows::Vec;
 
 constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100
+constexpr float kRound = 12582912.f;             // 1.5 * 2^23
 constexpr int kHeld = 4;                         // vectors per thread kept in registers
 
 struct Args {
@@ -33,15 +34,20 @@ struct Args {
     int k, S;
 };
 
-// EV codes as one access of EV bytes where QV says q allows it.
+// The low bytes of EV integers, as one access where QV says q allows it.
 template <int EV, bool QV>
 __device__ __forceinline__ void store_codes(signed char *p, const int (&c)[EV])
 {
     if constexpr (QV && EV >= 2) {
-        uint32_t w[(EV + 3) / 4] = {};
+        uint32_t w[(EV + 3) / 4] = {};  // the low bytes side by side
+        if constexpr (EV >= 4) {
 #pragma unroll
-        for (int i = 0; i < EV; ++i)
-            w[i / 4] |= (static_cast<uint32_t>(c[i]) & 255u) << (8 * (i % 4));
+            for (int i = 0; i < EV / 4; ++i)
+                w[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040),
+                                   __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040), 0x5410);
+        } else {
+            w[0] = __byte_perm(c[0], c[1], 0x0040);
+        }
         if constexpr (EV == 8)
             *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
         else if constexpr (EV == 4)
@@ -141,9 +147,12 @@ __global__ void __launch_bounds__(256, GATED ? 3 : 5) quantize_kernel(const Args
     const float scale = !finite ? __int_as_float(0x7FFFFFFF)
                                 : (some ? __fdiv_rn(amax, 127.f) : 0.f);
 
+    // The nearest integer, ties to even, is in the low bits after 1.5 * 2^23 is
+    // added (a conversion instruction has a quarter of the rate).
     auto codes = [&](const float (&x)[EV], int (&c)[EV]) {
 #pragma unroll
-        for (int i = 0; i < EV; ++i) c[i] = __float2int_rn(x[i] * inv);  // NaN -> 0
+        for (int i = 0; i < EV; ++i)
+            c[i] = finite ? __float_as_int(__fadd_rn(__fmul_rn(x[i], inv), kRound)) : 0;
     };
     auto put = [&](int v, const int (&c)[EV]) {
         if constexpr (EXPERT) {
