@@ -102,10 +102,7 @@ struct Results {
 // A lane holds 16 bytes of each of the warp's channels and tokens, a step is
 // 512 k: every load is 512 contiguous bytes.
 constexpr int kDotK = 512, kDotCh = 4;
-#ifndef I8_DB
-#define I8_DB 7
-#endif
-constexpr int kDotWarps = 4, kDotBlocks = I8_DB;  // of a block, of a multiprocessor
+constexpr int kDotWarps = 4, kDotBlocks = 7;  // of a block, of a multiprocessor
 
 __device__ __forceinline__ int dot16(const uint4 &x, const uint4 &y, int s)
 {

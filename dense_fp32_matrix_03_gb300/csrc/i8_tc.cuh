@@ -120,14 +120,8 @@ struct Cfg {
     static_assert(NT * kCh * 4 <= SLOTS * BSLOT || CG == 2, "partial sums fit the token slots");
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
-#ifndef I8_WIDE
-#define I8_WIDE 2, 256, 3, 3, 3, 8
-#endif
-#ifndef I8_NARROW
-#define I8_NARROW 1, 128, 3, 4, 3, 4
-#endif
-using Narrow = Cfg<I8_NARROW>;
-using Wide = Cfg<I8_WIDE>;
+using Narrow = Cfg<1, 128, 3, 4, 3, 4>;
+using Wide = Cfg<2, 256, 3, 3, 3, 8>;
 
 // Registers per thread after a warpgroup's give or take (HOLD, below).
 constexpr int kRegMisc = 56, kRegConv = 56, kRegEpi = 112;

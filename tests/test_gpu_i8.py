@@ -271,3 +271,74 @@ def test_two_streams_and_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(c, want)
+
+
+@pytest.mark.parametrize("M", [1, 3, 7, 40, 300])
+def test_operands_written_just_before(M):
+    """A product right behind the kernels that write its operands: its early
+    start (set-up and requests into L2 overlap their end) must not see older
+    values."""
+    import torch
+    import dense_fp32_matrix_03_gb300 as lib
+    N, K, rounds = 512, 1024, 12
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(6)
+    xs = torch.randn(rounds, M, K, device="cuda", generator=gen)
+    ws = torch.randn(rounds, N, K, device="cuda", generator=gen)
+    q = torch.zeros(M, K, dtype=torch.int8, device="cuda")
+    wq = torch.zeros(N, K, dtype=torch.int8, device="cuda")
+    s, sw = torch.zeros(M, device="cuda"), torch.zeros(N, device="cuda")
+    c = torch.zeros(rounds, M, N, device="cuda")
+
+    def call(i):
+        lib.check(lib.sgemm_i8_quantize_rows("fp32", "none", N, K, ws[i], K, wq, K, sw))
+        lib.check(lib.sgemm_i8_quantize_rows("fp32", "none", M, K, xs[i], K, q, K, s))
+        lib.check(lib.sgemm_i8("fp32", M, N, K, q, K, s, wq, K, sw, c[i], N))
+
+    for i in range(rounds):  # each alone
+        call(i)
+        torch.cuda.synchronize()
+    want = c.clone()
+    for _ in range(5):
+        c.zero_()
+        for i in range(rounds):
+            call(i)
+        torch.cuda.synchronize()
+        assert torch.equal(c, want)
+
+
+def test_experts_chain_written_just_before():
+    """Sort, dispatch and product in one chain, over and over into the same
+    buffers, as a decoding loop runs them."""
+    import torch
+    import dense_fp32_matrix_03_gb300 as lib
+    T, k, E, N, K, rounds = 24, 3, 8, 256, 512, 20
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(7)
+    ids = torch.randint(-1, E, (rounds, T, k), device="cuda", dtype=torch.int32, generator=gen)
+    xs = torch.randn(rounds, T, K, device="cuda", generator=gen)
+    w = torch.randint(-127, 128, (E, N, K), device="cuda", dtype=torch.int8, generator=gen)
+    sw = torch.rand(E, N, device="cuda", generator=gen)
+    S = T * k
+    i32 = dict(dtype=torch.int32, device="cuda")
+    off, slots, pos = torch.empty(E + 1, **i32), torch.empty(S, **i32), torch.empty(S, **i32)
+    q, s = torch.zeros(S, K, dtype=torch.int8, device="cuda"), torch.zeros(S, device="cuda")
+    y, out = torch.zeros(S, N, device="cuda"), torch.zeros(rounds, T, N, device="cuda")
+    wt = torch.rand(T, k, device="cuda", generator=gen)
+
+    def call(i):
+        lib.check(lib.sgemm_experts_sort(T, k, E, ids[i], off, slots, pos))
+        lib.check(lib.sgemm_experts_dispatch_i8("fp32", T, k, E, K, xs[i], K, pos, off, q, K, s))
+        lib.check(lib.sgemm_i8_experts("fp32", S, N, K, E, off, q, K, s, w, K, N * K, sw, y, N))
+        lib.check(lib.sgemm_experts_combine("fp32", T, k, E, N, y, N, pos, off, wt, out[i], N))
+
+    for i in range(rounds):
+        call(i)
+        torch.cuda.synchronize()
+    want = out.clone()
+    for _ in range(5):
+        out.zero_()
+        for i in range(rounds):
+            call(i)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
