@@ -67,7 +67,6 @@ using tcp::arrive_on;
 using tcp::cta_rank;
 using tcp::drain_cl;
 using tcp::wait_cl;
-using tcp::warp_wait_cl;
 
 constexpr int kCh = 128;     // channels per CTA
 constexpr int kSlotK = 128;  // k per slot
@@ -264,7 +263,7 @@ __device__ __forceinline__ uint32_t issue_slot(uint32_t d, uint32_t a, uint64_t 
     else
         asm volatile(
             "{\n\t.reg .pred q, p0, p1;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
-            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 q, [%5], %6;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 q, [%5], %6;\n\t"
             "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 p1, %4, %4;\n\t"
             "tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %7, p0;\n\t"
             "add.u32 a, %2, 8;\n\tadd.s64 b, %3, 2;\n\t"
@@ -327,6 +326,25 @@ __device__ __forceinline__ float4 cluster_sum(uint32_t addr)
         v[0].w += v[r].w;
     }
     return v[0];
+}
+
+// Bounded waits on barriers that the CTA pair shares (wide) acquire at cluster
+// scope; the narrow configuration's are its own, and acquire at CTA scope.
+template <int CG>
+__device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t parity, const Abort &ab,
+                                          unsigned int code, bool sleep = false)
+{
+    if constexpr (CG == 2)
+        return wait_cl(bar, parity, ab, code, sleep);
+    else
+        return mbar_wait(bar, parity, ab, code, sleep);
+}
+template <int CG>
+__device__ __forceinline__ bool warp_wait_pair(uint64_t *bar, uint32_t parity, const Abort &ab,
+                                               unsigned int code)
+{
+    const bool ok = wait_pair<CG>(bar, parity, ab, code);
+    return __all_sync(0xffffffffu, ok) != 0;
 }
 
 // Waits (bounded) for the last loads of a ring that stops early, so that none
@@ -545,12 +563,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     const Job j = job<C>(a, table, u, half);
                     const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(j.neff >> 3) << 17) |
                                            (static_cast<uint32_t>((kCh * CG) >> 4) << 24);
-                    if (!wait_cl(&acc_empty[acc.s], acc.ph ^ 1u, ab, kStatusWaitAcc)) break;
+                    if (!wait_pair<CG>(&acc_empty[acc.s], acc.ph ^ 1u, ab, kStatusWaitAcc)) break;
                     tc::tc_fence_after();
                     const uint32_t d = tmem + static_cast<uint32_t>(acc.s * C::NT);
                     uint32_t seen = 0;  // this slot is already known to be ready
                     for (int ks = ks_lo; ks < ks_hi; ++ks) {
-                        if (!seen && !wait_cl(&ready[sr.s], sr.ph, ab, kStatusWaitConv)) {
+                        if (!seen && !wait_pair<CG>(&ready[sr.s], sr.ph, ab, kStatusWaitConv)) {
                             ok = false;
                             break;
                         }
@@ -593,7 +611,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (turn == 0) {
                     turn = kSets;
                     // the slot before the load (Cfg: the order matters)
-                    if (!warp_wait_cl(&slot_empty[sr.s], sr.ph ^ 1u, ab, kStatusWaitMma) ||
+                    if (!warp_wait_pair<CG>(&slot_empty[sr.s], sr.ph ^ 1u, ab, kStatusWaitMma) ||
                         !warp_wait(&w_full[rr.s], rr.ph, ab, kStatusWaitFull, lane)) {
                         ok = false;
                         break;
@@ -642,7 +660,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (turn == 0) {
                     turn = kSets;
                     // the slot before the load (Cfg: the order matters)
-                    if (!warp_wait_cl(&slot_empty[sr.s], sr.ph ^ 1u, ab, kStatusWaitMma) ||
+                    if (!warp_wait_pair<CG>(&slot_empty[sr.s], sr.ph ^ 1u, ab, kStatusWaitMma) ||
                         !warp_wait(&t_full[rr.s], rr.ph, ab, kStatusWaitFull, lane)) {
                         ok = false;
                         break;
@@ -717,9 +735,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 __syncwarp();
             }
             int got = 1;
-            if (lane == 0) got = wait_cl(&acc_full[acc.s], acc.ph, ab, kStatusWaitAcc, true);
+            if (lane == 0) got = wait_pair<CG>(&acc_full[acc.s], acc.ph, ab, kStatusWaitAcc, true);
             if (!__shfl_sync(0xffffffffu, got, 0)) break;
-            drain_cl(&acc_full[acc.s], acc.ph, ab.limit);
+            if constexpr (CG == 2)  // (every lane acquires)
+                drain_cl(&acc_full[acc.s], acc.ph, ab.limit);
+            else
+                mbar_drain(&acc_full[acc.s], acc.ph, ab.limit);
             tc::tc_fence_after();
             const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) +
                                 static_cast<uint32_t>(acc.s * C::NT + col0);
