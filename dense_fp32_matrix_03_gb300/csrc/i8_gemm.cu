@@ -141,21 +141,45 @@ int run(const Args &a, cudaStream_t st)
         return launch_dot<T>(a, st);
     const int c_bytes = rows::Width().add(a.C).add(a.ldc * sizeof(T)).bytes();
     const int k_slots = (a.K + kSlotK - 1) / kSlotK;
-    if (a.E == 1 && a.M <= 16) {
-        if (a.M == 1) return launch_dots<T, 1>(a, st);
-        if (a.M == 2) return launch_dots<T, 2>(a, st);
-        if (a.M <= 4) return launch_dots<T, 4>(a, st);
-        return a.M <= 8 ? launch_few<T, 1, 1, 16, 2>(a, st) : launch_few<T, 2, 1, 16, 2>(a, st);
-    }
-    if (a.E > 1 && a.M <= 8LL * a.E) return launch_few<T, 1, 2, 4, 6>(a, st);
     const int pairs = ss_slots(a.num_sms);
+    const bool dense = a.offsets == nullptr;
+
+    // The kernels' times in us, as measured on GB300 (bf16; M x N x K):
+    //   few     a pass over the weights per 16 tokens, from HBM or L2:
+    //           17 .. 32 x 4096 x 4096 9.4, 48 14.2, 24 x 1024 x 1024 3.5
+    //   narrow  5 us and 0.8 a slot of 128 k and wave of tiles (a cluster's CTAs
+    //           share a tile's slots when tiles are few): 24 .. 64 x 4096 x 4096
+    //           11.8 .. 12.7, 256 19.1, 512 26.0, 1024 46, 24 x 1024 x 1024 6.3
+    //   wide    about 0.7 a slot and wave, of tiles four times as large: 256 ..
+    //           1024 x 4096 x 4096 28 .. 30, 2048 53; less when the GPU is full
+    // Narrow and wide differ little per slot, so the count of waves decides.
     const double narrow_tiles = tiles_expected(a, Narrow::NT, kCh);
     const double wide_tiles = tiles_expected(a, Wide::NT, 2 * kCh);
     int split = 1;
     while (split < 8 && narrow_tiles * split * 2 <= a.num_sms && k_slots >= 4 * split) split *= 2;
-    const double narrow_cost = 0.63 / split * ceil(narrow_tiles * split / a.num_sms);
+    const double narrow_waves = ceil(narrow_tiles * split / a.num_sms) / split;
+    if (dense) {
+        if (a.M == 1) return launch_dots<T, 1>(a, st);
+        if (a.M == 2) return launch_dots<T, 2>(a, st);
+        if (a.M <= 4) return launch_dots<T, 4>(a, st);
+        // blocks of 16 warps where all of them run at once, with two steps or
+        // more of k a warp; 8 otherwise (8 / 16 warps: 16 x 4096 x 4096 9.1 /
+        // 6.2, 16 x 8192 x 8192 21.1 / 21.9, 16 x 1024 x 1024 2.6 / 3.4)
+        const bool once = a.K >= 2048 && a.N <= 2LL * a.num_sms * 16;
+        if (a.M <= 8)
+            return once ? launch_few<T, 1, 1, 16, 2>(a, st) : launch_few<T, 1, 1, 8, 4>(a, st);
+        if (a.M <= 16 && once) return launch_few<T, 2, 1, 16, 2>(a, st);
+        const double pass = static_cast<double>(a.N) * a.K / 4.8e6;
+        if (a.M <= 16 || 2.9 + (a.M + 15) / 16 * (pass > 0.3 ? pass : 0.3) <
+                             5. + 0.8 * narrow_waves * k_slots)
+            return launch_few<T, 2, 1, 8, 4>(a, st);
+    } else if (a.M <= 12LL * a.E) {
+        // 32 experts of 2048 x 2048, few / narrow: 12 rows each 40 / 46 us, 16
+        // rows 47.6 / 46.9 (tiles of 16 tokens instead of 8: 42 and 48)
+        return launch_few<T, 1, 2, 4, 6>(a, st);
+    }
     const double wide_cost = (wide_tiles < pairs ? 0.70 : 0.60) * ceil(wide_tiles / pairs);
-    if (wide_cost < narrow_cost) {
+    if (wide_cost < 0.63 * narrow_waves) {
         const long long tiles = max_tiles(a, Wide::NT) * ((a.N + 2 * kCh - 1) / (2 * kCh));
         return launch_tc_i8<Wide, T>(a, tmW, tmT, tiles < pairs ? tiles : pairs, 1, c_bytes, st);
     }
