@@ -60,6 +60,8 @@ __device__ __forceinline__ void ask_weights(const Args &a, int n0, int ch)
     }
 }
 
+__device__ __forceinline__ int log2_of(int x) { return 31 - __clz(x); }
+
 // The results of a block: `groups` runs of CH channels from n0 on, for the
 // tokens of `tl`.  Thread tid makes results tid, tid + threads, ...;
 // neighbours have neighbouring channels.
@@ -67,33 +69,39 @@ template <class T, int CH>
 struct Results {
     const Args &a;
     const Tile &tl;
-    int n0, groups, count;
-    float sa, sb;  // the scales of this thread's first result
-    __device__ __forceinline__ Results(const Args &args, const Tile &tile, int first, int g)
-        : a(args), tl(tile), n0(first), groups(g), count(g * CH * tile.rows), sa(0.f), sb(0.f)
+    int n0, shift, count;  // channels of a token: 1 << shift (CH and groups are powers of two)
+    float sa, sb;          // the scales of this thread's first result
+    __device__ __forceinline__ Results(const Args &args, const Tile &tile, int first, int groups)
+        : a(args), tl(tile), n0(first), shift(log2_of(groups * CH)),
+          count(groups * CH * tile.rows), sa(0.f), sb(0.f)
     {
         const int i = threadIdx.x;
-        if (i < count && channel(i) < a.N) scales(i);
+        if (i < count && channel(i) < a.N) {
+            sa = a.scaleA[tl.row0 + token(i)];
+            sb = a.scaleB[static_cast<long long>(tl.e) * a.N + channel(i)];
+        }
     }
-    __device__ __forceinline__ int token(int i) const { return i / (CH * groups); }
-    __device__ __forceinline__ int group(int i) const { return i / CH % groups; }
-    __device__ __forceinline__ int channel(int i) const { return n0 + i % (CH * groups); }
-    __device__ __forceinline__ void scales(int i)
+    __device__ __forceinline__ int token(int i) const { return i >> shift; }
+    __device__ __forceinline__ int of_token(int i) const { return i & ((1 << shift) - 1); }
+    __device__ __forceinline__ int channel(int i) const { return n0 + of_token(i); }
+    template <class F>
+    __device__ __forceinline__ void put(int i, float x, float y, const F &sum)
     {
-        sa = a.scaleA[tl.row0 + token(i)];
-        sb = a.scaleB[static_cast<long long>(tl.e) * a.N + channel(i)];
+        static_cast<T *>(a.C)[(tl.row0 + token(i)) * a.ldc + channel(i)] =
+            rows::from_f<T>(sum(of_token(i) / CH, token(i), of_token(i) % CH) * x * y);
     }
     // sum(group, token, channel of the group): the unscaled sum
     template <class F>
     __device__ __forceinline__ void store(const F &sum)
     {
-        for (int i = threadIdx.x; i < count; i += blockDim.x) {
-            const int n = channel(i);
-            if (n >= a.N) continue;
-            if (i != static_cast<int>(threadIdx.x)) scales(i);
-            static_cast<T *>(a.C)[(tl.row0 + token(i)) * a.ldc + n] =
-                rows::from_f<T>(sum(group(i), token(i), i % CH) * sa * sb);
-        }
+        const int first = threadIdx.x, step = blockDim.x;
+        if (first < count && channel(first) < a.N) put(first, sa, sb, sum);
+        // (the scales of four results on their way together)
+#pragma unroll 4
+        for (int i = first + step; i < count; i += step)
+            if (channel(i) < a.N)
+                put(i, a.scaleA[tl.row0 + token(i)],
+                    a.scaleB[static_cast<long long>(tl.e) * a.N + channel(i)], sum);
     }
 };
 

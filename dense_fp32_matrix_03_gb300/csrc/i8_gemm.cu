@@ -145,11 +145,13 @@ int run(const Args &a, cudaStream_t st)
     const bool dense = a.offsets == nullptr;
 
     // The kernels' times in us, as measured on GB300 (bf16; M x N x K):
-    //   few     a pass over the weights per 16 tokens, from HBM or L2:
-    //           17 .. 32 x 4096 x 4096 9.4, 48 14.2, 24 x 1024 x 1024 3.5
-    //   narrow  5 us and 0.8 a slot of 128 k and wave of tiles (a cluster's CTAs
-    //           share a tile's slots when tiles are few): 24 .. 64 x 4096 x 4096
-    //           11.8 .. 12.7, 256 19.1, 512 26.0, 1024 46, 24 x 1024 x 1024 6.3
+    //   few     2.9 us and a pass over the weights per 16 tokens, from HBM or
+    //           L2, or the results: 17 .. 32 x 4096 x 4096 9.4, 48 14.2, 100 x
+    //           1024 x 1024 4.1, 64 x 4096 x 128 5.5
+    //   narrow  3.4 us (5 where a cluster's CTAs share a tile's slots, when tiles
+    //           are few) and 0.8 a slot of 128 k and wave of tiles: 24 .. 64 x
+    //           4096 x 4096 11.8 .. 12.7, 256 19.1, 512 26.0, 1024 46, 100 x 1024
+    //           x 1024 8.3, 64 x 4096 x 128 4.2
     //   wide    about 0.7 a slot and wave, of tiles four times as large: 256 ..
     //           1024 x 4096 x 4096 28 .. 30, 2048 53; less when the GPU is full
     // Narrow and wide differ little per slot, so the count of waves decides.
@@ -169,13 +171,14 @@ int run(const Args &a, cudaStream_t st)
         if (a.M <= 8)
             return once ? launch_few<T, 1, 1, 16, 2>(a, st) : launch_few<T, 1, 1, 8, 4>(a, st);
         if (a.M <= 16 && once) return launch_few<T, 2, 1, 16, 2>(a, st);
-        const double pass = static_cast<double>(a.N) * a.K / 4.8e6;
-        if (a.M <= 16 || 2.9 + (a.M + 15) / 16 * (pass > 0.3 ? pass : 0.3) <
-                             5. + 0.8 * narrow_waves * k_slots)
+        const double passes = (a.M + 15) / 16 * (static_cast<double>(a.N) * a.K / 4.8e6);
+        const double stores = static_cast<double>(a.M) * a.N / 7.5e4;
+        if (a.M <= 16 || 2.9 + (passes > stores ? passes : stores) <
+                             (split > 1 ? 5. : 3.4) + 0.8 * narrow_waves * k_slots)
             return launch_few<T, 2, 1, 8, 4>(a, st);
-    } else if (a.M <= 12LL * a.E) {
-        // 32 experts of 2048 x 2048, few / narrow: 12 rows each 40 / 46 us, 16
-        // rows 47.6 / 46.9 (tiles of 16 tokens instead of 8: 42 and 48)
+    } else if (a.M <= 16LL * a.E) {
+        // 32 experts of 2048 x 2048, few / narrow: 8 rows each 30 / 46 us, 12
+        // rows 36 / 46 us, 16 rows 43 / 47
         return launch_few<T, 1, 2, 4, 6>(a, st);
     }
     const double wide_cost = (wide_tiles < pairs ? 0.70 : 0.60) * ceil(wide_tiles / pairs);
