@@ -223,66 +223,85 @@ __device__ __forceinline__ void store_transposed(uint32_t addr, const uint32_t (
                  : "memory");
 }
 // One slot's MMAs (kind::f16): d (+)= A[tensor memory] * B[shared memory]^T,
-// eight steps of k = 16: A's columns a + 8 i, B's descriptors b0 + 2 i in the
-// slot's first box (b1 in its second).  The first overwrites d unless acc.
-// In the same block it tests, without blocking, whether the barrier at shared
-// address nbar (the next slot's) has completed the phase of parity npar, and
-// returns that: the tensor pipe's queue holds little more than the MMA in
-// flight, so a wait after the issue would leave it idle (measured before:
-// 1330 clocks a slot for 48 tokens, of which the MMAs' own time is 200).
+// eight steps of k = 16: A's columns a + 8 i; B's descriptors {b0 + 2 i, hi} in
+// the slot's first box, {b1 + 2 i, hi} in its second.  In two parts: the tensor
+// pipe's queue holds little more than the MMA in flight, so whatever the
+// issuing thread has to work out for the next slot belongs between the parts,
+// not after them.  The first MMA overwrites d unless acc.
 template <int CG>
-__device__ __forceinline__ uint32_t issue_slot(uint32_t d, uint32_t a, uint64_t b0, uint64_t b1,
-                                               uint32_t idesc, uint32_t acc, uint32_t nbar,
-                                               uint32_t npar)
+__device__ __forceinline__ void issue_first(uint32_t d, uint32_t a, uint32_t b0, uint32_t b1,
+                                            uint32_t hi, uint32_t idesc, uint32_t acc)
+{
+    if constexpr (CG == 2)
+        asm volatile(
+            "{\n\t.reg .pred p0, p1;\n\t.reg .b64 b;\n\t.reg .b32 a, l;\n\t"
+            "setp.ne.b32 p0, %5, 0;\n\tsetp.eq.b32 p1, %5, %5;\n\t"
+            "add.u32 a, %1, 0;\n\tadd.u32 l, %2, 0;\n\tmov.b64 b, {l, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %4, p0;\n\t"
+            "add.u32 a, %1, 8;\n\tadd.u32 l, %2, 2;\n\tmov.b64 b, {l, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %4, p1;\n\t"
+            "add.u32 a, %1, 16;\n\tadd.u32 l, %2, 4;\n\tmov.b64 b, {l, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %4, p1;\n\t"
+            "add.u32 a, %1, 24;\n\tadd.u32 l, %2, 6;\n\tmov.b64 b, {l, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %4, p1;\n\t"
+            "add.u32 a, %1, 32;\n\tadd.u32 l, %6, 0;\n\tmov.b64 b, {l, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %4, p1;\n\t"
+            "add.u32 a, %1, 40;\n\tadd.u32 l, %6, 2;\n\tmov.b64 b, {l, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %4, p1;\n\t"
+            "}" ::"r"(d), "r"(a), "r"(b0), "r"(hi), "r"(idesc), "r"(acc), "r"(b1)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p0, p1;\n\t.reg .b64 b;\n\t.reg .b32 a, l;\n\t"
+            "setp.ne.b32 p0, %5, 0;\n\tsetp.eq.b32 p1, %5, %5;\n\t"
+            "add.u32 a, %1, 0;\n\tadd.u32 l, %2, 0;\n\tmov.b64 b, {l, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, p0;\n\t"
+            "add.u32 a, %1, 8;\n\tadd.u32 l, %2, 2;\n\tmov.b64 b, {l, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, p1;\n\t"
+            "add.u32 a, %1, 16;\n\tadd.u32 l, %2, 4;\n\tmov.b64 b, {l, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, p1;\n\t"
+            "add.u32 a, %1, 24;\n\tadd.u32 l, %2, 6;\n\tmov.b64 b, {l, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, p1;\n\t"
+            "add.u32 a, %1, 32;\n\tadd.u32 l, %6, 0;\n\tmov.b64 b, {l, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, p1;\n\t"
+            "add.u32 a, %1, 40;\n\tadd.u32 l, %6, 2;\n\tmov.b64 b, {l, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, p1;\n\t"
+            "}" ::"r"(d), "r"(a), "r"(b0), "r"(hi), "r"(idesc), "r"(acc), "r"(b1)
+            : "memory");
+}
+// The last two, after a test, without blocking, of whether the barrier at
+// shared address nbar (the next slot's) has completed the phase of parity
+// npar; returns that.
+template <int CG>
+__device__ __forceinline__ uint32_t issue_last(uint32_t d, uint32_t a, uint32_t b1, uint32_t hi,
+                                               uint32_t idesc, uint32_t nbar, uint32_t npar)
 {
     uint32_t ready;
     if constexpr (CG == 2)
         asm volatile(
-            "{\n\t.reg .pred q, p0, p1;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
-            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 q, [%5], %6;\n\t"
-            "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 p1, %4, %4;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%1], [%2], %3, %7, p0;\n\t"
-            "add.u32 a, %2, 8;\n\tadd.s64 b, %3, 2;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %7, p1;\n\t"
-            "add.u32 a, %2, 16;\n\tadd.s64 b, %3, 4;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %7, p1;\n\t"
-            "add.u32 a, %2, 24;\n\tadd.s64 b, %3, 6;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %7, p1;\n\t"
-            "add.u32 a, %2, 32;\n\tadd.s64 b, %8, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %7, p1;\n\t"
-            "add.u32 a, %2, 40;\n\tadd.s64 b, %8, 2;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %7, p1;\n\t"
-            "add.u32 a, %2, 48;\n\tadd.s64 b, %8, 4;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %7, p1;\n\t"
-            "add.u32 a, %2, 56;\n\tadd.s64 b, %8, 6;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "{\n\t.reg .pred q, p1;\n\t.reg .b64 b;\n\t.reg .b32 a, l;\n\t"
+            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 q, [%6], %7;\n\t"
+            "setp.eq.b32 p1, %5, %5;\n\t"
+            "add.u32 a, %2, 48;\n\tadd.u32 l, %3, 4;\n\tmov.b64 b, {l, %4};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %5, p1;\n\t"
+            "add.u32 a, %2, 56;\n\tadd.u32 l, %3, 6;\n\tmov.b64 b, {l, %4};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%1], [a], b, %5, p1;\n\t"
             "selp.u32 %0, 1, 0, q;\n\t}"
             : "=r"(ready)
-            : "r"(d), "r"(a), "l"(b0), "r"(acc), "r"(nbar), "r"(npar), "r"(idesc), "l"(b1)
+            : "r"(d), "r"(a), "r"(b1), "r"(hi), "r"(idesc), "r"(nbar), "r"(npar)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred q, p0, p1;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
-            "mbarrier.test_wait.parity.shared::cta.b64 q, [%5], %6;\n\t"
-            "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 p1, %4, %4;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %7, p0;\n\t"
-            "add.u32 a, %2, 8;\n\tadd.s64 b, %3, 2;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %7, p1;\n\t"
-            "add.u32 a, %2, 16;\n\tadd.s64 b, %3, 4;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %7, p1;\n\t"
-            "add.u32 a, %2, 24;\n\tadd.s64 b, %3, 6;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %7, p1;\n\t"
-            "add.u32 a, %2, 32;\n\tadd.s64 b, %8, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %7, p1;\n\t"
-            "add.u32 a, %2, 40;\n\tadd.s64 b, %8, 2;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %7, p1;\n\t"
-            "add.u32 a, %2, 48;\n\tadd.s64 b, %8, 4;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %7, p1;\n\t"
-            "add.u32 a, %2, 56;\n\tadd.s64 b, %8, 6;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %7, p1;\n\t"
+            "{\n\t.reg .pred q, p1;\n\t.reg .b64 b;\n\t.reg .b32 a, l;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 q, [%6], %7;\n\t"
+            "setp.eq.b32 p1, %5, %5;\n\t"
+            "add.u32 a, %2, 48;\n\tadd.u32 l, %3, 4;\n\tmov.b64 b, {l, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %5, p1;\n\t"
+            "add.u32 a, %2, 56;\n\tadd.u32 l, %3, 6;\n\tmov.b64 b, {l, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%1], [a], b, %5, p1;\n\t"
             "selp.u32 %0, 1, 0, q;\n\t}"
             : "=r"(ready)
-            : "r"(d), "r"(a), "l"(b0), "r"(acc), "r"(nbar), "r"(npar), "r"(idesc), "l"(b1)
+            : "r"(d), "r"(a), "r"(b1), "r"(hi), "r"(idesc), "r"(nbar), "r"(npar)
             : "memory");
     return ready;
 }
@@ -559,6 +578,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 Ring<C::ACCS> acc;
                 bool ok = true, any = false;
                 const uint64_t bdesc = tc::kmajor_sw128_desc(smem_u32(base + C::OFF_B));
+                const uint32_t blo = static_cast<uint32_t>(bdesc),
+                               bhi = static_cast<uint32_t>(bdesc >> 32);
                 for (int u = cid; ok && u < tiles; u += ncl) {
                     const Job j = job<C>(a, table, u, half);
                     const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(j.neff >> 3) << 17) |
@@ -573,13 +594,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             break;
                         }
                         tc::tc_fence_after();
-                        const uint64_t b0 = bdesc + static_cast<uint64_t>(sr.s * (C::BSLOT >> 4));
+                        const uint32_t at = tmem + kACols + static_cast<uint32_t>(sr.s) * kSlotCols;
+                        const uint32_t b0 =
+                            blo + static_cast<uint32_t>(sr.s) * (C::BSLOT >> 4);
+                        issue_first<CG>(d, at, b0, b0 + (C::BBOX >> 4), bhi, idesc,
+                                        ks > ks_lo ? 1u : 0u);
                         Ring<C::SLOTS> nx = sr;
                         nx.next();
-                        seen = issue_slot<CG>(
-                            d, tmem + kACols + static_cast<uint32_t>(sr.s) * kSlotCols, b0,
-                            b0 + static_cast<uint64_t>(C::BBOX >> 4), idesc, ks > ks_lo ? 1u : 0u,
-                            smem_u32(&ready[nx.s]), nx.ph);
+                        seen = issue_last<CG>(d, at, b0 + (C::BBOX >> 4), bhi, idesc,
+                                              smem_u32(&ready[nx.s]), nx.ph);
                         if (ks + 1 == ks_hi) seen = 0;
                         any = true;
                         commit<CG>(&slot_empty[sr.s]);
