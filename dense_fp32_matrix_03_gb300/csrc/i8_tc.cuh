@@ -51,6 +51,9 @@
 // Every wait is bounded.
 #pragma once
 
+#include <type_traits>
+
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "../../include/sgemm.h"
@@ -198,20 +201,29 @@ __device__ __forceinline__ void tmem_wait_ld()
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+// Two values rounded to 16 bits, the first in the low half.
 template <class T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+__device__ __forceinline__ uint32_t pack2(float2 v)
 {
     if constexpr (sizeof(T) == 4) {
         return 0u;  // fp32 results are never packed
+    } else if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(v.x, v.y);
+        return *reinterpret_cast<const uint32_t *>(&h);
     } else {
-        union {
-            T h[2];
-            uint32_t u;
-        } x;
-        x.h[0] = rows::from_f<T>(lo);
-        x.h[1] = rows::from_f<T>(hi);
-        return x.u;
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+        return *reinterpret_cast<const uint32_t *>(&h);
     }
+}
+// Both products at once.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 // Four 8 x 8 matrices of 16-bit values, each transposed into rows of 16
 // bytes: lane l gives the address of row l % 8 of matrix l / 8.
@@ -782,8 +794,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         m[4 * t + i] = pack2<T>(
-                            __uint_as_float(v[i >> 1][4 * t + 2 * (i & 1)]) * s.x * sb[i],
-                            __uint_as_float(v[i >> 1][4 * t + 2 * (i & 1) + 1]) * s.y * sb[i]);
+                            mul2(mul2(make_float2(
+                                          __uint_as_float(v[i >> 1][4 * t + 2 * (i & 1)]),
+                                          __uint_as_float(v[i >> 1][4 * t + 2 * (i & 1) + 1])),
+                                      s),
+                                 make_float2(sb[i], sb[i])));
                 }
             };
             auto store_chunk = [&](int c0, const uint32_t (&m)[16]) {
