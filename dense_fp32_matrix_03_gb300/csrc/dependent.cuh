@@ -54,4 +54,16 @@ int launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, uns
     return SGEMM_OK;
 }
 
+// What a C entry point returns: f()'s status; nothing that the host side may
+// throw (allocation, locks) leaves it.
+template <class F>
+int c_entry(const F &f) noexcept
+{
+    try {
+        return f();
+    } catch (...) {
+        return SGEMM_ERR_LAUNCH;
+    }
+}
+
 }  // namespace sg

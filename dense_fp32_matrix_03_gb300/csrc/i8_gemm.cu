@@ -173,8 +173,11 @@ int run(const Args &a, cudaStream_t st)
         if (a.M <= 16 && once) return launch_few<T, 2, 1, 16, 2>(a, st);
         const double passes = (a.M + 15) / 16 * (static_cast<double>(a.N) * a.K / 4.8e6);
         const double stores = static_cast<double>(a.M) * a.N / 7.5e4;
-        if (a.M <= 16 || 2.9 + (passes > stores ? passes : stores) <
-                             (split > 1 ? 5. : 3.4) + 0.8 * narrow_waves * k_slots)
+        // (a grid holds 65535 token tiles)
+        if (a.M <= 16 ||
+            (a.M <= 16 * 65535 &&
+             2.9 + (passes > stores ? passes : stores) <
+                             (split > 1 ? 5. : 3.4) + 0.8 * narrow_waves * k_slots))
             return launch_few<T, 2, 1, 8, 4>(a, st);
     } else if (a.M <= 16LL * a.E) {
         // 32 experts of 2048 x 2048, few / narrow: 8 rows each 30 / 46 us, 12
@@ -236,8 +239,10 @@ extern "C" {
 int sgemm_i8(int type, int M, int N, int K, const signed char *A, int lda, const float *scaleA,
              const signed char *B, int ldb, const float *scaleB, void *C, int ldc, void *stream)
 {
-    return sg::i8::product(type, M, N, K, 1, nullptr, A, lda, scaleA, B, ldb, 0, scaleB, C, ldc,
-                           stream);
+    return sg::c_entry([&]() -> int {
+        return sg::i8::product(type, M, N, K, 1, nullptr, A, lda, scaleA, B, ldb, 0, scaleB, C, ldc,
+                               stream);
+    });
 }
 
 int sgemm_i8_experts(int type, int M, int N, int K, int E, const int *offsets,
@@ -245,12 +250,14 @@ int sgemm_i8_experts(int type, int M, int N, int K, int E, const int *offsets,
                      int ldb, long long strideB, const float *scaleB, void *C, int ldc,
                      void *stream)
 {
-    if (E < 1 || E > sg::i8::kMaxExperts || offsets == nullptr ||
-        !sg::rows::aligned_to(offsets, 4) || strideB < 0 ||
-        (E > 1 && N > 0 && strideB < (N - 1LL) * ldb + K))
-        return SGEMM_ERR_INVALID_ARG;
-    return sg::i8::product(type, M, N, K, E, offsets, A, lda, scaleA, B, ldb, strideB, scaleB, C,
-                           ldc, stream);
+    return sg::c_entry([&]() -> int {
+        if (E < 1 || E > sg::i8::kMaxExperts || offsets == nullptr ||
+            !sg::rows::aligned_to(offsets, 4) || strideB < 0 ||
+            (E > 1 && N > 0 && strideB < (N - 1LL) * ldb + K))
+            return SGEMM_ERR_INVALID_ARG;
+        return sg::i8::product(type, M, N, K, E, offsets, A, lda, scaleA, B, ldb, strideB, scaleB, C,
+                               ldc, stream);
+    });
 }
 
 }  // extern "C"

@@ -29,10 +29,8 @@
 //   B warps    16 bytes at a time -> 32 bytes of fp16 in shared memory
 //   MMA        one thread: 8 MMAs of k = 16
 //   epilogue   tensor memory -> scales -> result type -> staging -> C
-// A and B warps come in two sets that take alternate slots: a slot's chain of
-// waits, loads, stores and fences is about 1100 clocks long (with one set the
-// weights of a decoding step came at 4.0 TB/s and a 256 x 256 tile's slot took
-// 2490 clocks).
+// A and B warps come in two sets that take alternate slots: widening a slot
+// takes a set 550 (A) to 1000 (B, 128 tokens) clocks besides its waits.
 // The order of k inside a slot is permuted (the first eight values of every
 // 16-byte piece, then the second eight), the same way for both operands: a
 // token's 16-byte piece then becomes one 16-byte piece of each of the slot's
@@ -49,6 +47,17 @@
 //   wide    a CTA pair (cta_group::2), 256 channels x up to 256 tokens, each
 //           CTA widening its 128 channels and half the tokens.
 // Every wait is bounded.
+//
+// Measured on GB300, bf16 results: 8192 x 8192 x 8192 621 us (1772 TFLOP/s,
+// 0.93 of the measured 16-bit peak, above its sustained rate), x 4096 319 us,
+// x 1024 106 us; 32 experts of 4096 x 2048 over 32768 rows, unevenly, 368 us.
+// What bounds the wide form: the MMAs' 1024 clocks a slot stretch to about 1220
+// beside the converters (without them: 1000 to 1050), and a tile's end leaves
+// the tensor pipe idle for about 1850 clocks, while the accumulator is read.
+// What bounds the narrow form for few tokens: a slot takes one thread about
+// 1100 clocks to issue (eight MMAs cost at least 45 clocks each whatever their
+// N), so weights pass at 2.4 (8192 x 8192, 20 to 64 tokens: 27 us) to 3.2 TB/s;
+// i8_few.cuh takes over where it is faster.
 #pragma once
 
 #include <type_traits>
@@ -497,7 +506,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     dependent_release();
     if (a.offsets == nullptr && warp == 3 && lane == 0) {
         const int ch0 = (cid / ((a.M + C::NT - 1) / C::NT) * CG + static_cast<int>(half)) * kCh;
-        for (int ks = ks_lo; ks < ks_hi && ks < ks_lo + 16; ++ks)
+        for (int ks = ks_lo; ch0 < a.N && ks < ks_hi && ks < ks_lo + 16; ++ks)
             tma_prefetch_3d(&tmW, ks * kSlotK, ch0, 0);
     }
     dependent_wait();

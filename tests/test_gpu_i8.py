@@ -92,6 +92,13 @@ def test_dense_shapes(type_, M, N, K):
     run_dense(type_, M, N, K)
 
 
+@pytest.mark.parametrize("M,N,K", [(70000, 1, 16), (1100000, 3, 32), (3, 70000, 16), (600, 40000, 48)])
+def test_dense_lopsided(M, N, K):
+    """Many tokens for few channels and the other way: grids near and past
+    their limits."""
+    run_dense("fp32", M, N, K)
+
+
 @pytest.mark.parametrize("how", ["tight", "plus4"])
 @pytest.mark.parametrize("M,N,K", [(1, 100, 333), (70, 130, 65), (130, 300, 777), (5, 64, 4)])
 def test_dense_rows_off_16_bytes(how, M, N, K):
