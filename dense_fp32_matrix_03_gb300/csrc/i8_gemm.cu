@@ -1,6 +1,7 @@
 // i8_gemm.cu -- products of 8-bit integers with a scale for each token and
 // channel (include/int8_gemm.h): argument checks, the choice of the kernel
 // and the integer dot-product kernel (the tensor-core one is i8_tc.cuh).
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -128,6 +129,40 @@ double tiles_expected(const Args &a, int nt, int ch)
     return used * (each > 1. ? each : 1.) * cts;
 }
 
+// Clusters of `size` CTAs of the narrow kernel that the GPU runs at once (a
+// cluster stays within a processor group, so 152 multiprocessors hold fewer
+// than 19 of 8): cached per device.
+int narrow_room(int size, int num_sms)
+{
+    static std::atomic<int> room[64][4];  // sizes 1, 2, 4, 8; 0: not asked yet
+    const int i = size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : 3;
+    int dev = 0;
+    if (size == 1) return num_sms;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms / size / 2;
+    int n = room[dev][i].load();
+    if (n == 0) {
+        auto kern = i8_kernel<Narrow, float>;
+        if (smem_attr_once(reinterpret_cast<const void *>(kern), Narrow::SMEM)) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(static_cast<unsigned>(num_sms / size * size));
+            cfg.blockDim = dim3(Narrow::THREADS);
+            cfg.dynamicSmemBytes = Narrow::SMEM;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+        }
+        cudaGetLastError();
+        if (n < 1) n = 1;
+        room[dev][i].store(n);
+    }
+    return n;
+}
+
 template <class T>
 int run(const Args &a, cudaStream_t st)
 {
@@ -158,7 +193,8 @@ int run(const Args &a, cudaStream_t st)
     const double narrow_tiles = tiles_expected(a, Narrow::NT, kCh);
     const double wide_tiles = tiles_expected(a, Wide::NT, 2 * kCh);
     int split = 1;
-    while (split < 8 && narrow_tiles * split * 2 <= a.num_sms && k_slots >= 4 * split) split *= 2;
+    while (split < 8 && narrow_tiles <= narrow_room(2 * split, a.num_sms) && k_slots >= 4 * split)
+        split *= 2;
     const double narrow_waves = ceil(narrow_tiles * split / a.num_sms) / split;
     if (dense) {
         if (a.M == 1) return launch_dots<T, 1>(a, st);

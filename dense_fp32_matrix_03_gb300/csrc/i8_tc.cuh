@@ -819,33 +819,61 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 __syncwarp();
                 T *out = crow + static_cast<long long>(c0) * a.ldc;
+                // (addresses by additions: computed for each row they cost more
+                // than the stores)
+                const int rows_left = n - c0;
                 if (c_bytes == 16 && chq + 32 <= a.N) {
+                    const int r = lane >> 2, p = lane & 3;
+                    const uint32_t at = stage + r * 64 + ((p ^ ((r >> 1) & 3)) << 4);
+                    T *to = out + r * a.ldc + 8 * p;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int r = 8 * i + (lane >> 2), p = lane & 3;
-                        const uint4 x = lds128(stage + r * 64 + ((p ^ ((r >> 1) & 3)) << 4));
-                        if (c0 + r < n) *reinterpret_cast<uint4 *>(out + r * a.ldc + 8 * p) = x;
+                        const uint4 x = lds128(at + i * 512);
+                        if (8 * i + r < rows_left) *reinterpret_cast<uint4 *>(to) = x;
+                        to += 8 * a.ldc;
                     }
                 } else if (c_bytes >= 8 && chq + 32 <= a.N) {
+                    const int r = lane >> 3, p = lane & 7;
+                    T *to = out + r * a.ldc + 4 * p;
+                    uint32_t at[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        at[i] = stage + r * 64 +
+                                (((p >> 1) ^ ((2 * i + (r >> 1)) & 3)) << 4) + 8 * (p & 1);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int r = 4 * i + (lane >> 3), p = lane & 7;
                         uint2 x;
                         asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
                                      : "=r"(x.x), "=r"(x.y)
-                                     : "r"(stage + r * 64 + (((p >> 1) ^ ((r >> 1) & 3)) << 4) +
-                                           8 * (p & 1)));
-                        if (c0 + r < n) *reinterpret_cast<uint2 *>(out + r * a.ldc + 4 * p) = x;
+                                     : "r"(at[i & 1] + i * 256));
+                        if (4 * i + r < rows_left) *reinterpret_cast<uint2 *>(to) = x;
+                        to += 4 * a.ldc;
                     }
-                } else {  // a token's row at a time
-                    for (int r = 0; r < 32 && c0 + r < n; ++r) {
-                        uint16_t x;
-                        asm volatile("ld.shared.u16 %0, [%1];"
-                                     : "=h"(x)
-                                     : "r"(stage + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) +
-                                           2 * (lane & 7)));
-                        if (chq + lane < a.N)
-                            *reinterpret_cast<uint16_t *>(out + r * a.ldc + lane) = x;
+                } else {
+                    // off 8-byte boundaries, or past the last channel: a value a
+                    // lane, a token's row at a time; addresses by additions, eight
+                    // rows' loads together (a computed address per row made a
+                    // chunk 2000 clocks)
+                    uint32_t at[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        at[i] = stage + (((lane >> 3) ^ i) << 4) + 2 * (lane & 7);
+                    const bool mine = chq + lane < a.N;
+                    T *row = out + lane;
+#pragma unroll
+                    for (int r0 = 0; r0 < 32; r0 += 8) {
+                        uint16_t x[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            asm volatile("ld.shared.u16 %0, [%1];"
+                                         : "=h"(x[i])
+                                         : "r"(at[((r0 + i) >> 1) & 3] + (r0 + i) * 64));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (mine && r0 + i < rows_left)
+                                *reinterpret_cast<uint16_t *>(row) = x[i];
+                            row += a.ldc;
+                        }
                     }
                 }
             };
@@ -879,11 +907,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     for (int i = 0; i < 32; ++i)
                         part[(col0 + c0 + i) * kCh + q * 32 + lane] = v[i];
                 } else if (chq + lane < a.N) {
+                    T *row = crow + static_cast<long long>(c0) * a.ldc + lane;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (c0 + i < n)
-                            crow[(c0 + i) * a.ldc + lane] =
-                                rows::from_f<T>(v[i] * sa[c0 + i] * sb[0]);
+                    for (int i = 0; i < 32; ++i) {
+                        if (c0 + i < n) *row = rows::from_f<T>(v[i] * sa[c0 + i] * sb[0]);
+                        row += a.ldc;
+                    }
                 }
             }
             tc::tc_fence_before();

@@ -87,7 +87,7 @@ def run_dense(type_, M, N, K, how="pad16", ldc_pad=0, offset=0, seed=0, extreme=
     (1, 1, 1), (1, 4096, 4096), (2, 100, 15), (3, 128, 16), (8, 256, 17), (15, 7, 64), (16, 64, 127),
     (17, 129, 128), (32, 4092, 777), (33, 1500, 129), (37, 4092, 4092), (63, 200, 1024),
     (64, 512, 2048), (65, 257, 256), (128, 384, 640), (129, 1000, 500), (200, 640, 1100),
-    (255, 256, 96), (256, 256, 512), (257, 300, 1000), (513, 2050, 300), (1000, 1500, 777)])
+    (255, 256, 96), (90, 2121, 448), (700, 2121, 448), (333, 1026, 64), (256, 256, 512), (257, 300, 1000), (513, 2050, 300), (1000, 1500, 777)])
 def test_dense_shapes(type_, M, N, K):
     run_dense(type_, M, N, K)
 
@@ -115,6 +115,7 @@ def test_dense_bases_off_16_bytes(offset):
 def test_dense_result_pitches(type_, ldc_pad, c_off):
     run_dense(type_, 75, 264, 200, ldc_pad=ldc_pad, c_off=c_off)
     run_dense(type_, 300, 520, 140, ldc_pad=ldc_pad, c_off=c_off)
+    run_dense(type_, 2100, 2050, 70, ldc_pad=ldc_pad, c_off=c_off)
 
 
 @pytest.mark.parametrize("M,N,K", [(16, 128, 1024), (40, 200, 1040), (300, 256, 9000), (5, 128, 16384)])
