@@ -239,7 +239,8 @@ unsigned sort_cluster(int S)
 
 struct Args {
     int T, k, S;              // S = T * k
-    int nvec;                 // vectors in a row
+    unsigned nvec;            // vectors in a row (unsigned: an index past the end of the
+                              // longest row by a stride must not wrap below it)
     const int *positions;
     const int *total;         // offsets[E]: the kept choices
     const float *weights;     // may be null: 1
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const Args a)
 #pragma unroll
         for (int j = 0; j < kGroup; ++j)
             p[j] = j0 + j < a.k ? a.positions[t * a.k + j0 + j] : -1;
-        for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < a.nvec;
+        for (unsigned v = blockIdx.y * blockDim.x + threadIdx.x; v < a.nvec;
              v += gridDim.y * blockDim.x) {
             Vec<T, VB> x, z;
             x.load(a.tok + t * a.tok_pitch + static_cast<long long>(v) * VB);
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(256, 6) combine_kernel(const Args a)
     const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (t >= a.T) return;
     const int total = min(*a.total, a.S);
-    for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < a.nvec; v += gridDim.y * blockDim.x) {
+    for (unsigned v = blockIdx.y * blockDim.x + threadIdx.x; v < a.nvec; v += gridDim.y * blockDim.x) {
         float acc[V::N];
 #pragma unroll
         for (int i = 0; i < V::N; ++i) acc[i] = 0.f;
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(256, 5) combine_grad_kernel(const Args a)
             w[j] = in && a.weights ? a.weights[t * a.k + j0 + j] : 1.f;
             dw[j] = 0.f;
         }
-        for (int v = threadIdx.x; live && v < a.nvec; v += blockDim.x) {
+        for (unsigned v = threadIdx.x; live && v < a.nvec; v += blockDim.x) {
             const long long at = static_cast<long long>(v) * VB;
             V g, x[kGroup];
             g.load(a.tok + t * a.tok_pitch + at);
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(256, 5) combine_grad_kernel(const Args a)
 struct Grid {
     dim3 grid, block;
 };
-Grid row_grid(int T, int nvec, bool split_columns)
+Grid row_grid(int T, unsigned nvec, bool split_columns)
 {
     const int tx = rows::pow2_threads(nvec, 32, 256), ty = 256 / tx;
     const unsigned gx = static_cast<unsigned>((static_cast<long long>(T) + ty - 1) / ty);
@@ -497,7 +498,7 @@ int combine(int type, int T, int k, int E, int H, const void *rws, int ldr, cons
     a.row_pitch = ldr * es;
     a.tok_pitch = ldo * es;
     const int vb = rows::Width().add(rws).add(out).add(a.row_pitch).add(a.tok_pitch).add(H * es).bytes();
-    a.nvec = static_cast<int>(H * es / vb);
+    a.nvec = static_cast<unsigned>(H * es / vb);
     return rows::with_vec(type, vb, ex::Launch{ex::kCombine, a, static_cast<cudaStream_t>(stream)});
 }
 
@@ -542,7 +543,7 @@ int sgemm_experts_dispatch(int type, int T, int k, int E, int H, const void *x, 
         a.row_out_pitch = ldr * es;
         const int vb =
             rows::Width().add(x).add(rws).add(a.tok_pitch).add(a.row_out_pitch).add(H * es).bytes();
-        a.nvec = static_cast<int>(H * es / vb);
+        a.nvec = static_cast<unsigned>(H * es / vb);
         return rows::with_vec(type, vb, ex::Launch{ex::kDispatch, a, static_cast<cudaStream_t>(stream)});
     });
 }
@@ -596,7 +597,7 @@ int sgemm_experts_combine_grad(int type, int T, int k, int E, int H, const void 
         }
         // H == 0: pointers may be null; the kernel writes zero dweights only
         const int vb = H == 0 ? 16 : w.bytes();
-        a.nvec = static_cast<int>(H * es / vb);
+        a.nvec = static_cast<unsigned>(H * es / vb);
         return rows::with_vec(type, vb,
                               ex::Launch{ex::kCombineGrad, a, static_cast<cudaStream_t>(stream)});
     });

@@ -237,7 +237,7 @@ int product(int type, int M, int N, int K, int E, const int *offsets, const sign
             const float *scaleB, void *C, int ldc, void *stream)
 {
     if (!rows::valid_type(type) || M < 0 || N < 0 || K < 0 || lda < 1 || ldb < 1 || ldc < 1 ||
-        lda < K || ldb < K || ldc < N || K > kMaxK)
+        lda < K || ldb < K || ldc < N || K > kMaxK || M > kMaxSide || N > kMaxSide)
         return SGEMM_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return SGEMM_OK;
     if (C == nullptr || scaleA == nullptr || scaleB == nullptr ||

@@ -29,7 +29,8 @@ constexpr int kHeld = 4;                         // vectors per thread kept in r
 
 struct Args {
     int M, K;               // rows, values (codes) per row
-    int nvec;               // vectors per row
+    unsigned nvec;          // vectors per row (unsigned: an index past the end of the longest
+                            // row by a stride must not wrap below it)
     const char *x;
     long long x_pitch;      // bytes
     long long up;           // SwiGLU: bytes from the gates to the values
@@ -69,7 +70,7 @@ __device__ __forceinline__ void store_codes(signed char *p, const int (&c)[EV])
 
 // One vector of the values to quantise, in fp32.
 template <class T, int VB, bool GATED>
-__device__ __forceinline__ void load_values(const Args &a, const char *row, int v,
+__device__ __forceinline__ void load_values(const Args &a, const char *row, unsigned v,
                                             float (&f)[Vec<T, VB>::N])
 {
     Vec<T, VB> g;
@@ -93,7 +94,7 @@ __device__ __forceinline__ void load_values(const Args &a, const char *row, int 
 template <class T, int VB, bool GATED>
 struct Held {
     Vec<T, VB> v;
-    __device__ __forceinline__ void load(const Args &, const char *row, int i)
+    __device__ __forceinline__ void load(const Args &, const char *row, unsigned i)
     {
         v.load(row + static_cast<long long>(i) * VB);
     }
@@ -102,7 +103,7 @@ struct Held {
 template <class T, int VB>
 struct Held<T, VB, true> {
     float f[Vec<T, VB>::N];
-    __device__ __forceinline__ void load(const Args &a, const char *row, int i)
+    __device__ __forceinline__ void load(const Args &a, const char *row, unsigned i)
     {
         load_values<T, VB, true>(a, row, i, f);
     }
@@ -119,14 +120,14 @@ __global__ void __launch_bounds__(256, GATED ? 3 : 5) quantize_kernel(const Args
     const long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     const bool live = r < a.M;
     const char *row = a.x + (live ? r : 0) * a.x_pitch;
-    const int tx = threadIdx.x, nx = blockDim.x, warps = nx >> 5;
-    const int nvec = live ? a.nvec : 0;
+    const unsigned tx = threadIdx.x, nx = blockDim.x, warps = nx >> 5;
+    const unsigned nvec = live ? a.nvec : 0;
 
     Held<T, VB, GATED> held[kHeld];
     unsigned big = 0;
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
-        const int v = tx + h * nx;
+        const unsigned v = tx + h * nx;
         if (v < nvec) held[h].load(a, row, v);
     }
 #pragma unroll
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(256, GATED ? 3 : 5) quantize_kernel(const Args
 #pragma unroll
             for (int i = 0; i < EV; ++i)
                 big = max(big, __float_as_uint(held[h].get(i)) & 0x7FFFFFFFu);
-    for (int v = tx + kHeld * nx; v < nvec; v += nx) {
+    for (unsigned v = tx + kHeld * nx; v < nvec; v += nx) {
         float g[EV];
         load_values<T, VB, GATED>(a, row, v, g);
 #pragma unroll
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(256, GATED ? 3 : 5) quantize_kernel(const Args
     if (warps > 1) {
         if ((tx & 31) == 0) part[threadIdx.y * warps + (tx >> 5)] = big;
         __syncthreads();
-        for (int w = 0; w < warps; ++w) big = max(big, part[threadIdx.y * warps + w]);
+        for (unsigned w = 0; w < warps; ++w) big = max(big, part[threadIdx.y * warps + w]);
     }
     if (!live) return;
     const float amax = __uint_as_float(big);
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(256, GATED ? 3 : 5) quantize_kernel(const Args
         for (int i = 0; i < EV; ++i)
             c[i] = finite ? __float_as_int(__fadd_rn(__fmul_rn(x[i], inv), kRound)) : 0;
     };
-    auto put = [&](int v, const int (&c)[EV]) {
+    auto put = [&](unsigned v, const int (&c)[EV]) {
         if constexpr (EXPERT) {
             const int total = *a.total;
             int none[EV] = {};
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(256, GATED ? 3 : 5) quantize_kernel(const Args
     };
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
-        const int v = tx + h * nx;
+        const unsigned v = tx + h * nx;
         if (v < nvec) {
             float f[EV];
             int c[EV];
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(256, GATED ? 3 : 5) quantize_kernel(const Args
             put(v, c);
         }
     }
-    for (int v = tx + kHeld * nx; v < nvec; v += nx) {
+    for (unsigned v = tx + kHeld * nx; v < nvec; v += nx) {
         float g[EV];
         int c[EV];
         load_values<T, VB, GATED>(a, row, v, g);
@@ -264,7 +265,7 @@ int sgemm_i8_quantize_rows(int type, int act, int M, int K, const void *X, int l
         a.ldq = ldq;
         a.scale = scale;
         const int vb = K == 0 ? 16 : rows::Width().add(X).add(a.x_pitch).add(a.up).bytes();
-        a.nvec = static_cast<int>(K * es / vb);
+        a.nvec = static_cast<unsigned>(K * es / vb);
         return rows::with_vec(type, vb,
                               qz::Launch{a, gated, false, static_cast<cudaStream_t>(stream)});
     });
@@ -303,7 +304,7 @@ int sgemm_experts_dispatch_i8(int type, int T, int k, int E, int H, const void *
         a.k = k;
         a.S = T * k;
         const int vb = H == 0 ? 16 : rows::Width().add(x).add(a.x_pitch).add(H * es).bytes();
-        a.nvec = static_cast<int>(H * es / vb);
+        a.nvec = static_cast<unsigned>(H * es / vb);
         return rows::with_vec(type, vb,
                               qz::Launch{a, false, true, static_cast<cudaStream_t>(stream)});
     });

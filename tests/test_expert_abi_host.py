@@ -97,3 +97,12 @@ def test_names_of_types_and_acts(lib):
     assert call(lib, "sgemm_i8_quantize_rows", type_="bf16", act="none", M=0) == lib.SGEMM_OK
     with pytest.raises(KeyError):
         call(lib, "sgemm_i8", type_="int8")
+
+
+@pytest.mark.parametrize("name", ["sgemm_i8", "sgemm_i8_experts"])
+def test_sides_end_where_a_tile_past_them_is_still_an_int(lib, name):
+    most = 2 ** 31 - 512
+    more = dict(strideB=8 * (most + 1)) if name == "sgemm_i8_experts" else {}
+    for side in ("M", "N"):
+        kw = dict(ldc=most + 1, **more)
+        assert call(lib, name, **{side: most + 1}, **kw) == lib.SGEMM_ERR_INVALID_ARG

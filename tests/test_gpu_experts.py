@@ -114,7 +114,8 @@ def test_sort_of_nothing():
 # than a warp's vectors and longer than a block's, more choices than move at once
 SHAPES = [(1, 1, 1, 1, 0, 0), (5, 2, 3, 7, 0, 0), (16, 4, 32, 2048, 0, 0), (3, 8, 8, 64, 0, 0),
           (9, 3, 4, 333, 0, 1), (17, 9, 12, 96, 8, 8), (130, 2, 5, 1500, 4, 4), (6, 17, 20, 40, 0, 2),
-          (4, 3, 2, 9000, 24, 0), (2, 64, 100, 10, 1, 0)]
+          (4, 3, 2, 9000, 24, 0), (2, 64, 100, 10, 1, 0), (40, 5, 6, 2825, 0, 0), (12, 2, 3, 641, 3, 5),
+          (7, 2, 4, 17, 0, 3), (300, 4, 6, 1123, 0, 0)]
 
 
 @pytest.mark.parametrize("type_", TYPES)
@@ -360,6 +361,25 @@ def test_rows_beyond_32_bit_offsets():
     assert torch.equal(out, 2 * x)  # integers up to 16: exact
     at = torch.tensor([0, 1, T * k // 2, T * k - 1], device="cuda")
     assert torch.equal(rows[at], x[slots[at].long() // k])
+
+
+def test_longest_row():
+    """One row of 2^31 - 1 values, moved one by one: a column index a stride
+    past the end does not fit 31 bits."""
+    import torch
+    import dense_fp32_matrix_03_gb300 as lib
+    H = 2 ** 31 - 1
+    x = torch.zeros(H, dtype=torch.bfloat16, device="cuda")
+    ends = torch.arange(1, 100001, device="cuda") % 255
+    x[:100000], x[-100000:] = ends, ends
+    offsets = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    positions = torch.zeros(1, dtype=torch.int32, device="cuda")
+    row, out = torch.empty_like(x), torch.empty_like(x)
+    assert lib.sgemm_experts_dispatch("bf16", 1, 1, 1, H, x, H, positions, offsets, row, H) == 0
+    assert torch.equal(row, x)
+    assert lib.sgemm_experts_combine("bf16", 1, 1, 1, H, row, H, positions, offsets, None, out,
+                                     H) == 0
+    assert torch.equal(out, x)
 
 
 def test_side_stream_repeats_bit_for_bit():
