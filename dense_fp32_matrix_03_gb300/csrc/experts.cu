@@ -22,7 +22,6 @@ constexpr int kSortAhead = 8;     // steps of a warp's walk loaded at once
 // other's chain of position, row and sum best (65536 rows of 4096 bf16
 // combined, by choices x blocks: 8 x 4 97 us, 4 x 6 95, 4 x 8 (spills) 299,
 // 2 x 8 112; the gradient of 32768 rows of 2048: 8 x 4 66, 4 x 5 48, 2 x 8 61).
-constexpr int kGroup = 4;
 
 // ------------------------------------------------------------------ sort
 //
@@ -227,15 +226,27 @@ unsigned sort_cluster(int S)
 // All move whole rows and compute next to nothing: bound by HBM.  A block
 // takes blockDim.y tokens, blockDim.x threads over a row's vectors, and works
 // token by token: a token's k rows are read (combine) or written (dispatch)
-// together, so its own row moves once and up to kGroup loads per thread are
-// in flight.  p(t,j) is checked against T * k, so a corrupt position cannot
-// reach outside the rows.
+// together, G choices at a time, so its own row moves once.  A block lives for
+// three dependent loads (kept count, position, row), so what counts is how
+// many bytes each thread then has in flight: U vectors a block's width apart
+// (neighbouring threads stay on neighbouring addresses) of each of G rows, 16
+// bytes of each row where registers allow.  p(t,j) is checked against T * k,
+// so a corrupt position cannot reach outside the rows.
+//
+// G and U by choices and alignment (us, one vector of four rows / as chosen):
+//   k <= 2: two rows, two vectors or more: combine 8192 x 2 rows of 4096 bf16
+//     43 / 38, 16384 x 1 of 1024 19.4 / 15, its gradient 56 / 51, 27 / 19
+//   rows on 8 bytes or less: 16 bytes of four rows (at most four vectors):
+//     3000 x 2 rows of 2825 fp16 49 / 21, 7252 x 3 of 2612 bf16 64 / 43, 1874 x
+//     5 of 2825 fp16 51 / 28, dispatch of these 38 / 21, 35 / 32, 36 / 22
+//   the gradient on 8 bytes: one vector, since it keeps a token's vector and
+//     the sums too (7252 x 3 of 2612: 55; two vectors 73)
 //
 // Measured on GB300, bf16 (us, share of the measured copy bandwidth for the
 // bytes of kept rows, tokens' rows and results): 65536 rows of 4096 dispatched
 // 93 (0.96), combined 95 (0.93), combine's gradient 170 (0.99); 32768 rows of
 // 2048 28 (0.89), 31 (0.81), 48 (0.92).  Eight tokens of 2048: 1.7 to 2.3 us,
-// launch and three dependent loads (kept count, position, row).
+// launch and the three loads.
 
 struct Args {
     int T, k, S;              // S = T * k
@@ -255,32 +266,43 @@ struct Args {
 template <class T, int VB>
 __global__ void __launch_bounds__(256) dispatch_kernel(const Args a)
 {
+    constexpr int G = 4, U = rows::kAhead<VB>;
     dependent_release();
     dependent_wait();
     const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (t >= a.T) return;
     const int total = *a.total;
-    for (int j0 = 0; j0 < a.k; j0 += kGroup) {
-        int p[kGroup];
+    const char *tok = a.tok + t * a.tok_pitch;
+    for (int j0 = 0; j0 < a.k; j0 += G) {
+        int p[G];
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j)
+        for (int j = 0; j < G; ++j)
             p[j] = j0 + j < a.k ? a.positions[t * a.k + j0 + j] : -1;
-        for (unsigned v = blockIdx.y * blockDim.x + threadIdx.x; v < a.nvec;
-             v += gridDim.y * blockDim.x) {
-            Vec<T, VB> x, z;
-            x.load(a.tok + t * a.tok_pitch + static_cast<long long>(v) * VB);
+        for (unsigned v = blockIdx.y * U * blockDim.x + threadIdx.x; v < a.nvec;
+             v += gridDim.y * U * blockDim.x) {
+            Vec<T, VB> x[U], z;
             z.zero();
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j)
-                if (p[j] >= 0 && p[j] < a.S)
-                    (p[j] < total ? x : z)
-                        .store(a.row_out + p[j] * a.row_out_pitch +
-                               static_cast<long long>(v) * VB);
+            for (int u = 0; u < U; ++u) {
+                const unsigned i = v + u * blockDim.x;
+                if (i < a.nvec) x[u].load(tok + static_cast<long long>(i) * VB);
+            }
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                if (p[j] < 0 || p[j] >= a.S) continue;
+                char *out = a.row_out + p[j] * a.row_out_pitch;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const unsigned i = v + u * blockDim.x;
+                    if (i < a.nvec)
+                        (p[j] < total ? x[u] : z).store(out + static_cast<long long>(i) * VB);
+                }
+            }
         }
     }
 }
 
-template <class T, int VB>
+template <class T, int VB, int G, int U>
 __global__ void __launch_bounds__(256, 6) combine_kernel(const Args a)
 {
     using V = Vec<T, VB>;
@@ -289,98 +311,135 @@ __global__ void __launch_bounds__(256, 6) combine_kernel(const Args a)
     const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (t >= a.T) return;
     const int total = min(*a.total, a.S);
-    for (unsigned v = blockIdx.y * blockDim.x + threadIdx.x; v < a.nvec; v += gridDim.y * blockDim.x) {
-        float acc[V::N];
+    char *out = a.tok_out + t * a.tok_pitch;
+    for (unsigned v = blockIdx.y * U * blockDim.x + threadIdx.x; v < a.nvec;
+         v += gridDim.y * U * blockDim.x) {
+        float acc[U][V::N];
 #pragma unroll
-        for (int i = 0; i < V::N; ++i) acc[i] = 0.f;
-        for (int j0 = 0; j0 < a.k; j0 += kGroup) {
-            V x[kGroup];
-            float w[kGroup];
-            bool on[kGroup];
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j) {
+            for (int i = 0; i < V::N; ++i) acc[u][i] = 0.f;
+        for (int j0 = 0; j0 < a.k; j0 += G) {
+            V x[G][U];
+            float w[G];
+            bool on[G];
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
                 on[j] = false;
                 if (j0 + j < a.k) {
                     const int p = a.positions[t * a.k + j0 + j];
                     w[j] = a.weights ? a.weights[t * a.k + j0 + j] : 1.f;
                     on[j] = p >= 0 && p < total;
-                    if (on[j])
-                        x[j].load(a.row + p * a.row_pitch + static_cast<long long>(v) * VB);
+                    if (on[j]) {
+                        const char *row = a.row + p * a.row_pitch;
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const unsigned i = v + u * blockDim.x;
+                            if (u == 0 || i < a.nvec)
+                                x[j][u].load(row + static_cast<long long>(i) * VB);
+                        }
+                    }
                 }
             }
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j)
+            for (int j = 0; j < G; ++j)
                 if (on[j]) {
 #pragma unroll
-                    for (int i = 0; i < V::N; ++i) acc[i] = fmaf(w[j], x[j].get(i), acc[i]);
+                    for (int u = 0; u < U; ++u)
+                        if (u == 0 || v + u * blockDim.x < a.nvec)
+#pragma unroll
+                            for (int i = 0; i < V::N; ++i)
+                                acc[u][i] = fmaf(w[j], x[j][u].get(i), acc[u][i]);
                 }
         }
-        V o;
 #pragma unroll
-        for (int i = 0; i < V::N; ++i) o.set(i, acc[i]);
-        o.store(a.tok_out + t * a.tok_pitch + static_cast<long long>(v) * VB);
+        for (int u = 0; u < U; ++u) {
+            const unsigned c = v + u * blockDim.x;
+            V o;
+#pragma unroll
+            for (int i = 0; i < V::N; ++i) o.set(i, acc[u][i]);
+            if (u == 0 || c < a.nvec) o.store(out + static_cast<long long>(c) * VB);
+        }
     }
 }
 
 // DW: dweights wanted (rows is read).  blockDim.x threads of one token sum
 // their products over the row, then over lanes and warps in a fixed order.
-template <class T, int VB, bool DW>
-__global__ void __launch_bounds__(256, 5) combine_grad_kernel(const Args a)
+template <class T, int VB, int G, int U, bool DW>
+__global__ void __launch_bounds__(256, G * U == 16 ? 4 : 5) combine_grad_kernel(const Args a)
 {
     using V = Vec<T, VB>;
-    __shared__ float part[8][kGroup];  // one row per warp of the block
+    __shared__ float part[8][G];  // one row per warp of the block
     dependent_release();
     dependent_wait();
     const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     const bool live = t < a.T;
     const int total = min(*a.total, a.S);
     const int wid = (threadIdx.y * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-    for (int j0 = 0; j0 < a.k; j0 += kGroup) {
-        float w[kGroup], dw[kGroup];
-        int p[kGroup];
+    const char *tok = a.tok + t * a.tok_pitch;
+    for (int j0 = 0; j0 < a.k; j0 += G) {
+        float w[G], dw[G];
+        int p[G];
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
+        for (int j = 0; j < G; ++j) {
             const bool in = live && j0 + j < a.k;
             p[j] = in ? a.positions[t * a.k + j0 + j] : -1;
             if (p[j] >= a.S) p[j] = -1;
             w[j] = in && a.weights ? a.weights[t * a.k + j0 + j] : 1.f;
             dw[j] = 0.f;
         }
-        for (unsigned v = threadIdx.x; live && v < a.nvec; v += blockDim.x) {
-            const long long at = static_cast<long long>(v) * VB;
-            V g, x[kGroup];
-            g.load(a.tok + t * a.tok_pitch + at);
+        for (unsigned v = threadIdx.x; live && v < a.nvec; v += U * blockDim.x) {
+            V g[U], x[G][U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const unsigned i = v + u * blockDim.x;
+                if (u == 0 || i < a.nvec) g[u].load(tok + static_cast<long long>(i) * VB);
+            }
             if (DW) {
 #pragma unroll
-                for (int j = 0; j < kGroup; ++j)
-                    if (p[j] >= 0 && p[j] < total) x[j].load(a.row + p[j] * a.row_pitch + at);
+                for (int j = 0; j < G; ++j)
+                    if (p[j] >= 0 && p[j] < total) {
+                        const char *row = a.row + p[j] * a.row_pitch;
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const unsigned i = v + u * blockDim.x;
+                            if (u == 0 || i < a.nvec)
+                                x[j][u].load(row + static_cast<long long>(i) * VB);
+                        }
+                    }
             }
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j) {
+            for (int j = 0; j < G; ++j) {
                 if (p[j] < 0) continue;
-                V o;
-                if (p[j] < total) {
+                char *out = a.row_out + p[j] * a.row_out_pitch;
 #pragma unroll
-                    for (int i = 0; i < V::N; ++i) {
-                        if (DW) dw[j] = fmaf(x[j].get(i), g.get(i), dw[j]);
-                        o.set(i, w[j] * g.get(i));
+                for (int u = 0; u < U; ++u) {
+                    const unsigned at = v + u * blockDim.x;
+                    if (u > 0 && at >= a.nvec) continue;
+                    V o;
+                    if (p[j] < total) {
+#pragma unroll
+                        for (int i = 0; i < V::N; ++i) {
+                            if (DW) dw[j] = fmaf(x[j][u].get(i), g[u].get(i), dw[j]);
+                            o.set(i, w[j] * g[u].get(i));
+                        }
+                    } else {
+                        o.zero();
                     }
-                } else {
-                    o.zero();
+                    o.store(out + static_cast<long long>(at) * VB);
                 }
-                o.store(a.row_out + p[j] * a.row_out_pitch + at);
             }
         }
         if (DW) {
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j) {
+            for (int j = 0; j < G; ++j) {
 #pragma unroll
                 for (int d = 16; d > 0; d /= 2) dw[j] += __shfl_xor_sync(0xffffffffu, dw[j], d);
                 if (lane == 0) part[wid][j] = dw[j];
             }
             __syncthreads();
             const int warps = blockDim.x >> 5;
-            if (live && threadIdx.x < kGroup && j0 + static_cast<int>(threadIdx.x) < a.k) {
+            if (live && threadIdx.x < G && j0 + static_cast<int>(threadIdx.x) < a.k) {
                 float s = 0.f;
                 for (int i = 0; i < warps; ++i) s += part[threadIdx.y * warps + i][threadIdx.x];
                 a.dweights[t * a.k + j0 + threadIdx.x] = s;
@@ -390,19 +449,21 @@ __global__ void __launch_bounds__(256, 5) combine_grad_kernel(const Args a)
     }
 }
 
-// Threads over a row and tokens per block (256 threads, at least a warp per
-// token), and blocks over a row's columns: enough that few tokens still
-// spread over the GPU.
+// Threads over a row (per_thread vectors each) and tokens per block (256
+// threads, at least a warp per token), and blocks over a row's columns: enough
+// that few tokens still spread over the GPU.
 struct Grid {
     dim3 grid, block;
 };
-Grid row_grid(int T, unsigned nvec, bool split_columns)
+Grid row_grid(int T, unsigned nvec, unsigned per_thread, bool split_columns)
 {
-    const int tx = rows::pow2_threads(nvec, 32, 256), ty = 256 / tx;
+    const unsigned pieces = nvec == 0 ? 1 : (nvec + per_thread - 1) / per_thread;
+    const unsigned turns = (pieces + 255) / 256;
+    const int tx = ((pieces + turns - 1) / turns + 31) / 32 * 32, ty = 256 / tx;
     const unsigned gx = static_cast<unsigned>((static_cast<long long>(T) + ty - 1) / ty);
     unsigned gy = 1;
     if (split_columns) {
-        gy = static_cast<unsigned>((nvec + tx - 1) / tx);
+        gy = (pieces + tx - 1) / tx;
         if (gy > 64) gy = 64;
     }
     return {dim3(gx, gy), dim3(static_cast<unsigned>(tx), static_cast<unsigned>(ty))};
@@ -417,11 +478,18 @@ struct Launch {
     template <class T, int VB>
     int run() const
     {
-        const Grid g = row_grid(a.T, a.nvec, op != kCombineGrad);
-        auto kern = op == kDispatch              ? dispatch_kernel<T, VB>
-                    : op == kCombine             ? combine_kernel<T, VB>
-                    : a.dweights != nullptr      ? combine_grad_kernel<T, VB, true>
-                                                 : combine_grad_kernel<T, VB, false>;
+        constexpr int U = rows::kAhead<VB>, U2 = U > 2 ? U : 2;
+        constexpr int UG = VB < 8 ? U : 1;  // combine's gradient, beyond two choices
+        const bool two = op != kDispatch && a.k <= 2, dw = a.dweights != nullptr;
+        const Grid g =
+            row_grid(a.T, a.nvec, two ? U2 : op == kCombineGrad ? UG : U, op != kCombineGrad);
+        auto kern = op == kDispatch ? dispatch_kernel<T, VB>
+                    : op == kCombine
+                        ? (two ? combine_kernel<T, VB, 2, U2> : combine_kernel<T, VB, 4, U>)
+                    : dw ? (two ? combine_grad_kernel<T, VB, 2, U2, true>
+                                : combine_grad_kernel<T, VB, 4, UG, true>)
+                         : (two ? combine_grad_kernel<T, VB, 2, U2, false>
+                                : combine_grad_kernel<T, VB, 4, UG, false>);
         return launch_dependent(kern, g.grid, g.block, 0, 1, st, a);
     }
 };

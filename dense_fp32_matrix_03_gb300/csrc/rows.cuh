@@ -92,6 +92,11 @@ struct Vec {
     __device__ __forceinline__ void set(int i, float x) { v[i] = from_f<T>(x); }
 };
 
+// Vectors of VB bytes that a thread moves at a time: up to 16 bytes, at most
+// four.
+template <int VB>
+constexpr int kAhead = VB < 8 ? 4 : 16 / VB;
+
 inline int elem_size(int type) { return type == SGEMM_TYPE_FP32 ? 4 : 2; }
 inline bool valid_type(int type)
 {
