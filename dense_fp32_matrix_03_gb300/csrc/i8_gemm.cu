@@ -118,15 +118,18 @@ bool rows_on_16(const Args &a)
            (a.E == 1 || a.strideB % 16 == 0);
 }
 
-// Output tiles of nt tokens x ch channels that a call is expected to have:
-// experts share the rows about evenly, and end in half a tile.
+// Output tiles of nt tokens x ch channels that a call is expected to have.
+// Experts' counts are on the GPU: of equal ones each ends in one short tile (in
+// one more where the mean is about a multiple of nt), of uneven ones in half a
+// tile on average; the mean of the two.
 double tiles_expected(const Args &a, int nt, int ch)
 {
     const double cts = (a.N + ch - 1) / ch;
     if (a.offsets == nullptr) return (a.M + nt - 1LL) / nt * cts;
     const int used = a.E < a.M ? a.E : a.M;
-    const double each = static_cast<double>(a.M) / used / nt + 0.5;
-    return used * (each > 1. ? each : 1.) * cts;
+    const double mean = static_cast<double>(a.M) / used / nt;
+    const double uneven = mean > 0.5 ? mean + 0.5 : 1.;
+    return used * 0.5 * (ceil(mean + 0.1) + uneven) * cts;
 }
 
 // Clusters of `size` CTAs of the narrow kernel that the GPU runs at once (a
@@ -189,7 +192,6 @@ int run(const Args &a, cudaStream_t st)
     //           x 1024 8.3, 64 x 4096 x 128 4.2
     //   wide    about 0.7 a slot and wave, of tiles four times as large: 256 ..
     //           1024 x 4096 x 4096 28 .. 30, 2048 53; less when the GPU is full
-    // Narrow and wide differ little per slot, so the count of waves decides.
     const double narrow_tiles = tiles_expected(a, Narrow::NT, kCh);
     const double wide_tiles = tiles_expected(a, Wide::NT, 2 * kCh);
     int split = 1;
@@ -220,8 +222,27 @@ int run(const Args &a, cudaStream_t st)
         // rows 36 / 46 us, 16 rows 43 / 47
         return launch_few<T, 1, 2, 4, 6>(a, st);
     }
-    const double wide_cost = (wide_tiles < pairs ? 0.70 : 0.60) * ceil(wide_tiles / pairs);
-    if (wide_cost < 0.63 * narrow_waves) {
+    // A tile takes as long as its epilogue (short k) or its multiplies (long k),
+    // whichever is longer, us by slots of k; K = 128, 512, 1024, 2048, narrow /
+    // wide: 8192 x 8192 71 / 64, 92 / 73, 155 / 103, 286 / 175; 32 experts of
+    // 3840 channels, 99 rows each, 24 / 30, 31 / 36, 48 / 51, 81 / 84, and of
+    // 3837 channels, 128 rows each, 40 / 49, 50 / 61, 69 / 66, 113 / 90; fp32,
+    // 8192 x 4096, 67 / 40, 78 / 52, - , 154 / 108.
+    const double s = k_slots, sn = s / split;
+    const bool fp32 = sizeof(T) == 4, odd = c_bytes < 8 && !fp32;
+    const double narrow_end = fp32 ? 4.1 + 0.27 * sn : odd ? 2.9 + 0.28 * sn : 2.2 + 0.25 * sn;
+    const double narrow_mma = 0.8 + 0.6 * sn;
+    const double wide_end = fp32 ? 4.6 + 0.5 * s : odd ? 6.0 + 0.4 * s : 4.2 + 0.2 * s;
+    const double wide_mma = 1.9 + (fp32 ? 0.8 : 0.63) * s;
+    const double narrow_cost = (narrow_end > narrow_mma ? narrow_end : narrow_mma) *
+                                   ceil(narrow_tiles * split / a.num_sms) +
+                               (split > 1 ? 1.6 : 0.);
+    const double wide_cost =
+        (wide_end > wide_mma ? wide_end : wide_mma) * ceil(wide_tiles / pairs) + 0.8;
+    // (experts of unknown counts: narrow where it is clearly ahead, since more of
+    // its tiles may turn out to be needed: 60 experts of 200 rows x 1536 x 128
+    // 37 / 27)
+    if ((dense ? 1. : 0.9) * wide_cost < narrow_cost) {
         const long long tiles = max_tiles(a, Wide::NT) * ((a.N + 2 * kCh - 1) / (2 * kCh));
         return launch_tc_i8<Wide, T>(a, tmW, tmT, tiles < pairs ? tiles : pairs, 1, c_bytes, st);
     }
