@@ -14,6 +14,12 @@
 // (4.9 TB/s; with two or eight vectors a thread 22.5 and 21.0), 8192 x 8192 38 us
 // (5.3), 65536 rows of 4096 in expert order from 8192 tokens 55 us (6.1), one
 // row of 4096 1.5 us.
+//
+// Rows off 16 bytes are loaded in pieces of what their alignment allows, into
+// vectors of at least four values whose codes go out as one word: codes stored
+// one by one cost more than the loads (one value / four values at a time, bf16:
+// 8192 x 4095 80 / 30 us, 8192 x 4094 42 / 30, 32768 rows of 2001 in expert
+// order from 8192 tokens 69 / 31, one row of 4095 3.9 / 1.6).
 #include "../../include/expert_layer.h"
 #include "dependent.cuh"
 #include "rows.cuh"
@@ -42,11 +48,12 @@ struct Args {
     int k, S;
 };
 
-// The low bytes of EV integers, as one access where QV says q allows it.
+// The low bytes of the first n of EV integers, as one access where QV says
+// that q allows it and all are stored.
 template <int EV, bool QV>
-__device__ __forceinline__ void store_codes(signed char *p, const int (&c)[EV])
+__device__ __forceinline__ void store_codes(signed char *p, const int (&c)[EV], int n)
 {
-    if constexpr (QV && EV >= 2) {
+    if (QV && n == EV) {
         uint32_t w[(EV + 3) / 4] = {};  // the low bytes side by side
         if constexpr (EV >= 4) {
 #pragma unroll
@@ -64,20 +71,30 @@ __device__ __forceinline__ void store_codes(signed char *p, const int (&c)[EV])
             *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(w[0]);
     } else {
 #pragma unroll
-        for (int i = 0; i < EV; ++i) p[i] = static_cast<signed char>(c[i]);
+        for (int i = 0; i < EV; ++i)
+            if (i < n) p[i] = static_cast<signed char>(c[i]);
     }
 }
 
-// One vector of the values to quantise, in fp32.
-template <class T, int VB, bool GATED>
+// Bytes of the row from vector v on, as far as a vector goes.
+template <class T, int VB>
+__device__ __forceinline__ unsigned bytes_left(const Args &a, unsigned v)
+{
+    constexpr unsigned EV = Vec<T, VB>::N;
+    return min(static_cast<unsigned>(a.K) - v * EV, EV) * static_cast<unsigned>(sizeof(T));
+}
+
+// One vector of the values to quantise, in fp32 (past the row: zeros).
+template <class T, int VB, int LB, bool GATED>
 __device__ __forceinline__ void load_values(const Args &a, const char *row, unsigned v,
                                             float (&f)[Vec<T, VB>::N])
 {
+    const unsigned left = bytes_left<T, VB>(a, v);
     Vec<T, VB> g;
-    g.load(row + static_cast<long long>(v) * VB);
+    g.template load_pieces<LB>(row + static_cast<long long>(v) * VB, left);
     if constexpr (GATED) {
         Vec<T, VB> u;
-        u.load(row + a.up + static_cast<long long>(v) * VB);
+        u.template load_pieces<LB>(row + a.up + static_cast<long long>(v) * VB, left);
 #pragma unroll
         for (int i = 0; i < Vec<T, VB>::N; ++i) {
             const float x = g.get(i);
@@ -91,26 +108,26 @@ __device__ __forceinline__ void load_values(const Args &a, const char *row, unsi
 
 // A vector of values kept until the maximum is known: as loaded, or, gated,
 // as computed.
-template <class T, int VB, bool GATED>
+template <class T, int VB, int LB, bool GATED>
 struct Held {
     Vec<T, VB> v;
-    __device__ __forceinline__ void load(const Args &, const char *row, unsigned i)
+    __device__ __forceinline__ void load(const Args &a, const char *row, unsigned i)
     {
-        v.load(row + static_cast<long long>(i) * VB);
+        v.template load_pieces<LB>(row + static_cast<long long>(i) * VB, bytes_left<T, VB>(a, i));
     }
     __device__ __forceinline__ float get(int i) const { return v.get(i); }
 };
-template <class T, int VB>
-struct Held<T, VB, true> {
+template <class T, int VB, int LB>
+struct Held<T, VB, LB, true> {
     float f[Vec<T, VB>::N];
     __device__ __forceinline__ void load(const Args &a, const char *row, unsigned i)
     {
-        load_values<T, VB, true>(a, row, i, f);
+        load_values<T, VB, LB, true>(a, row, i, f);
     }
     __device__ __forceinline__ float get(int i) const { return f[i]; }
 };
 
-template <class T, int VB, bool GATED, bool EXPERT, bool QV>
+template <class T, int VB, int LB, bool GATED, bool EXPERT, bool QV>
 __global__ void __launch_bounds__(256, GATED ? 3 : 5) quantize_kernel(const Args a)
 {
     constexpr int EV = Vec<T, VB>::N;
@@ -123,7 +140,7 @@ __global__ void __launch_bounds__(256, GATED ? 3 : 5) quantize_kernel(const Args
     const unsigned tx = threadIdx.x, nx = blockDim.x, warps = nx >> 5;
     const unsigned nvec = live ? a.nvec : 0;
 
-    Held<T, VB, GATED> held[kHeld];
+    Held<T, VB, LB, GATED> held[kHeld];
     unsigned big = 0;
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
@@ -138,7 +155,7 @@ __global__ void __launch_bounds__(256, GATED ? 3 : 5) quantize_kernel(const Args
                 big = max(big, __float_as_uint(held[h].get(i)) & 0x7FFFFFFFu);
     for (unsigned v = tx + kHeld * nx; v < nvec; v += nx) {
         float g[EV];
-        load_values<T, VB, GATED>(a, row, v, g);
+        load_values<T, VB, LB, GATED>(a, row, v, g);
 #pragma unroll
         for (int i = 0; i < EV; ++i) big = max(big, __float_as_uint(g[i]) & 0x7FFFFFFFu);
     }
@@ -163,6 +180,8 @@ __global__ void __launch_bounds__(256, GATED ? 3 : 5) quantize_kernel(const Args
             c[i] = finite ? __float_as_int(__fadd_rn(__fmul_rn(x[i], inv), kRound)) : 0;
     };
     auto put = [&](unsigned v, const int (&c)[EV]) {
+        const int n = LB == VB ? EV
+                               : static_cast<int>(bytes_left<T, VB>(a, v) / sizeof(T));
         if constexpr (EXPERT) {
             const int total = *a.total;
             int none[EV] = {};
@@ -171,12 +190,12 @@ __global__ void __launch_bounds__(256, GATED ? 3 : 5) quantize_kernel(const Args
                 if (p < 0 || p >= a.S) continue;
                 signed char *dst = a.q + p * a.ldq + static_cast<long long>(v) * EV;
                 if (p < total)
-                    store_codes<EV, QV>(dst, c);
+                    store_codes<EV, QV>(dst, c, n);
                 else
-                    store_codes<EV, QV>(dst, none);
+                    store_codes<EV, QV>(dst, none, n);
             }
         } else {
-            store_codes<EV, QV>(a.q + r * a.ldq + static_cast<long long>(v) * EV, c);
+            store_codes<EV, QV>(a.q + r * a.ldq + static_cast<long long>(v) * EV, c, n);
         }
     };
 #pragma unroll
@@ -194,7 +213,7 @@ __global__ void __launch_bounds__(256, GATED ? 3 : 5) quantize_kernel(const Args
     for (unsigned v = tx + kHeld * nx; v < nvec; v += nx) {
         float g[EV];
         int c[EV];
-        load_values<T, VB, GATED>(a, row, v, g);
+        load_values<T, VB, LB, GATED>(a, row, v, g);
         codes(g, c);
         put(v, c);
     }
@@ -209,26 +228,30 @@ __global__ void __launch_bounds__(256, GATED ? 3 : 5) quantize_kernel(const Args
 }
 
 struct Launch {
-    const Args &a;
+    const Args &args;
     bool gated, expert;
     cudaStream_t st;
-    template <class T, int VB, bool GATED, bool EXPERT>
+    template <class T, int LB, bool GATED, bool EXPERT>
     int go() const
     {
+        // at least four values a vector: narrower loads make one up
+        constexpr int V4 = 4 * static_cast<int>(sizeof(T)), VB = LB > V4 ? LB : V4;
         constexpr int EV = Vec<T, VB>::N;
+        Args a = args;
+        a.nvec = a.K > 0 ? (static_cast<unsigned>(a.K) - 1) / EV + 1 : 0;
         const bool qv = rows::aligned_to(a.q, EV) && a.ldq % EV == 0;
         const int tx = rows::pow2_threads((a.nvec + kHeld - 1) / kHeld, 32, 256), ty = 256 / tx;
         const dim3 block(static_cast<unsigned>(tx), static_cast<unsigned>(ty));
         const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.M) + ty - 1) / ty));
-        auto kern = qv ? quantize_kernel<T, VB, GATED, EXPERT, true>
-                       : quantize_kernel<T, VB, GATED, EXPERT, false>;
+        auto kern = qv ? quantize_kernel<T, VB, LB, GATED, EXPERT, true>
+                       : quantize_kernel<T, VB, LB, GATED, EXPERT, false>;
         return launch_dependent(kern, grid, block, 0, 1, st, a);
     }
-    template <class T, int VB>
+    template <class T, int LB>
     int run() const
     {
-        if (expert) return go<T, VB, false, true>();
-        return gated ? go<T, VB, true, false>() : go<T, VB, false, false>();
+        if (expert) return go<T, LB, false, true>();
+        return gated ? go<T, LB, true, false>() : go<T, LB, false, false>();
     }
 };
 
@@ -265,7 +288,6 @@ int sgemm_i8_quantize_rows(int type, int act, int M, int K, const void *X, int l
         a.ldq = ldq;
         a.scale = scale;
         const int vb = K == 0 ? 16 : rows::Width().add(X).add(a.x_pitch).add(a.up).bytes();
-        a.nvec = static_cast<unsigned>(K * es / vb);
         return rows::with_vec(type, vb,
                               qz::Launch{a, gated, false, static_cast<cudaStream_t>(stream)});
     });
@@ -304,7 +326,6 @@ int sgemm_experts_dispatch_i8(int type, int T, int k, int E, int H, const void *
         a.k = k;
         a.S = T * k;
         const int vb = H == 0 ? 16 : rows::Width().add(x).add(a.x_pitch).add(H * es).bytes();
-        a.nvec = static_cast<unsigned>(H * es / vb);
         return rows::with_vec(type, vb,
                               qz::Launch{a, false, true, static_cast<cudaStream_t>(stream)});
     });

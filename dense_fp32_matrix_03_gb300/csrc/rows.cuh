@@ -83,6 +83,23 @@ struct Vec {
     {
         raw = *static_cast<const typename Raw<VB>::T *>(p);
     }
+    // In pieces of LB bytes, the first `bytes` of them (a multiple of LB); zeros
+    // for the rest.
+    template <int LB>
+    __device__ __forceinline__ void load_pieces(const char *p, unsigned bytes)
+    {
+        if constexpr (LB == VB) {
+            load(p);
+        } else {
+            using P = typename Raw<LB>::T;
+#pragma unroll
+            for (int i = 0; i < VB / LB; ++i)
+                reinterpret_cast<P *>(&raw)[i] =
+                    static_cast<unsigned>(i * LB) < bytes
+                        ? *reinterpret_cast<const P *>(p + i * LB)
+                        : P{};
+        }
+    }
     __device__ __forceinline__ void store(void *p) const
     {
         *static_cast<typename Raw<VB>::T *>(p) = raw;

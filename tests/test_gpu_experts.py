@@ -249,7 +249,8 @@ def check_codes(q, s, x, slack=127 * 2.0 ** -23, scale_err=2.0 ** -23):
 @pytest.mark.parametrize("type_", TYPES)
 @pytest.mark.parametrize("M,K,pad,offset,qpad", [
     (1, 1, 0, 0, 0), (3, 7, 0, 0, 0), (70, 64, 0, 0, 0), (5, 333, 1, 1, 3), (9, 1500, 4, 0, 4),
-    (2, 4096, 0, 8, 0), (37, 4092, 0, 0, 4), (3, 20000, 0, 0, 0), (300, 40, 0, 2, 9)])
+    (2, 4096, 0, 8, 0), (37, 4092, 0, 0, 4), (3, 20000, 0, 0, 0), (300, 40, 0, 2, 9),
+    (2, 4095, 0, 0, 1), (40, 2002, 0, 0, 14), (6, 2001, 2, 1, 15), (5, 5, 0, 0, 3)])
 @pytest.mark.parametrize("act", ["none", "swiglu"])
 def test_quantize_rows(type_, M, K, pad, offset, qpad, act):
     import torch
