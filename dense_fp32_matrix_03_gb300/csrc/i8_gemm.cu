@@ -209,6 +209,15 @@ int run(const Args &a, cudaStream_t st)
         if (a.M <= 8)
             return once ? launch_few<T, 1, 1, 16, 2>(a, st) : launch_few<T, 1, 1, 8, 4>(a, st);
         if (a.M <= 16 && once) return launch_few<T, 2, 1, 16, 2>(a, st);
+        // 32 tokens a block of 16 warps, likewise where all run at once (against the
+        // kernels chosen below: 64 x 1024 x 4096 8.9 / 6.3, 64 x 1200 x 8192 12.9 /
+        // 8.9, 1024 x 64 x 4096 9.2 / 6.4, 17 x 2048 x 2048 5.9 / 4.8; with more
+        // blocks, 96 x 1024 x 4096 9.2 / 11.5; at shorter k, 64 x 1024 x 1024 3.9 /
+        // 5.4; with few blocks at that, 64 x 256 x 2048 3.2 / 4.5)
+        const long long blocks = (a.N + 15) / 16 * ((a.M + 31LL) / 32);
+        if (a.M > 16 && blocks <= a.num_sms &&
+            (a.K >= 4096 || (a.K >= 2048 && 4 * blocks >= a.num_sms)))
+            return launch_few<T, 4, 1, 16, 1>(a, st);
         const double passes = (a.M + 15) / 16 * (static_cast<double>(a.N) * a.K / 4.8e6);
         const double stores = static_cast<double>(a.M) * a.N / 7.5e4;
         // (a grid holds 65535 token tiles)

@@ -87,7 +87,9 @@ def run_dense(type_, M, N, K, how="pad16", ldc_pad=0, offset=0, seed=0, extreme=
     (1, 1, 1), (1, 4096, 4096), (2, 100, 15), (3, 128, 16), (8, 256, 17), (15, 7, 64), (16, 64, 127),
     (17, 129, 128), (32, 4092, 777), (33, 1500, 129), (37, 4092, 4092), (63, 200, 1024),
     (64, 512, 2048), (65, 257, 256), (128, 384, 640), (129, 1000, 500), (200, 640, 1100),
-    (255, 256, 96), (90, 2121, 448), (700, 2121, 448), (333, 1026, 64), (256, 256, 512), (257, 300, 1000), (513, 2050, 300), (1000, 1500, 777)])
+    (255, 256, 96), (90, 2121, 448), (700, 2121, 448), (333, 1026, 64), (256, 256, 512), (257, 300, 1000), (513, 2050, 300), (1000, 1500, 777),
+    (17, 1500, 2100), (33, 777, 2049), (40, 1000, 4100), (64, 1024, 4097), (1000, 33, 4099),
+    (300, 512, 2048), (40, 256, 2048), (300, 900, 5000)])
 def test_dense_shapes(type_, M, N, K):
     run_dense(type_, M, N, K)
 
