@@ -234,7 +234,7 @@ int run(const Args &a, cudaStream_t st)
     // A tile takes as long as its epilogue (short k) or its multiplies (long k),
     // whichever is longer, us by slots of k; K = 128, 512, 1024, 2048, narrow /
     // wide: 8192 x 8192 71 / 64, 92 / 73, 155 / 103, 286 / 175; 32 experts of
-    // 3840 channels, 99 rows each, 24 / 30, 31 / 36, 48 / 51, 81 / 84, and of
+    // 3840 channels, 99 rows each, 22 / 30, 30 / 36, 48 / 51, 81 / 84, and of
     // 3837 channels, 128 rows each, 40 / 49, 50 / 61, 69 / 66, 113 / 90; fp32,
     // 8192 x 4096, 67 / 40, 78 / 52, - , 154 / 108.
     const double s = k_slots, sn = s / split;

@@ -759,13 +759,43 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const uint32_t st_row = stage + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
         float *sa = reinterpret_cast<float *>(base + C::OFF_SCALE) + w * C::ECOLS;
         Ring<C::ACCS> acc;
+        constexpr bool PACK = sizeof(T) == 2;
+        // Narrow: a tile's place and scales are asked for before the stores of
+        // the tile before, since the waits for them would open every tile
+        // (19000 x 1088 x 128 29 us; so 25).  Wide holds a tile's results in the
+        // registers that would take (8192 x 8192 x 4096 316 us, with it 321).
+        constexpr bool AHEAD = !C::HOLD;
+        constexpr int NSA = C::ECOLS / 32;
+        float nsa[NSA], nsb[4] = {};  // 16 bits: channels lane / 4 + 8 i; else channel lane
+        Job nj{};
+        auto ask_next = [&](int u) {
+            if (u >= tiles) return;
+            const Job j = nj = job<C>(a, table, u, half);
+            if (split > 1) return;
+            const int chq = j.ch0 + q * 32, n = j.n - col0;
+            const float *sp = a.scaleB + static_cast<long long>(j.e) * a.N + chq;
+#pragma unroll
+            for (int i = 0; i < NSA; ++i)
+                nsa[i] = lane + 32 * i < n ? a.scaleA[j.row0 + col0 + lane + 32 * i] : 0.f;
+#pragma unroll
+            for (int i = 0; i < (PACK ? 4 : 1); ++i) {
+                const int c = PACK ? 8 * i + (lane >> 2) : lane;
+                nsb[i] = chq + c < a.N ? sp[c] : 0.f;
+            }
+        };
+        if (AHEAD) ask_next(cid);
         for (int u = cid; u < tiles; u += ncl) {
-            const Job j = job<C>(a, table, u, half);
+            const Job j = AHEAD ? nj : job<C>(a, table, u, half);
             const int chq = j.ch0 + q * 32;        // this warp's first channel
             const int n = min(j.n - col0, C::ECOLS);
-            constexpr bool PACK = sizeof(T) == 2;
-            float sb[4] = {};  // 16 bits: rows lane / 4 + 8 i; else row lane
-            if (split == 1) {
+            float sb[4] = {};
+            if (AHEAD && split == 1) {
+#pragma unroll
+                for (int i = 0; i < NSA; ++i) sa[lane + 32 * i] = nsa[i];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sb[i] = nsb[i];
+                __syncwarp();
+            } else if (split == 1) {
                 const float *sp = a.scaleB + static_cast<long long>(j.e) * a.N;
                 for (int i = lane; i < C::ECOLS; i += 32)
                     sa[i] = i < n ? a.scaleA[j.row0 + col0 + i] : 0.f;
@@ -892,6 +922,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 acc.next();
                 continue;
             }
+            if (AHEAD) ask_next(u + ncl);
 #pragma unroll 1
             for (int c0 = 0; c0 < n; c0 += 32) {
                 if (PACK && split == 1) {
