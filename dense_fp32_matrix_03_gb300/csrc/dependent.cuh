@@ -14,7 +14,8 @@ namespace sg {
 // Every thread, before its first access to global memory: the kernels before
 // this one have completed and their writes are visible.  (Every thread, also
 // of blocks without work: a kernel that completed without waiting would let
-// the one after it overtake the one before.)
+// the one after it overtake the one before.)  What the kernels before write is
+// read by ordinary loads: no __ldg, no const pointer declared __restrict__.
 __device__ __forceinline__ void dependent_wait()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -69,7 +69,9 @@ __device__ __forceinline__ int cluster_load(const int *p, int rank)
 }
 
 // The keys of this lane's choices i, i + 32, ... (dropped: E; past the
-// segment: -1), all on their way at once.
+// segment: -1), all on their way at once.  (No pointer here is __restrict__:
+// the router may still write ids when the kernel starts, and a const pointer
+// so declared allows loads that are defined for unchanging memory only.)
 __device__ __forceinline__ void load_keys(int (&key)[kSortAhead], const int *ids, long long i,
                                           long long hi, int E)
 {
@@ -81,8 +83,7 @@ __device__ __forceinline__ void load_keys(int (&key)[kSortAhead], const int *ids
 }
 
 __global__ void __launch_bounds__(kSortThreads, 1)
-    sort_kernel(const int *__restrict__ ids, int S, int E, int *__restrict__ offsets,
-                int *__restrict__ slots, int *__restrict__ positions)
+    sort_kernel(const int *ids, int S, int E, int *offsets, int *slots, int *positions)
 {
     extern __shared__ int sm[];
     const int E1 = E + 1;

@@ -41,9 +41,12 @@ __device__ __forceinline__ uint4 load_tail(const signed char *row, int k, int K)
                 w[i] |= (static_cast<uint32_t>(row[k + 4 * i + b]) & 255u) << (8 * b);
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// (An ordinary load: the kernel before may still write the operands when this
+// one starts, and a read-only load is defined for memory that stays as it is
+// while the kernel lives.)
 __device__ __forceinline__ uint4 load_row(const signed char *p)
 {
-    return __ldg(reinterpret_cast<const uint4 *>(p));
+    return *reinterpret_cast<const uint4 *>(p);
 }
 
 // Dense calls: asks L2 for the weights of `ch` channels from n0 on, a line of
