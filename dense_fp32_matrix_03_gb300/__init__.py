@@ -47,6 +47,16 @@ SGEMM_ACT_NONE = 0
 SGEMM_ACT_SWIGLU = 1
 ACTS = {"none": SGEMM_ACT_NONE, "swiglu": SGEMM_ACT_SWIGLU}
 
+SGEMM_I8_KERNEL_AUTO = 0
+SGEMM_I8_KERNEL_DOTS = 1
+SGEMM_I8_KERNEL_FEW = 2
+SGEMM_I8_KERNEL_NARROW = 3
+SGEMM_I8_KERNEL_WIDE = 4
+SGEMM_I8_KERNEL_ANY_LAYOUT = 5
+I8_KERNELS = {"auto": SGEMM_I8_KERNEL_AUTO, "dots": SGEMM_I8_KERNEL_DOTS,
+              "few": SGEMM_I8_KERNEL_FEW, "narrow": SGEMM_I8_KERNEL_NARROW,
+              "wide": SGEMM_I8_KERNEL_WIDE, "any_layout": SGEMM_I8_KERNEL_ANY_LAYOUT}
+
 SGEMM_ROUTE_AUTO = 0
 SGEMM_ROUTE_SMALL = 1
 SGEMM_ROUTE_PAIR = 2
@@ -105,6 +115,9 @@ SIGNATURES = {
     "sgemm_i8_quantize_rows": (_i, [_i, _i, _i, _i, _p, _i, _p, _i, _p, _p]),
     "sgemm_i8": (_i, [_i, _i, _i, _i, _p, _i, _p, _p, _i, _p, _p, _i, _p]),
     "sgemm_i8_experts": (_i, [_i, _i, _i, _i, _i, _p, _p, _i, _p, _p, _i, _ll, _p, _p, _i, _p]),
+    "sgemm_i8_tune_force": (_i, [_i]),
+    "sgemm_i8_last_kernel": (_i, []),
+    "sgemm_i8_last_split_count": (_i, []),
     # include/expert_layer.h
     "sgemm_experts_sort": (_i, [_i, _i, _i, _p, _p, _p, _p, _p]),
     "sgemm_experts_dispatch": (_i, [_i, _i, _i, _i, _i, _p, _i, _p, _p, _p, _i, _p]),
@@ -394,6 +407,22 @@ def sgemm_i8_experts(type_, M, N, K, E, offsets, A, lda, scaleA, B, ldb, strideB
     return _lib.sgemm_i8_experts(_type(type_), M, N, K, E, _ptr(offsets), _ptr(A), lda,
                                  _ptr(scaleA), _ptr(B), ldb, strideB, _ptr(scaleB), _ptr(C), ldc,
                                  _stream(stream))
+
+
+def sgemm_i8_tune_force(kernel) -> int:
+    """Process-wide forced kernel of the products (tests and measurement; see
+    include/int8_gemm.h)."""
+    if isinstance(kernel, str):
+        kernel = I8_KERNELS[kernel]
+    return _lib.sgemm_i8_tune_force(kernel)
+
+
+def sgemm_i8_last_kernel() -> int:
+    return _lib.sgemm_i8_last_kernel()
+
+
+def sgemm_i8_last_split_count() -> int:
+    return _lib.sgemm_i8_last_split_count()
 
 
 # ---- tokens to experts and back (include/expert_layer.h)

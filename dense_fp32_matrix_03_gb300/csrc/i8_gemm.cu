@@ -108,7 +108,7 @@ int launch_dot(const Args &a, cudaStream_t st)
     return SGEMM_OK;
 }
 
-// ------------------------------------------------- the kernel for a call
+// ------------------------------------------------- what a call looks like
 
 // Whether the tensor-core kernel can read the operands: rows on 16-byte
 // boundaries.
@@ -166,6 +166,51 @@ int narrow_room(int size, int num_sms)
     return n;
 }
 
+// ------------------------------------------------- the kernel for a call
+
+// The kernel every later call is made to take (sgemm_i8_tune_force), and the
+// kernel and split of the last product enqueued.
+std::atomic<int> g_force{SGEMM_I8_KERNEL_AUTO};
+std::atomic<int> g_last_kernel{SGEMM_I8_KERNEL_AUTO}, g_last_split{1};
+
+void note_product(int kernel, int split)
+{
+    g_last_kernel.store(kernel, std::memory_order_relaxed);
+    g_last_split.store(split, std::memory_order_relaxed);
+}
+
+// The few-token kernel's form for a dense call.
+struct FewForm {
+    bool once;   // blocks of 16 warps: all of them run at once, with two steps or
+                 // more of k a warp (8 / 16 warps: 16 x 4096 x 4096 9.1 / 6.2,
+                 // 16 x 8192 x 8192 21.1 / 21.9, 16 x 1024 x 1024 2.6 / 3.4)
+    bool large;  // 32 tokens a block of 16 warps, likewise where all run at once
+                 // (against the kernels chosen otherwise: 64 x 1024 x 4096 8.9 /
+                 // 6.3, 64 x 1200 x 8192 12.9 / 8.9, 1024 x 64 x 4096 9.2 / 6.4,
+                 // 17 x 2048 x 2048 5.9 / 4.8; with more blocks, 96 x 1024 x 4096
+                 // 9.2 / 11.5; at shorter k, 64 x 1024 x 1024 3.9 / 5.4; with few
+                 // blocks at that, 64 x 256 x 2048 3.2 / 4.5)
+    explicit FewForm(const Args &a)
+    {
+        const long long blocks = (a.N + 15) / 16 * ((a.M + 31LL) / 32);
+        once = a.K >= 2048 && a.N <= 2LL * a.num_sms * 16;
+        large = a.M > 16 && blocks <= a.num_sms &&
+                (a.K >= 4096 || (a.K >= 2048 && 4 * blocks >= a.num_sms));
+    }
+};
+
+template <class T>
+int launch_few_tokens(const Args &a, cudaStream_t st)
+{
+    if (a.offsets != nullptr) return launch_few<T, 1, 2, 4, 6>(a, st);
+    const FewForm form(a);
+    if (a.M <= 8)
+        return form.once ? launch_few<T, 1, 1, 16, 2>(a, st) : launch_few<T, 1, 1, 8, 4>(a, st);
+    if (a.M <= 16 && form.once) return launch_few<T, 2, 1, 16, 2>(a, st);
+    if (form.large) return launch_few<T, 4, 1, 16, 1>(a, st);
+    return launch_few<T, 2, 1, 8, 4>(a, st);
+}
+
 template <class T>
 int run(const Args &a, cudaStream_t st)
 {
@@ -173,14 +218,23 @@ int run(const Args &a, cudaStream_t st)
     alignas(64) CUtensorMap tmT;
     std::memset(&tmW, 0, sizeof(tmW));
     std::memset(&tmT, 0, sizeof(tmT));
-    if (a.K == 0 || !rows_on_16(a) ||
+    const int forced = g_force.load(std::memory_order_relaxed);
+    if (a.K == 0 || !rows_on_16(a) || forced == SGEMM_I8_KERNEL_ANY_LAYOUT ||
         !encode_operand8(&tmW, a.B, a.N, a.K, a.ldb, a.E, a.strideB, kCh) ||
-        !encode_operand8(&tmT, a.A, a.M, a.K, a.lda, 1, 0, kBoxRows))
+        !encode_operand8(&tmT, a.A, a.M, a.K, a.lda, 1, 0, kBoxRows)) {
+        note_product(SGEMM_I8_KERNEL_ANY_LAYOUT, 1);
         return launch_dot<T>(a, st);
+    }
     const int c_bytes = rows::Width().add(a.C).add(a.ldc * sizeof(T)).bytes();
     const int k_slots = (a.K + kSlotK - 1) / kSlotK;
     const int pairs = ss_slots(a.num_sms);
     const bool dense = a.offsets == nullptr;
+    const bool dots_can = dense && a.M <= 4;
+    // (a grid holds 65535 token tiles, of 8 rows by expert, of 16 or more else)
+    const bool few_can = dense ? a.M <= 16 * 65535 : max_tiles(a, 8) <= 65535;
+    int kernel = forced;
+    if ((kernel == SGEMM_I8_KERNEL_DOTS && !dots_can) || (kernel == SGEMM_I8_KERNEL_FEW && !few_can))
+        kernel = SGEMM_I8_KERNEL_AUTO;
 
     // The kernels' times in us, as measured on GB300 (bf16; M x N x K):
     //   few     2.9 us and a pass over the weights per 16 tokens, from HBM or
@@ -198,38 +252,20 @@ int run(const Args &a, cudaStream_t st)
     while (split < 8 && narrow_tiles <= narrow_room(2 * split, a.num_sms) && k_slots >= 4 * split)
         split *= 2;
     const double narrow_waves = ceil(narrow_tiles * split / a.num_sms) / split;
-    if (dense) {
-        if (a.M == 1) return launch_dots<T, 1>(a, st);
-        if (a.M == 2) return launch_dots<T, 2>(a, st);
-        if (a.M <= 4) return launch_dots<T, 4>(a, st);
-        // blocks of 16 warps where all of them run at once, with two steps or
-        // more of k a warp; 8 otherwise (8 / 16 warps: 16 x 4096 x 4096 9.1 /
-        // 6.2, 16 x 8192 x 8192 21.1 / 21.9, 16 x 1024 x 1024 2.6 / 3.4)
-        const bool once = a.K >= 2048 && a.N <= 2LL * a.num_sms * 16;
-        if (a.M <= 8)
-            return once ? launch_few<T, 1, 1, 16, 2>(a, st) : launch_few<T, 1, 1, 8, 4>(a, st);
-        if (a.M <= 16 && once) return launch_few<T, 2, 1, 16, 2>(a, st);
-        // 32 tokens a block of 16 warps, likewise where all run at once (against the
-        // kernels chosen below: 64 x 1024 x 4096 8.9 / 6.3, 64 x 1200 x 8192 12.9 /
-        // 8.9, 1024 x 64 x 4096 9.2 / 6.4, 17 x 2048 x 2048 5.9 / 4.8; with more
-        // blocks, 96 x 1024 x 4096 9.2 / 11.5; at shorter k, 64 x 1024 x 1024 3.9 /
-        // 5.4; with few blocks at that, 64 x 256 x 2048 3.2 / 4.5)
-        const long long blocks = (a.N + 15) / 16 * ((a.M + 31LL) / 32);
-        if (a.M > 16 && blocks <= a.num_sms &&
-            (a.K >= 4096 || (a.K >= 2048 && 4 * blocks >= a.num_sms)))
-            return launch_few<T, 4, 1, 16, 1>(a, st);
-        const double passes = (a.M + 15) / 16 * (static_cast<double>(a.N) * a.K / 4.8e6);
-        const double stores = static_cast<double>(a.M) * a.N / 7.5e4;
-        // (a grid holds 65535 token tiles)
-        if (a.M <= 16 ||
-            (a.M <= 16 * 65535 &&
-             2.9 + (passes > stores ? passes : stores) <
-                             (split > 1 ? 5. : 3.4) + 0.8 * narrow_waves * k_slots))
-            return launch_few<T, 2, 1, 8, 4>(a, st);
-    } else if (a.M <= 16LL * a.E) {
-        // 32 experts of 2048 x 2048, few / narrow: 8 rows each 30 / 46 us, 12
-        // rows 36 / 46 us, 16 rows 43 / 47
-        return launch_few<T, 1, 2, 4, 6>(a, st);
+    if (kernel == SGEMM_I8_KERNEL_AUTO && dots_can) kernel = SGEMM_I8_KERNEL_DOTS;
+    if (kernel == SGEMM_I8_KERNEL_AUTO && few_can) {
+        if (dense) {
+            const double passes = (a.M + 15) / 16 * (static_cast<double>(a.N) * a.K / 4.8e6);
+            const double stores = static_cast<double>(a.M) * a.N / 7.5e4;
+            if (a.M <= 16 || FewForm(a).large ||
+                2.9 + (passes > stores ? passes : stores) <
+                    (split > 1 ? 5. : 3.4) + 0.8 * narrow_waves * k_slots)
+                kernel = SGEMM_I8_KERNEL_FEW;
+        } else if (a.M <= 16LL * a.E) {
+            // 32 experts of 2048 x 2048, few / narrow: 8 rows each 30 / 46 us, 12
+            // rows 36 / 46 us, 16 rows 43 / 47
+            kernel = SGEMM_I8_KERNEL_FEW;
+        }
     }
     // A tile takes as long as its epilogue (short k) or its multiplies (long k),
     // whichever is longer, us by slots of k; K = 128, 512, 1024, 2048, narrow /
@@ -237,21 +273,32 @@ int run(const Args &a, cudaStream_t st)
     // 3840 channels, 99 rows each, 22 / 30, 30 / 36, 48 / 51, 81 / 84, and of
     // 3837 channels, 128 rows each, 40 / 49, 50 / 61, 69 / 66, 113 / 90; fp32,
     // 8192 x 4096, 67 / 40, 78 / 52, - , 154 / 108.
-    const double s = k_slots, sn = s / split;
-    const bool fp32 = sizeof(T) == 4, odd = c_bytes < 8 && !fp32;
-    const double narrow_end = fp32 ? 4.1 + 0.27 * sn : odd ? 2.9 + 0.28 * sn : 2.2 + 0.25 * sn;
-    const double narrow_mma = 0.8 + 0.6 * sn;
-    const double wide_end = fp32 ? 4.6 + 0.5 * s : odd ? 6.0 + 0.4 * s : 4.2 + 0.2 * s;
-    const double wide_mma = 1.9 + (fp32 ? 0.8 : 0.63) * s;
-    const double narrow_cost = (narrow_end > narrow_mma ? narrow_end : narrow_mma) *
-                                   ceil(narrow_tiles * split / a.num_sms) +
-                               (split > 1 ? 1.6 : 0.);
-    const double wide_cost =
-        (wide_end > wide_mma ? wide_end : wide_mma) * ceil(wide_tiles / pairs) + 0.8;
-    // (experts of unknown counts: narrow where it is clearly ahead, since more of
-    // its tiles may turn out to be needed: 60 experts of 200 rows x 1536 x 128
-    // 37 / 27)
-    if ((dense ? 1. : 0.9) * wide_cost < narrow_cost) {
+    if (kernel == SGEMM_I8_KERNEL_AUTO) {
+        const double s = k_slots, sn = s / split;
+        const bool fp32 = sizeof(T) == 4, odd = c_bytes < 8 && !fp32;
+        const double narrow_end = fp32 ? 4.1 + 0.27 * sn : odd ? 2.9 + 0.28 * sn : 2.2 + 0.25 * sn;
+        const double narrow_mma = 0.8 + 0.6 * sn;
+        const double wide_end = fp32 ? 4.6 + 0.5 * s : odd ? 6.0 + 0.4 * s : 4.2 + 0.2 * s;
+        const double wide_mma = 1.9 + (fp32 ? 0.8 : 0.63) * s;
+        const double narrow_cost = (narrow_end > narrow_mma ? narrow_end : narrow_mma) *
+                                       ceil(narrow_tiles * split / a.num_sms) +
+                                   (split > 1 ? 1.6 : 0.);
+        const double wide_cost =
+            (wide_end > wide_mma ? wide_end : wide_mma) * ceil(wide_tiles / pairs) + 0.8;
+        // (experts of unknown counts: narrow where it is clearly ahead, since more of
+        // its tiles may turn out to be needed: 60 experts of 200 rows x 1536 x 128
+        // 37 / 27)
+        kernel = (dense ? 1. : 0.9) * wide_cost < narrow_cost ? SGEMM_I8_KERNEL_WIDE
+                                                              : SGEMM_I8_KERNEL_NARROW;
+    }
+    note_product(kernel, kernel == SGEMM_I8_KERNEL_NARROW ? split : 1);
+    if (kernel == SGEMM_I8_KERNEL_DOTS) {
+        if (a.M == 1) return launch_dots<T, 1>(a, st);
+        if (a.M == 2) return launch_dots<T, 2>(a, st);
+        return launch_dots<T, 4>(a, st);
+    }
+    if (kernel == SGEMM_I8_KERNEL_FEW) return launch_few_tokens<T>(a, st);
+    if (kernel == SGEMM_I8_KERNEL_WIDE) {
         const long long tiles = max_tiles(a, Wide::NT) * ((a.N + 2 * kCh - 1) / (2 * kCh));
         return launch_tc_i8<Wide, T>(a, tmW, tmT, tiles < pairs ? tiles : pairs, 1, c_bytes, st);
     }
@@ -301,6 +348,18 @@ int product(int type, int M, int N, int K, int E, const int *offsets, const sign
 }  // namespace sg
 
 extern "C" {
+
+int sgemm_i8_tune_force(int kernel)
+{
+    if (kernel < SGEMM_I8_KERNEL_AUTO || kernel > SGEMM_I8_KERNEL_ANY_LAYOUT)
+        return SGEMM_ERR_INVALID_ARG;
+    sg::i8::g_force.store(kernel);
+    return SGEMM_OK;
+}
+
+int sgemm_i8_last_kernel(void) { return sg::i8::g_last_kernel.load(); }
+
+int sgemm_i8_last_split_count(void) { return sg::i8::g_last_split.load(); }
 
 int sgemm_i8(int type, int M, int N, int K, const signed char *A, int lda, const float *scaleA,
              const signed char *B, int ldb, const float *scaleB, void *C, int ldc, void *stream)

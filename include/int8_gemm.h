@@ -80,6 +80,31 @@ int sgemm_i8_experts(int type, int M, int N, int K, int E, const int *offsets,
                      int ldb, long long strideB, const float *scaleB, void *C, int ldc,
                      void *stream);
 
+/* Hooks for tests and measurement.  A product runs on one of five kernels,
+ * chosen by a rule on its sizes, type and alignment:
+ *   DOTS        up to four tokens, dense: integer dot products
+ *   FEW         few tokens
+ *   NARROW      tensor cores, 128 channels x 128 tokens a CTA; the CTAs of a
+ *               cluster may share a tile's k ("split")
+ *   WIDE        tensor cores, 256 channels x 256 tokens a CTA pair
+ *   ANY_LAYOUT  rows off 16 bytes, and K == 0
+ * sgemm_i8_tune_force(kernel) makes every later product in the process take
+ * that kernel (AUTO: the rule again; a product the kernel cannot take follows
+ * the rule); SGEMM_ERR_INVALID_ARG for an unknown one.  It is a process-wide
+ * setting: do not change it while other threads call the library.
+ * sgemm_i8_last_kernel and sgemm_i8_last_split_count return the kernel and the
+ * CTAs that share a tile's k of the most recent product enqueued in this
+ * process, racy across threads that call at the same time. */
+#define SGEMM_I8_KERNEL_AUTO 0
+#define SGEMM_I8_KERNEL_DOTS 1
+#define SGEMM_I8_KERNEL_FEW 2
+#define SGEMM_I8_KERNEL_NARROW 3
+#define SGEMM_I8_KERNEL_WIDE 4
+#define SGEMM_I8_KERNEL_ANY_LAYOUT 5
+int sgemm_i8_tune_force(int kernel);
+int sgemm_i8_last_kernel(void);
+int sgemm_i8_last_split_count(void);
+
 #ifdef __cplusplus
 }
 #endif
