@@ -18,10 +18,17 @@
  *
  * Arithmetic: the quantiser works in fp32 (IEEE division and product).  The
  * product's sum is exact while the sum of |A||B| over k stays within 2^24
- * (always for K <= 1024); beyond that it is accumulated in fp32 on the
- * tensor cores, with at most a relative 2^-23 of the running sum lost per 16
- * values of k.  The scales are applied in fp32 (token first) and the result
- * is rounded once to its type.
+ * (always for K <= 1024).  Beyond that dense calls of up to four tokens, and
+ * operands off 16 bytes, still add integers exactly and round once; all other
+ * calls add in fp32 on the matrix units, where each 16 values of k may lose
+ * 5 * 2^-23 of the largest partial sum, always towards zero: products are cut
+ * two bits below fp32's last place of the largest number added, sums at it.
+ * (Partial sums within 2^26 lose nothing but their own last place.  The most
+ * that was measured, on rows of equal codes 127 times 97: 3e-5 of the sum at
+ * K = 8192, 1e-4 at 16384, 1.4e-3 at 131056.  Sums of both signs rarely leave
+ * 2^24.)  The same row may so give slightly different results in calls of
+ * other sizes.  The scales are applied in fp32 (token first) and the result is
+ * rounded once to its type.
  *
  * Errors: SGEMM_ERR_INVALID_ARG (dimensions, leading dimensions, type, NULL
  * where data is read or written, pointers not aligned to their type) before
