@@ -25,8 +25,10 @@ struct Args {
 };
 
 // At most this many token tiles of `tm` rows: every expert may end in a
-// short one, but none has one without a row.
-inline long long max_tiles(const Args &a, int tm)
+// short one, but none has one without a row.  (Of ascending offsets.  Others
+// may give several experts the same rows; tiles from this number on are left
+// out then, in every kernel.)
+__host__ __device__ inline long long max_tiles(const Args &a, int tm)
 {
     if (a.offsets == nullptr) return (static_cast<long long>(a.M) + tm - 1) / tm;
     return a.M / tm + (a.E < a.M ? a.E : a.M);

@@ -517,7 +517,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     dependent_wait();
     if (warp == 2) {  // the tile table
+        // (cut at the most that ascending offsets have: what descending ones add
+        // up to need not fit an int, and a cluster that shares k has one tile;
+        // C bounds `most` and 32 experts' tiles far below 2^31)
         const int cts = (a.N + kCh * CG - 1) / (kCh * CG);
+        const int most = static_cast<int>(max_tiles(a, C::NT) * cts);
         int sum = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             int lo = 0, hi = 0;
@@ -529,8 +533,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const int x = __shfl_up_sync(0xffffffffu, inc, d);
                 if (lane >= d) inc += x;
             }
-            if (e0 + lane < a.E) table[e0 + lane] = sum + inc - n;
-            sum += __shfl_sync(0xffffffffu, inc, 31);
+            if (e0 + lane < a.E) table[e0 + lane] = min(sum + inc - n, most);
+            sum = min(sum + __shfl_sync(0xffffffffu, inc, 31), most);
         }
         if (lane == 0) table[a.E] = sum;
     }

@@ -243,6 +243,33 @@ def test_one_expert_has_every_row(forced, kernel):
     experts(kernel, "bf16", [0] * 40 + [1000] + [0] * 23, 200, 300, 24)
 
 
+@pytest.mark.parametrize("K", [64, 1104])
+@pytest.mark.parametrize("kernel,tm", [("few", 8), ("narrow", 128), ("wide", 256),
+                                       ("any_layout", 64)])
+def test_offsets_that_descend(forced, kernel, tm, K):
+    """Experts 0, 2, 4 and 6 have all rows, the others none.  Every kernel works
+    off as many tiles as ascending offsets can need, in the experts' order, and
+    leaves out the rest: a row holds one of these experts' whole results."""
+    import torch
+    import dense_fp32_matrix_03_gb300 as lib
+    E, M, N = 8, 1024, 128
+    a = torch.ones(M, K, dtype=torch.int8, device="cuda")
+    b = torch.arange(1, E + 1, dtype=torch.int8, device="cuda")[:, None, None].repeat(1, N, K)
+    one = torch.ones(max(M, E * N), device="cuda")
+    pad = 4096
+    c = torch.full((M * N + 2 * pad,), 7.0, device="cuda")
+    off = torch.tensor([0, M] * (E // 2) + [0], dtype=torch.int32, device="cuda")
+    forced(kernel)
+    assert lib.sgemm_i8_experts("fp32", M, N, K, E, off, a, K, one, b, K, N * K, one,
+                                c.data_ptr() + pad * 4, N) == lib.SGEMM_OK
+    ran(kernel)
+    assert bool((c[:pad] == 7).all() and (c[pad + M * N:] == 7).all())
+    worked = [e for i, e in enumerate(range(0, E, 2)) if i * (M // tm) < M // tm + E]
+    allowed = torch.tensor([K * (e + 1.0) for e in worked], device="cuda")
+    rows = c[pad:pad + M * N].view(M, N)
+    assert bool((rows[:, :, None] == allowed).any(2).all())
+
+
 @pytest.mark.parametrize("kernel", TILED)
 def test_weights_beyond_32_bit_offsets(forced, kernel):
     """Experts' weights of more than 2^31 bytes; results checked in the last."""
