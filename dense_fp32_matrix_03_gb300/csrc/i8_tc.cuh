@@ -442,8 +442,9 @@ __device__ __forceinline__ Job job(const Args &a, const int *table, int u, uint3
 
 // tmW: the weights (K, N, E) in boxes of 128 k by 128 channels, tmT: the
 // tokens (K, M) in boxes of 128 k by 32 rows, both in the 128-byte swizzle.
-// (A box past an expert's last token holds the next expert's: their columns
-// of the result are not stored.)  split: CTAs of the cluster that share a tile's k (narrow only);
+// (A box past an expert's last token holds the next expert's or, past the last
+// expert, rows that are no one's -- at most 47, where a pair's second half of
+// 16 tokens takes a box of 32: their columns of the result are not stored.)  split: CTAs of the cluster that share a tile's k (narrow only);
 // then each cluster has one tile.  c_bytes: accesses that C's rows allow
 // (16, 8 or fewer).
 template <class C, class T>

@@ -81,8 +81,11 @@ int sgemm_i8(int type, int M, int N, int K, const signed char *A, int lda, const
  * scaleB[e * N + n], to the same rows of C.  offsets (E + 1 values, DEVICE)
  * is read on the GPU: the host needs no counts.  Its values are cut to 0 .. M;
  * where they descend, experts have rows in common, and such a row gets the
- * result of one of them or is left as it is.  Rows from offsets[E] on are
- * neither read nor written.  1 <= E <= 1024; strideB >= (N-1) * ldb + K; the
+ * result of one of them or is left as it is.  Rows from offsets[E] on are not
+ * written, nothing that they hold reaches a result, and their scales are not
+ * read; their codes may be (the tensor cores fetch whole boxes of tokens: up to
+ * 47 rows past the last one, within M), so another stream may fill them
+ * meanwhile, but not free them.  1 <= E <= 1024; strideB >= (N-1) * ldb + K; the
  * tensor cores need strideB a multiple of 16 as well. */
 int sgemm_i8_experts(int type, int M, int N, int K, int E, const int *offsets,
                      const signed char *A, int lda, const float *scaleA, const signed char *B,

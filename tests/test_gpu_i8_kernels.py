@@ -243,6 +243,33 @@ def test_one_expert_has_every_row(forced, kernel):
     experts(kernel, "bf16", [0] * 40 + [1000] + [0] * 23, 200, 300, 24)
 
 
+@pytest.mark.parametrize("kernel", TILED + ["any_layout"])
+def test_rows_past_the_last_expert_reach_nothing(forced, kernel):
+    """Bit for bit the same results whatever codes and scales stand there."""
+    import torch
+    import dense_fp32_matrix_03_gb300 as lib
+    N, K, tail = 200, 300, 60
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(10)
+    rnd = lambda *s: torch.randint(-128, 128, s, device="cuda", dtype=torch.int8, generator=gen)
+    for counts in ([1], [33, 65], [256, 0, 129]):
+        E, M = len(counts), sum(counts) + tail
+        off = torch.tensor([0, *np.cumsum(counts)], dtype=torch.int32, device="cuda")
+        a, b, ld = rnd(M, 304), rnd(E, N, 304), 304
+        sa, sb = torch.rand(M, device="cuda", generator=gen), torch.ones(E, N, device="cuda")
+        forced(kernel)
+        results = []
+        for code, scale in ((-128, float("nan")), (127, float("inf")), (0, 1.0)):
+            a[M - tail:], sa[M - tail:] = code, scale
+            c = torch.full((M, N), 7.0, device="cuda")
+            assert lib.sgemm_i8_experts("fp32", M, N, K, E, off, a, ld, sa, b, ld, N * ld, sb, c,
+                                        N) == lib.SGEMM_OK
+            ran(kernel)
+            assert bool((c[M - tail:] == 7).all())
+            results.append(c)
+        assert torch.equal(results[0], results[1]) and torch.equal(results[0], results[2])
+
+
 @pytest.mark.parametrize("K", [64, 1104])
 @pytest.mark.parametrize("kernel,tm", [("few", 8), ("narrow", 128), ("wide", 256),
                                        ("any_layout", 64)])
