@@ -19,8 +19,9 @@
  *
  * Rows of dropped choices are never read: what they hold, NaN included, does
  * not reach a result.  A token whose choices are all dropped gets a row of
- * zeros.  Sums are fp32, in the order of j (of h for dw, fixed by the shape:
- * repeated calls give the same bits), rounded once to the row type.
+ * zeros.  Sums are fp32, in the order of j, rounded once to the row type; dw's
+ * over h in an order fixed by the sizes and the alignment of all rows: repeated
+ * calls give the same bits, calls on rows aligned differently may not.
  *
  * All matrices are row-major with leading dimensions in elements (>= H);
  * slots and positions have T * k entries, offsets E + 1; weights and dweights
