@@ -13,8 +13,6 @@ namespace ex {
 using rows::aligned_to;
 using rows::Vec;
 
-constexpr int kMaxExperts = 1024;
-constexpr int kMaxChoices = 64;   // k
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortAhead = 8;     // steps of a warp's walk loaded at once
 // Choices of a token whose rows are in flight together.  Four, on blocks small
@@ -495,12 +493,6 @@ struct Launch {
     }
 };
 
-bool dims_ok(int T, int k, int E)
-{
-    return T >= 0 && k >= 1 && k <= kMaxChoices && E >= 1 && E <= kMaxExperts &&
-           static_cast<long long>(T) * k <= 0x7FFFFFFFLL;
-}
-
 }  // namespace ex
 }  // namespace sg
 
@@ -511,7 +503,7 @@ namespace {
 
 bool int_aligned(const void *p) { return rows::aligned_to(p, 4); }
 
-// The checks every row call shares; ok = false: return rc as it is.
+// The checks every row call shares; run = false: return rc as it is.
 struct Checked {
     int rc;
     bool run;
@@ -519,7 +511,7 @@ struct Checked {
 Checked check_rows(int type, int T, int k, int E, int H, const void *tok, int ld_tok,
                    const void *row, int ld_row, const int *positions, const int *offsets)
 {
-    if (!rows::valid_type(type) || !ex::dims_ok(T, k, E) || H < 0 || ld_tok < 1 || ld_row < 1 ||
+    if (!rows::valid_type(type) || !choices_ok(T, k, E) || H < 0 || ld_tok < 1 || ld_row < 1 ||
         ld_tok < H || ld_row < H)
         return {SGEMM_ERR_INVALID_ARG, false};
     if (T == 0) return {SGEMM_OK, false};
@@ -579,7 +571,7 @@ int sgemm_experts_sort(int T, int k, int E, const int *ids, int *offsets, int *s
                        int *positions, void *stream)
 {
     return c_entry([&]() -> int {
-        if (!ex::dims_ok(T, k, E) || offsets == nullptr || !int_aligned(offsets))
+        if (!choices_ok(T, k, E) || offsets == nullptr || !int_aligned(offsets))
             return SGEMM_ERR_INVALID_ARG;
         const int S = T * k;
         if (S > 0 && (ids == nullptr || slots == nullptr || positions == nullptr ||

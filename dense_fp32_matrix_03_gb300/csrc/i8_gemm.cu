@@ -376,7 +376,7 @@ int sgemm_i8_experts(int type, int M, int N, int K, int E, const int *offsets,
                      void *stream)
 {
     return sg::c_entry([&]() -> int {
-        if (E < 1 || E > sg::i8::kMaxExperts || offsets == nullptr ||
+        if (E < 1 || E > sg::kMaxExperts || offsets == nullptr ||
             !sg::rows::aligned_to(offsets, 4) || strideB < 0 ||
             (E > 1 && N > 0 && strideB < (N - 1LL) * ldb + K))
             return SGEMM_ERR_INVALID_ARG;

@@ -4,10 +4,11 @@
 
 #include <cuda_runtime.h>
 
+#include "rows.cuh"
+
 namespace sg {
 namespace i8 {
 
-constexpr int kMaxExperts = 1024;
 constexpr int kMaxK = 131071;  // 2^14 * K < 2^31: the 32-bit integer sums cannot overflow
 constexpr int kMaxSide = 0x7FFFFFFF - 511;  // an index a tile past the last row or channel still is an int
 

@@ -298,9 +298,8 @@ int sgemm_experts_dispatch_i8(int type, int T, int k, int E, int H, const void *
                               float *scale, void *stream)
 {
     return c_entry([&]() -> int {
-        if (!rows::valid_type(type) || T < 0 || k < 1 || k > 64 || E < 1 || E > 1024 ||
-            static_cast<long long>(T) * k > 0x7FFFFFFFLL || H < 0 || ldx < 1 || ldq < 1 || ldx < H ||
-            ldq < H)
+        if (!rows::valid_type(type) || !choices_ok(T, k, E) || H < 0 || ldx < 1 || ldq < 1 ||
+            ldx < H || ldq < H)
             return SGEMM_ERR_INVALID_ARG;
         if (T == 0) return SGEMM_OK;
         const long long es = rows::elem_size(type);

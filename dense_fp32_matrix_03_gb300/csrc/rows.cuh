@@ -1,6 +1,6 @@
 // rows.cuh -- rows of bf16, fp16 or fp32 values moved in vectors of 2 to 16
 // bytes, and the host-side choice of the vector: shared by the row kernels
-// (experts.cu, quant.cu).
+// (experts.cu, quant.cu); the expert operators' limits.
 #pragma once
 
 #include <cstdint>
@@ -13,6 +13,18 @@
 #include "internal.h"
 
 namespace sg {
+
+// Limits of the expert operators and the products by expert.
+constexpr int kMaxExperts = 1024;  // E
+constexpr int kMaxChoices = 64;    // k
+
+// T tokens with k choices out of E.
+inline bool choices_ok(int T, int k, int E)
+{
+    return T >= 0 && k >= 1 && k <= kMaxChoices && E >= 1 && E <= kMaxExperts &&
+           static_cast<long long>(T) * k <= 0x7FFFFFFFLL;
+}
+
 namespace rows {
 
 // A vector of VB bytes.
