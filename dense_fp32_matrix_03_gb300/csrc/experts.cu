@@ -240,6 +240,10 @@ unsigned sort_cluster(int S)
 //     5 of 2825 fp16 51 / 28, dispatch of these 38 / 21, 35 / 32, 36 / 22
 //   the gradient on 8 bytes: one vector, since it keeps a token's vector and
 //     the sums too (7252 x 3 of 2612: 55; two vectors 73)
+// (The register limits that keep five or six blocks on a multiprocessor spill in
+// some of the forms chosen: combine's two-row form of 16-bit rows on 16 bytes 30
+// words, its four-row form of bf16 on 8 bytes 12, the others 9 or fewer, the
+// gradient's 1 or 2.)
 //
 // Measured on GB300, bf16 (us, share of the measured copy bandwidth for the
 // bytes of kept rows, tokens' rows and results): 65536 rows of 4096 dispatched

@@ -6,7 +6,7 @@
 // takes little longer than HBM needs for them.  Both kernels here keep their
 // sums in registers and need no tensor memory, barriers or pipeline, whose
 // setting up is most of the time of the kernel in i8_tc.cuh for one token
-// (4096 x 4096 on GB300: 11.5 us; 4.7 here, a plain read of the weights 4.1).
+// (4096 x 4096 on GB300: 11.0 us; 4.5 here, a plain read of the weights 4.1).
 //   dots_kernel  up to four tokens at a time, integer dot products (dp4a):
 //                16 instructions per 2 KB of weights and token, but on units
 //                too slow for more (eight tokens took 16.7 us)
@@ -16,7 +16,7 @@
 //                the same condition as in i8_tc.cuh; 80 instructions widen 2 KB
 //                of weights.  (The integer matrix instruction needs none, but
 //                its rate, about 115 products a clock and multiprocessor, made
-//                16 tokens 7.9 us where this kernel takes 6.7.)
+//                16 tokens 7.9 us where this kernel takes 6.4.)
 // In both the warps of a block share the steps of k of a few channels, add
 // their sums in shared memory in order of k, and scale and store them; the
 // weights of a dense call start on their way into L2 before the kernel waits
@@ -113,6 +113,8 @@ struct Results {
 // A lane holds 16 bytes of each of the warp's channels and tokens, a step is
 // 512 k: every load is 512 contiguous bytes.
 constexpr int kDotK = 512, kDotCh = 4;
+// (Seven blocks leave 72 registers: 18 words of the four-token form's spill, 4
+// of the two-token form's; four tokens take 6.0 us at 4096 x 4096, two 5.0.)
 constexpr int kDotWarps = 4, kDotBlocks = 7;  // of a block, of a multiprocessor
 
 __device__ __forceinline__ int dot16(const uint4 &x, const uint4 &y, int s)

@@ -21,7 +21,11 @@ namespace i8 {
 // of 64 k staged in shared memory as words of four 8-bit values (dp4a: four
 // products and an exact 32-bit sum).  Any base and leading dimension: words
 // are read whole where all allow it, byte by byte otherwise; bytes past K
-// read as zero.
+// read as zero.  A plain kernel, bound by its loads, which nothing overlaps (us,
+// by bytes / by words / the kernels for rows on 16 bytes; 4096 x 4096, 1 token
+// 248 / 192 / 4.5, 16 266 / 203 / 6.4, 256 383 / 263 / 19, 1000 696 / 475 / 29;
+// 8192 x 8192 x 4092 by words 6150, 317).  Weights are laid out once: rows padded
+// to 16 bytes cost less than any kernel for rows that are not.
 constexpr int kDT = 64, kDK = 64, kDW = kDK / 4;
 
 template <bool WORDS>
@@ -182,14 +186,14 @@ void note_product(int kernel, int split)
 // The few-token kernel's form for a dense call.
 struct FewForm {
     bool once;   // blocks of 16 warps: all of them run at once, with two steps or
-                 // more of k a warp (8 / 16 warps: 16 x 4096 x 4096 9.1 / 6.2,
-                 // 16 x 8192 x 8192 21.1 / 21.9, 16 x 1024 x 1024 2.6 / 3.4)
+                 // more of k a warp (8 / 16 warps: 16 x 4096 x 4096 9.0 / 6.4,
+                 // 16 x 8192 x 8192 20.7 / 21.2, 16 x 1024 x 1024 2.5 / 3.3)
     bool large;  // 32 tokens a block of 16 warps, likewise where all run at once
-                 // (against the kernels chosen otherwise: 64 x 1024 x 4096 8.9 /
-                 // 6.3, 64 x 1200 x 8192 12.9 / 8.9, 1024 x 64 x 4096 9.2 / 6.4,
-                 // 17 x 2048 x 2048 5.9 / 4.8; with more blocks, 96 x 1024 x 4096
-                 // 9.2 / 11.5; at shorter k, 64 x 1024 x 1024 3.9 / 5.4; with few
-                 // blocks at that, 64 x 256 x 2048 3.2 / 4.5)
+                 // (against the kernels chosen otherwise: 64 x 1024 x 4096 8.5 /
+                 // 6.5, 64 x 1200 x 8192 12.7 / 9.1, 1024 x 64 x 4096 8.8 / 6.6,
+                 // 17 x 2048 x 2048 5.7 / 5.0; with more blocks, 96 x 1024 x 4096
+                 // 8.9 / 11.6; at shorter k, 64 x 1024 x 1024 3.7 / 5.3; with few
+                 // blocks at that, 64 x 256 x 2048 3.2 / 4.6)
     explicit FewForm(const Args &a)
     {
         const long long blocks = (a.N + 15) / 16 * ((a.M + 31LL) / 32);
@@ -238,14 +242,14 @@ int run(const Args &a, cudaStream_t st)
 
     // The kernels' times in us, as measured on GB300 (bf16; M x N x K):
     //   few     2.9 us and a pass over the weights per 16 tokens, from HBM or
-    //           L2, or the results: 17 .. 32 x 4096 x 4096 9.4, 48 14.2, 100 x
-    //           1024 x 1024 4.1, 64 x 4096 x 128 5.5
+    //           L2, or the results: 17 .. 32 x 4096 x 4096 9.1, 48 13.5, 100 x
+    //           1024 x 1024 4.1, 64 x 4096 x 128 5.8
     //   narrow  3.4 us (5 where a cluster's CTAs share a tile's slots, when tiles
     //           are few) and 0.8 a slot of 128 k and wave of tiles: 24 .. 64 x
-    //           4096 x 4096 11.8 .. 12.7, 256 19.1, 512 26.0, 1024 46, 100 x 1024
-    //           x 1024 8.3, 64 x 4096 x 128 4.2
+    //           4096 x 4096 11.6 .. 12.6, 256 19.1, 512 25.2, 1024 45, 100 x 1024
+    //           x 1024 8.4, 64 x 4096 x 128 4.3
     //   wide    about 0.7 a slot and wave, of tiles four times as large: 256 ..
-    //           1024 x 4096 x 4096 28 .. 30, 2048 53; less when the GPU is full
+    //           1024 x 4096 x 4096 27 .. 29, 2048 51; less when the GPU is full
     const double narrow_tiles = tiles_expected(a, Narrow::NT, kCh);
     const double wide_tiles = tiles_expected(a, Wide::NT, 2 * kCh);
     int split = 1;
@@ -262,8 +266,13 @@ int run(const Args &a, cudaStream_t st)
                     (split > 1 ? 5. : 3.4) + 0.8 * narrow_waves * k_slots)
                 kernel = SGEMM_I8_KERNEL_FEW;
         } else if (a.M <= 16LL * a.E) {
-            // 32 experts of 2048 x 2048, few / narrow: 8 rows each 30 / 46 us, 12
-            // rows 36 / 46 us, 16 rows 43 / 47
+            // 32 experts of 2048 x 2048, few / narrow: 8 rows each 30 / 44 us, 12
+            // rows 36 / 44 us, 16 rows 43 / 45.  The host knows the mean only.
+            // Where rows gather on few experts, narrow would do better: 64 experts
+            // of 2048 x 2048, rows in proportion to 1, 1/2, 1/3, ... 81 / 74, 256
+            // rows on one and 16 on most others 69 / 65, all 1024 on one 66 / 18;
+            // of small weights few keeps ahead (512 x 1024: 15 / 17, 13 / 18, 13 /
+            // 11; even rows 10 / 16)
             kernel = SGEMM_I8_KERNEL_FEW;
         }
     }

@@ -13,7 +13,13 @@
 // keep enough rows in flight.  Measured on GB300, bf16: 8192 x 4096 20.7 us
 // (4.9 TB/s; with two or eight vectors a thread 22.5 and 21.0), 8192 x 8192 38 us
 // (5.3), 65536 rows of 4096 in expert order from 8192 tokens 55 us (6.1), one
-// row of 4096 1.5 us.
+// row of 4096 1.5 us; fp32 8192 x 4096 27.8 us (6.0), 8192 x 8192 67 (5.0: half
+// of a row is read a second time).
+//
+// Of the gated activation: 8192 x 4096 bf16 57 us (2.9 TB/s, 2.3 times its bytes'
+// time), fp32 70 (4.3), 8192 x 4095 bf16 70, 65536 x 768 bf16 84 (3.0), one row of
+// 4096 3.5 us.  An expf and an IEEE division a value, and values held in fp32 at
+// three blocks a multiprocessor, keep it off the memory's rate.
 //
 // Rows off 16 bytes are loaded in pieces of what their alignment allows, into
 // vectors of at least four values whose codes go out as one word: codes stored
