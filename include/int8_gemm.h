@@ -59,8 +59,9 @@ extern "C" {
  * ldx >= K (2 K), ldq >= K; columns K .. ldq-1 of Q are not written.
  *  - A row whose largest magnitude is below 2^-100 (zeros among them) gets
  *    scale 0 and codes 0.
- *  - A row that holds an infinity or NaN gets scale NaN and codes 0, so that
- *    every result made from it is NaN.
+ *  - A row that holds an infinity or NaN, or whose gated activation leaves
+ *    fp32's range, gets scale NaN and codes 0, so that every result made from
+ *    it is NaN.
  * For the product's fast path give Q a 16-byte aligned base and a leading
  * dimension that is a multiple of 16.  M == 0 or K == 0: scale = 0. */
 int sgemm_i8_quantize_rows(int type, int act, int M, int K, const void *X, int ldx,
