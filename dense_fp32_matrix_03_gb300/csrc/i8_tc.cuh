@@ -54,9 +54,12 @@
 //           CTA widening its 128 channels and half the tokens.
 // Every wait is bounded.
 //
-// Measured on GB300, bf16 results: 8192 x 8192 x 8192 621 us (1772 TFLOP/s,
-// 0.93 of the measured 16-bit peak, above its sustained rate), x 4096 319 us,
-// x 1024 106 us; 32 experts of 4096 x 2048 over 32768 rows, unevenly, 368 us.
+// Measured on GB300, bf16 results: 8192 x 8192 x 8192 612 us (1796 TFLOP/s,
+// 0.94 of the measured 16-bit peak, above its sustained rate), x 4096 317 us,
+// x 1024 104 us; 32 experts of 4096 x 2048 over 32768 rows, unevenly, 366 us.
+// fp32 results: 8192 x 8192 x 4096 347 us, 8192 x 4096 x 2048 107 us (bf16 91): the
+// accumulator is released after the stores, since a tile of them does not fit
+// the registers.
 // What bounds the wide form: the MMAs' 1024 clocks a slot stretch to about 1220
 // beside the converters (without them: 1000 to 1050), and a tile's end leaves
 // the tensor pipe idle for about 1850 clocks, while the accumulator is read.
