@@ -11,7 +11,7 @@ import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                     "dense_fp32_matrix_03_gb300", "csrc")
-READ_ONLY = re.compile(r"__ldg\s*\(|ld\.global(\.\w+)*\.nc\b|\bconst\s+\w+\s*\*\s*__restrict__")
+READ_ONLY = re.compile(r"__ldg\s*\(|ld\.global(\.\w+)*\.nc\b|__restrict__")
 
 
 def code(path):
