@@ -47,6 +47,14 @@ SGEMM_ACT_NONE = 0
 SGEMM_ACT_SWIGLU = 1
 ACTS = {"none": SGEMM_ACT_NONE, "swiglu": SGEMM_ACT_SWIGLU}
 
+SGEMM_FP4_MX = 0
+SGEMM_FP4_NV = 1
+FP4_FORMATS = {"mx": SGEMM_FP4_MX, "nv": SGEMM_FP4_NV}
+
+SGEMM_EXPERTS_I8 = 0
+SGEMM_EXPERTS_SAME = 1
+EXPERT_WEIGHTS = {"i8": SGEMM_EXPERTS_I8, "same": SGEMM_EXPERTS_SAME}
+
 SGEMM_I8_KERNEL_AUTO = 0
 SGEMM_I8_KERNEL_DOTS = 1
 SGEMM_I8_KERNEL_FEW = 2
@@ -126,6 +134,21 @@ SIGNATURES = {
     "sgemm_experts_combine": (_i, [_i, _i, _i, _i, _i, _p, _i, _p, _p, _p, _p, _i, _p]),
     "sgemm_experts_combine_grad": (_i, [_i, _i, _i, _i, _i, _p, _i, _p, _i, _p, _p, _p, _p, _i,
                                         _p, _p]),
+    "sgemm_experts_layer_workspace_size": (ctypes.c_size_t, [_i, _i, _i, _i]),
+    "sgemm_experts_layer": (_i, [_i, _i, _i, _i, _i, _i, _i, _p, _i, _p, _p, _p, _i, _ll, _p, _p,
+                                 _i, _ll, _p, _p, _i, _p, ctypes.c_size_t, _p]),
+    # include/fp4_gemm.h
+    "sgemm_fp4_scales_size": (ctypes.c_size_t, [_i, _i, _i]),
+    "sgemm_fp4_quantize_rows": (_i, [_i, _i, _i, _i, _i, _p, _i, _p, _i, _p, _p, _p]),
+    "sgemm_fp4": (_i, [_i, _i, _i, _i, _i, _p, _i, _p, _p, _p, _i, _p, _p, _p, _i, _p]),
+    # include/rms_norm.h
+    "sgemm_rms_norm": (_i, [_i, _i, _i, _f, _p, _i, _p, _i, _p, _p, _i, _p, _i, _p]),
+    "sgemm_rms_norm_i8": (_i, [_i, _i, _i, _f, _p, _i, _p, _i, _p, _p, _i, _p, _i, _p, _p]),
+    "sgemm_rms_norm_fp4": (_i, [_i, _i, _i, _i, _f, _p, _i, _p, _i, _p, _p, _i, _p, _i, _p, _p,
+                                _p]),
+    "sgemm_rms_norm_grad_workspace_size": (ctypes.c_size_t, [_i, _i]),
+    "sgemm_rms_norm_grad": (_i, [_i, _i, _i, _f, _p, _i, _p, _p, _i, _p, _i, _p, _i, _p, _p,
+                                 ctypes.c_size_t, _p]),
 }
 
 
@@ -465,6 +488,87 @@ def sgemm_experts_combine_grad(type_, T, k, E, H, dout, ldo, rows, ldr, position
     return _lib.sgemm_experts_combine_grad(_type(type_), T, k, E, H, _ptr(dout), ldo, _ptr(rows),
                                            ldr, _ptr(positions), _ptr(offsets), _ptr(weights),
                                            _ptr(drows), ldd, _ptr(dweights), _stream(stream))
+
+
+def sgemm_experts_layer_workspace_size(T, k, H, F) -> int:
+    return int(_lib.sgemm_experts_layer_workspace_size(T, k, H, F))
+
+
+def sgemm_experts_layer(type_, wtype, T, k, E, H, F, x, ldx, ids, weights, W1, ld1, stride1,
+                        scale1, W2, ld2, stride2, scale2, out, ldo, workspace, workspace_bytes,
+                        stream=None) -> int:
+    """wtype: "i8" (8-bit weights with a scale per row) or "same" (weights of
+    the row type; scale1 and scale2 None)."""
+    if isinstance(wtype, str):
+        wtype = EXPERT_WEIGHTS[wtype]
+    return _lib.sgemm_experts_layer(_type(type_), wtype, T, k, E, H, F, _ptr(x), ldx, _ptr(ids),
+                                    _ptr(weights), _ptr(W1), ld1, stride1, _ptr(scale1),
+                                    _ptr(W2), ld2, stride2, _ptr(scale2), _ptr(out), ldo,
+                                    _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+# ---- 4-bit floating-point products (include/fp4_gemm.h)
+
+def _format(format_) -> int:
+    return FP4_FORMATS[format_] if isinstance(format_, str) else format_
+
+
+def sgemm_fp4_scales_size(format_, rows, K) -> int:
+    """Bytes of the block scales of `rows` rows of K values."""
+    return int(_lib.sgemm_fp4_scales_size(_format(format_), rows, K))
+
+
+def sgemm_fp4_quantize_rows(type_, act, format_, M, K, X, ldx, Q, ldq, sf, scale,
+                            stream=None) -> int:
+    """Q: codes, two to a byte (ldq in values); sf: block scales; scale: M fp32
+    values."""
+    if isinstance(act, str):
+        act = ACTS[act]
+    return _lib.sgemm_fp4_quantize_rows(_type(type_), act, _format(format_), M, K, _ptr(X), ldx,
+                                        _ptr(Q), ldq, _ptr(sf), _ptr(scale), _stream(stream))
+
+
+def sgemm_fp4(type_, format_, M, N, K, A, lda, sfA, scaleA, B, ldb, sfB, scaleB, C, ldc,
+              stream=None) -> int:
+    return _lib.sgemm_fp4(_type(type_), _format(format_), M, N, K, _ptr(A), lda, _ptr(sfA),
+                          _ptr(scaleA), _ptr(B), ldb, _ptr(sfB), _ptr(scaleB), _ptr(C), ldc,
+                          _stream(stream))
+
+
+# ---- root-mean-square norm (include/rms_norm.h)
+
+def sgemm_rms_norm(type_, M, H, eps, x, ldx, res, ldr, weight, sum_, lds, y, ldy,
+                   stream=None) -> int:
+    """res, weight and sum_ may be None."""
+    return _lib.sgemm_rms_norm(_type(type_), M, H, eps, _ptr(x), ldx, _ptr(res), ldr,
+                               _ptr(weight), _ptr(sum_), lds, _ptr(y), ldy, _stream(stream))
+
+
+def sgemm_rms_norm_i8(type_, M, H, eps, x, ldx, res, ldr, weight, sum_, lds, q, ldq, scale,
+                      stream=None) -> int:
+    return _lib.sgemm_rms_norm_i8(_type(type_), M, H, eps, _ptr(x), ldx, _ptr(res), ldr,
+                                  _ptr(weight), _ptr(sum_), lds, _ptr(q), ldq, _ptr(scale),
+                                  _stream(stream))
+
+
+def sgemm_rms_norm_fp4(type_, format_, M, H, eps, x, ldx, res, ldr, weight, sum_, lds, q, ldq, sf,
+                       scale, stream=None) -> int:
+    return _lib.sgemm_rms_norm_fp4(_type(type_), _format(format_), M, H, eps, _ptr(x), ldx,
+                                   _ptr(res), ldr, _ptr(weight), _ptr(sum_), lds, _ptr(q), ldq,
+                                   _ptr(sf), _ptr(scale), _stream(stream))
+
+
+def sgemm_rms_norm_grad_workspace_size(M, H) -> int:
+    return int(_lib.sgemm_rms_norm_grad_workspace_size(M, H))
+
+
+def sgemm_rms_norm_grad(type_, M, H, eps, s, lds, weight, dy, ldy, dsum, ldds, dx, ldx, dweight,
+                        workspace, workspace_bytes, stream=None) -> int:
+    """weight, dsum and dweight (then workspace too) may be None."""
+    return _lib.sgemm_rms_norm_grad(_type(type_), M, H, eps, _ptr(s), lds, _ptr(weight),
+                                    _ptr(dy), ldy, _ptr(dsum), ldds, _ptr(dx), ldx,
+                                    _ptr(dweight), _ptr(workspace), int(workspace_bytes),
+                                    _stream(stream))
 
 
 def check(status: int) -> None:

@@ -1,0 +1,533 @@
+// expert_few.cu -- a whole expert layer for a few tokens in two kernels
+// (include/expert_layer.h):
+//   up    h[t,j] = silu(x G_e^T) * (x U_e^T), a block for each chosen expert
+//         and 16 of its rows of G and of U
+//   down  out[t] = sum_e w D_e h[t,e], a block for 16 channels of out and ALL
+//         chosen experts, so that nothing is added across blocks
+// Both find the chosen experts and their tokens from the ids themselves (at
+// most 512): no sort, no rows in expert order, no counts on the host.
+//
+// What counts is to read the chosen experts' weights once.  The products run
+// on the matrix units (mma.sync m16n8k16, fp32 sums), the weights its 16 rows,
+// the tokens its 8 columns; 8-bit weights are widened in registers, exactly, to
+// the row type.  Lane (g, t) = (lane / 4, lane % 4) holds rows g and g + 8 of
+// the weights and token g; which k it holds is ours to choose as long as both
+// operands agree, so a lane takes 16 consecutive bytes of a weight row at a
+// time and the same k of the token: every load is 16 bytes, a quad reads 64
+// bytes of a row together, nothing passes through shared memory.
+#include <type_traits>
+
+#include "../../include/expert_layer.h"
+#include "dependent.cuh"
+#include "rows.cuh"
+
+namespace sg {
+namespace few {
+
+constexpr int kMaxRows = 512;   // T * k
+constexpr int kMaxTokens = 64;  // T
+constexpr int kMaxSide = 65536; // H, F
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kCh = 16;         // channels of a fragment
+
+struct Args {
+    int T, k, E, H, F;
+    const void *x;
+    long long ldx;
+    const int *ids;
+    const float *weights;
+    const void *W1, *W2;  // addresses in bytes from here on: pitches, strides
+    long long p1, stride1, p2, stride2;
+    const float *scale1, *scale2;
+    void *out;
+    long long ldo;
+    void *h;       // T * k rows of ldh values
+    long long ldh;
+};
+
+// The chosen experts in ascending order and, for each, its tokens in ascending
+// order.  A token that chose an expert more than once is one row, whose weight
+// is the sum.
+struct Choices {
+    int ids[kMaxRows];
+    float w[kMaxRows];
+    short first[kMaxRows + 1];    // first row of used expert u
+    short expert[kMaxRows];       // its id
+    short token[kMaxRows];        // of a row
+    short choice[kMaxRows];       // t * k + the first j
+    float weight[kMaxRows];
+    int used;
+};
+
+// Fills `c` (all threads of the block call).  The loads pass L1 by: the down
+// kernel is here while the up kernel still runs.
+__device__ __forceinline__ void find_choices(const Args &a, Choices &c)
+{
+    const int S = a.T * a.k, tid = threadIdx.x;
+    for (int s = tid; s < S; s += kThreads) {
+        const int e = __ldcg(a.ids + s);
+        c.ids[s] = e >= 0 && e < a.E ? e : -1;
+        c.w[s] = a.weights != nullptr ? __ldcg(a.weights + s) : 1.f;
+    }
+    __syncthreads();
+    // a choice's row: how many distinct (expert, token) pairs come before it
+    int keep[kMaxRows / kThreads], pos[kMaxRows / kThreads];
+    float sum[kMaxRows / kThreads];
+#pragma unroll
+    for (int i = 0; i < kMaxRows / kThreads; ++i) {
+        const int s = tid + i * kThreads;
+        keep[i] = 0;
+        pos[i] = 0;
+        sum[i] = 0.f;
+        if (s >= S || c.ids[s] < 0) continue;
+        const int t0 = s / a.k * a.k, e = c.ids[s];
+        keep[i] = 1;
+        for (int j = t0; j < t0 + a.k; ++j)
+            if (c.ids[j] == e) {
+                if (j < s) keep[i] = 0;
+                sum[i] += c.w[j];
+            }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMaxRows / kThreads; ++i) {
+        const int s = tid + i * kThreads;
+        if (s < S && c.ids[s] >= 0 && !keep[i]) c.ids[s] = -2 - c.ids[s];  // not a row
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMaxRows / kThreads; ++i) {
+        const int s = tid + i * kThreads;
+        if (!keep[i]) continue;
+        const int e = c.ids[s];
+        for (int j = 0; j < S; ++j) {
+            const int o = c.ids[j];
+            pos[i] += o >= 0 && (o < e || (o == e && j < s));
+        }
+        c.token[pos[i]] = static_cast<short>(s / a.k);
+        c.choice[pos[i]] = static_cast<short>(s);
+        c.weight[pos[i]] = sum[i];
+    }
+    // rows, and where a new expert begins
+    int rows_ = 0;
+    for (int s0 = 0; s0 < S; s0 += kThreads)
+        rows_ += __syncthreads_count(s0 + tid < S && c.ids[s0 + tid] >= 0);
+    if (tid < 32) {
+        int used = 0;
+        for (int p0 = 0; p0 < rows_; p0 += 32) {
+            const int p = p0 + tid;
+            int e = -1;
+            bool begins = false;
+            if (p < rows_) {
+                e = c.ids[c.choice[p]];
+                begins = p == 0 || c.ids[c.choice[p - 1]] != e;
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, begins);
+            if (begins) {
+                const int u = used + __popc(m & ((1u << tid) - 1u));
+                c.first[u] = static_cast<short>(p);
+                c.expert[u] = static_cast<short>(e);
+            }
+            used += __popc(m);
+        }
+        if (tid == 0) {
+            c.first[used] = static_cast<short>(rows_);
+            c.used = used;
+        }
+    }
+    __syncthreads();
+}
+
+// ------------------------------------------------------------- the operands
+
+// Four 8-bit integers as four values of T: pairs lo, hi.
+template <class T>
+__device__ __forceinline__ void widen4(uint32_t x, uint32_t &lo, uint32_t &hi)
+{
+    if constexpr (std::is_same<T, __half>::value) {
+        // x ^ 0x80 = x + 128 as an unsigned byte u; 0x64uu is fp16's 1024 + u
+        const uint32_t u = x ^ 0x80808080u;
+        const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140);
+        const uint32_t b = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 ha = __hsub2(*reinterpret_cast<const __half2 *>(&a), bias);
+        const __half2 hb = __hsub2(*reinterpret_cast<const __half2 *>(&b), bias);
+        lo = *reinterpret_cast<const uint32_t *>(&ha);
+        hi = *reinterpret_cast<const uint32_t *>(&hb);
+    } else {
+        // bf16 has seven bits below the leading one: the low seven bits of x above
+        // 128, plus -128 or, of a negative x (its top bit stands for -128), -256
+        auto pair = [](uint32_t w) {
+            const uint32_t a = (w & 0x007F007Fu) | 0x43004300u;  // 128 + low bits
+            const uint32_t b = (w & 0x00800080u) | 0xC300C300u;  // -128 or -256
+            const __nv_bfloat162 s = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                             *reinterpret_cast<const __nv_bfloat162 *>(&b));
+            return *reinterpret_cast<const uint32_t *>(&s);
+        };
+        lo = pair(__byte_perm(x, 0u, 0x4140));
+        hi = pair(__byte_perm(x, 0u, 0x4342));
+    }
+}
+
+// d (+)= the 16 x 16 weights times 16 x 8 tokens.
+template <class T>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    if constexpr (std::is_same<T, __half>::value)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 bytes of a row of ES-byte values from value k on; zeros past K, nothing
+// past K is read.  VEC: the row starts on a 16-byte boundary.
+template <int ES, bool VEC>
+__device__ __forceinline__ uint4 load16(const char *row, int k, int K)
+{
+    constexpr int N = 16 / ES;
+    if (VEC && k + N <= K) return *reinterpret_cast<const uint4 *>(row + static_cast<long long>(k) * ES);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (k + i < K) {
+            if (ES == 1)
+                w[i / 4] |= static_cast<uint32_t>(reinterpret_cast<const unsigned char *>(row)[k + i])
+                            << (8 * (i % 4));
+            else
+                w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[k + i])
+                            << (16 * (i % 2));
+        }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// What differs between 8-bit weights and weights of the row type T: the values
+// in 16 bytes.
+template <class T, bool I8>
+struct Weights {
+    static constexpr int ES = I8 ? 1 : 2;
+    static constexpr int N = 16 / ES;         // values of a lane's piece
+    static constexpr int TOK = N / 8;         // 16-byte pieces of a token's values
+    static constexpr int STEP = 8 * N;        // k of a warp's step: two pieces a lane
+    // pairs of T from a piece
+    static __device__ __forceinline__ void pairs(const uint4 &v, uint32_t (&p)[N / 2])
+    {
+        if constexpr (I8) {
+            widen4<T>(v.x, p[0], p[1]);
+            widen4<T>(v.y, p[2], p[3]);
+            widen4<T>(v.z, p[4], p[5]);
+            widen4<T>(v.w, p[6], p[7]);
+        } else {
+            p[0] = v.x;
+            p[1] = v.y;
+            p[2] = v.z;
+            p[3] = v.w;
+        }
+    }
+};
+
+// One step (STEP values of k from k0 on) of CF fragments of weights and NF of
+// tokens: acc += weights * tokens.  wrow: rows g and g + 8 of each fragment;
+// trow: token g of each.  Lane t takes k0 + N t + 4 N i + 0 .. N-1 of piece i.
+template <class T, bool I8, int CF, int NF, bool XV>
+__device__ __forceinline__ void step(float (&acc)[CF][NF][4], const char *const (&wrow)[CF][2],
+                                     const char *const (&trow)[NF], int k0, int K, int t,
+                                     int tokens)
+{
+    using W = Weights<T, I8>;
+    uint4 w[CF][2][2], x[NF][2][W::TOK];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int k = k0 + W::N * t + 4 * W::N * i;
+#pragma unroll
+        for (int c = 0; c < CF; ++c)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) w[c][r][i] = load16<W::ES, true>(wrow[c][r], k, K);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int k = k0 + W::N * t + 4 * W::N * i;
+#pragma unroll
+        for (int n = 0; n < NF; ++n)
+#pragma unroll
+            for (int j = 0; j < W::TOK; ++j) x[n][i][j] = load16<2, XV>(trow[n], k + 8 * j, K);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int c = 0; c < CF; ++c) {
+            uint32_t lo[W::N / 2], hi[W::N / 2];
+            W::pairs(w[c][0][i], lo);
+            W::pairs(w[c][1][i], hi);
+#pragma unroll
+            for (int n = 0; n < NF; ++n)
+                if (n == 0 || 8 * n < tokens) {
+#pragma unroll
+                    for (int j = 0; j < W::N / 4; ++j) {
+                        const uint4 &v = x[n][i][j / 2];
+                        mma<T>(acc[c][n], lo[2 * j], hi[2 * j], lo[2 * j + 1], hi[2 * j + 1],
+                               j % 2 ? v.z : v.x, j % 2 ? v.w : v.y);
+                    }
+                }
+        }
+}
+
+// ---------------------------------------------------------------------- up
+
+// grid: 16 rows of G and U (x), the used expert (y).
+template <class T, bool I8, int NF, bool XV>
+__global__ void __launch_bounds__(kThreads, NF == 4 ? 2 : 3) up_kernel(const Args a)
+{
+    constexpr int TK = 8 * NF;
+    using W = Weights<T, I8>;
+    __shared__ Choices c;
+    __shared__ float part[kWarps][TK][2 * kCh + 4];
+    dependent_wait();
+    dependent_release();  // (after the wait: the next kernel reads ids and weights early)
+    find_choices(a, c);
+    const int u = blockIdx.y;
+    if (u >= c.used) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int e = c.expert[u], f0 = blockIdx.x * kCh;
+    const char *wrow[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            wrow[i][r] = static_cast<const char *>(a.W1) + e * a.stride1 +
+                         (static_cast<long long>(i) * a.F + min(f0 + g + 8 * r, a.F - 1)) * a.p1;
+    for (int r0 = c.first[u]; r0 < c.first[u + 1]; r0 += TK) {
+        const int n = min(TK, c.first[u + 1] - r0);
+        const char *trow[NF];
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+            trow[i] = static_cast<const char *>(a.x) +
+                      c.token[r0 + min(8 * i + g, n - 1)] * a.ldx * static_cast<int>(sizeof(T));
+        float acc[2][NF][4] = {};
+        for (int k = warp * W::STEP; k < a.H; k += kWarps * W::STEP)
+            step<T, I8, 2, NF, XV>(acc, wrow, trow, k, a.H, t, n);
+        __syncthreads();  // the last turn's readers are done
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int m = 0; m < NF; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    part[warp][8 * m + 2 * t + (j & 1)][kCh * i + 8 * (j >> 1) + g] = acc[i][m][j];
+        __syncthreads();
+        for (int i = threadIdx.x; i < n * kCh; i += kThreads) {
+            const int m = i / kCh, f = i % kCh;
+            float gate = 0.f, up = 0.f;
+            if (f0 + f < a.F) {
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    gate += part[w][m][f];
+                    up += part[w][m][kCh + f];
+                }
+                if (I8) {
+                    const float *s = a.scale1 + static_cast<long long>(e) * 2 * a.F + f0 + f;
+                    gate *= s[0];
+                    up *= s[a.F];
+                }
+            }
+            // (values past F are zeros: gate is)
+            static_cast<T *>(a.h)[c.choice[r0 + m] * a.ldh + f0 + f] =
+                rows::from_f<T>(gate / (1.f + expf(-gate)) * up);
+        }
+    }
+}
+
+// -------------------------------------------------------------------- down
+
+// grid: 16 channels of out.  The steps of all used experts form one list, a
+// part of which is each warp's; a warp adds an expert's results, weighted, to
+// sums of its own, and the block adds those in the warps' order.
+template <class T, bool I8, int NF>
+__global__ void __launch_bounds__(kThreads, 2) down_kernel(const Args a)
+{
+    constexpr int TK = 8 * NF;
+    using W = Weights<T, I8>;
+    __shared__ Choices c;
+    extern __shared__ float sums[];  // [warp][token][channel], rows of kCh + 1
+    dependent_release();
+    // The up kernel releases its dependents after its own wait, so what it found
+    // complete, ids and weights among it, is complete here too.  (F == 0: there is
+    // no up kernel.)
+    if (a.F == 0) dependent_wait();
+    find_choices(a, c);
+    dependent_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int h0 = blockIdx.x * kCh;
+    float *mine = sums + static_cast<long long>(warp) * a.T * (kCh + 1);
+    for (int i = lane; i < a.T * (kCh + 1); i += 32) mine[i] = 0.f;
+    __syncwarp();
+    const int steps = (a.F + W::STEP - 1) / W::STEP, total = c.used * steps;
+    int at = static_cast<int>(static_cast<long long>(total) * warp / kWarps);
+    const int end = static_cast<int>(static_cast<long long>(total) * (warp + 1) / kWarps);
+    while (at < end) {
+        const int u = at / steps, lo = at - u * steps, hi = min(steps, lo + end - at);
+        const int e = c.expert[u];
+        const char *wrow[1][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            wrow[0][r] = static_cast<const char *>(a.W2) + e * a.stride2 +
+                         min(h0 + g + 8 * r, a.H - 1) * a.p2;
+        float scale[2] = {1.f, 1.f};
+        if (I8)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                scale[r] = a.scale2[static_cast<long long>(e) * a.H + min(h0 + g + 8 * r, a.H - 1)];
+        for (int r0 = c.first[u]; r0 < c.first[u + 1]; r0 += TK) {
+            const int n = min(TK, c.first[u + 1] - r0);
+            const char *trow[NF];
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+                trow[i] = static_cast<const char *>(a.h) +
+                          c.choice[r0 + min(8 * i + g, n - 1)] * a.ldh * static_cast<int>(sizeof(T));
+            float acc[1][NF][4] = {};
+            for (int s = lo; s < hi; ++s)
+                step<T, I8, 1, NF, true>(acc, wrow, trow, s * W::STEP, a.F, t, n);
+#pragma unroll
+            for (int m = 0; m < NF; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int col = 8 * m + 2 * t + (j & 1);
+                    if (col < n)
+                        mine[c.token[r0 + col] * (kCh + 1) + 8 * (j >> 1) + g] +=
+                            c.weight[r0 + col] * (scale[j >> 1] * acc[0][m][j]);
+                }
+            __syncwarp();
+        }
+        at += hi - lo;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.T * kCh; i += kThreads) {
+        const int m = i / kCh, ch = i % kCh;
+        if (h0 + ch >= a.H) continue;
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) s += sums[(w * a.T + m) * (kCh + 1) + ch];
+        static_cast<T *>(a.out)[m * a.ldo + h0 + ch] = rows::from_f<T>(s);
+    }
+}
+
+template <class T, bool I8, int NF>
+int launch(const Args &a, bool x_vec, cudaStream_t st)
+{
+    const int rows_ = a.T * a.k, most = a.E < rows_ ? a.E : rows_;
+    const dim3 grid(static_cast<unsigned>((a.F + kCh - 1) / kCh), static_cast<unsigned>(most));
+    if (a.F > 0 && a.H > 0) {
+        const int s = launch_dependent(x_vec ? up_kernel<T, I8, NF, true> : up_kernel<T, I8, NF, false>,
+                                       grid, dim3(kThreads), 0, 1, st, a);
+        if (s != SGEMM_OK) return s;
+    }
+    const size_t smem = sizeof(float) * kWarps * a.T * (kCh + 1);
+    auto kern = down_kernel<T, I8, NF>;
+    if (!smem_attr_once(reinterpret_cast<const void *>(kern),
+                        static_cast<int>(sizeof(float)) * kWarps * kMaxTokens * (kCh + 1)))
+        return SGEMM_ERR_LAUNCH;
+    return launch_dependent(kern, dim3(static_cast<unsigned>((a.H + kCh - 1) / kCh)),
+                            dim3(kThreads), smem, 1, st, a);
+}
+
+template <class T, bool I8>
+int run(const Args &a, bool x_vec, cudaStream_t st)
+{
+    if (a.T <= 8) return launch<T, I8, 1>(a, x_vec, st);
+    if (a.T <= 16) return launch<T, I8, 2>(a, x_vec, st);
+    return launch<T, I8, 4>(a, x_vec, st);
+}
+
+bool sizes_ok(int T, int k, int H, int F)
+{
+    return choices_ok(T, k, 1) && T <= kMaxTokens && static_cast<long long>(T) * k <= kMaxRows &&
+           H >= 0 && H <= kMaxSide && F >= 0 && F <= kMaxSide;
+}
+// A row of h: whole fragments, whose pad the kernel writes.
+long long row_of_h(int F) { return (F + kCh - 1LL) / kCh * kCh; }
+
+}  // namespace few
+}  // namespace sg
+
+using namespace sg;
+
+extern "C" {
+
+size_t sgemm_experts_layer_workspace_size(int T, int k, int H, int F)
+{
+    if (!few::sizes_ok(T, k, H, F)) return 0;
+    return static_cast<size_t>(T) * k * static_cast<size_t>(few::row_of_h(F)) * 2;
+}
+
+int sgemm_experts_layer(int type, int wtype, int T, int k, int E, int H, int F, const void *x,
+                        int ldx, const int *ids, const float *weights, const void *W1, int ld1,
+                        long long stride1, const float *scale1, const void *W2, int ld2,
+                        long long stride2, const float *scale2, void *out, int ldo,
+                        void *workspace, size_t workspace_bytes, void *stream)
+{
+    return c_entry([&]() -> int {
+        const bool i8 = wtype == SGEMM_EXPERTS_I8;
+        if ((type != SGEMM_TYPE_BF16 && type != SGEMM_TYPE_FP16) ||
+            (!i8 && wtype != SGEMM_EXPERTS_SAME) || !few::sizes_ok(T, k, H, F) || E < 1 ||
+            E > kMaxExperts || ldx < 1 || ldx < H || ldo < 1 || ldo < H || ld1 < 1 || ld1 < H ||
+            ld2 < 1 || ld2 < F || stride1 < 0 || stride2 < 0)
+            return SGEMM_ERR_INVALID_ARG;
+        if (E > 1 && ((F > 0 && stride1 < (2LL * F - 1) * ld1 + H) ||
+                      (H > 0 && stride2 < (H - 1LL) * ld2 + F)))
+            return SGEMM_ERR_INVALID_ARG;
+        const long long ws = i8 ? 1 : 2;
+        if (ld1 * ws % 16 != 0 || ld2 * ws % 16 != 0 || stride1 * ws % 16 != 0 ||
+            stride2 * ws % 16 != 0 || !rows::aligned_to(W1, 16) || !rows::aligned_to(W2, 16) ||
+            !rows::aligned_to(x, 2) || !rows::aligned_to(out, 2) || !rows::aligned_to(ids, 4) ||
+            !rows::aligned_to(weights, 4) || !rows::aligned_to(scale1, 4) ||
+            !rows::aligned_to(scale2, 4) || !rows::aligned_to(workspace, 16))
+            return SGEMM_ERR_INVALID_ARG;
+        if (T == 0 || H == 0) return SGEMM_OK;
+        if (x == nullptr || ids == nullptr || out == nullptr) return SGEMM_ERR_INVALID_ARG;
+        if (F > 0 && (W1 == nullptr || W2 == nullptr || (i8 && (scale1 == nullptr || scale2 == nullptr)) ||
+                      workspace == nullptr ||
+                      workspace_bytes < sgemm_experts_layer_workspace_size(T, k, H, F)))
+            return SGEMM_ERR_INVALID_ARG;
+        int num_sms = 0;
+        unsigned int *status = nullptr;
+        if (!current_sm103(&num_sms, &status)) return SGEMM_ERR_UNSUPPORTED;
+        few::Args a{};
+        a.T = T;
+        a.k = k;
+        a.E = E;
+        a.H = H;
+        a.F = F;
+        a.x = x;
+        a.ldx = ldx;
+        a.ids = ids;
+        a.weights = weights;
+        a.W1 = W1;
+        a.W2 = W2;
+        a.p1 = ld1 * ws;
+        a.stride1 = stride1 * ws;
+        a.p2 = ld2 * ws;
+        a.stride2 = stride2 * ws;
+        a.scale1 = scale1;
+        a.scale2 = scale2;
+        a.out = out;
+        a.ldo = ldo;
+        a.h = workspace;
+        a.ldh = few::row_of_h(F);
+        const bool x_vec = rows::aligned_to(x, 16) && ldx % 8 == 0;
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        if (type == SGEMM_TYPE_BF16)
+            return i8 ? few::run<__nv_bfloat16, true>(a, x_vec, st)
+                      : few::run<__nv_bfloat16, false>(a, x_vec, st);
+        return i8 ? few::run<__half, true>(a, x_vec, st) : few::run<__half, false>(a, x_vec, st);
+    });
+}
+
+}  // extern "C"

@@ -116,6 +116,20 @@ struct Vec {
     {
         *static_cast<typename Raw<VB>::T *>(p) = raw;
     }
+    // In pieces of LB bytes, the first `bytes` of them (a multiple of LB).
+    template <int LB>
+    __device__ __forceinline__ void store_pieces(char *p, unsigned bytes) const
+    {
+        if constexpr (LB == VB) {
+            store(p);
+        } else {
+            using P = typename Raw<LB>::T;
+#pragma unroll
+            for (int i = 0; i < VB / LB; ++i)
+                if (static_cast<unsigned>(i * LB) < bytes)
+                    *reinterpret_cast<P *>(p + i * LB) = reinterpret_cast<const P *>(&raw)[i];
+        }
+    }
     __device__ __forceinline__ void zero() { raw = typename Raw<VB>::T{}; }
     __device__ __forceinline__ float get(int i) const { return to_f<T>(v[i]); }
     __device__ __forceinline__ void set(int i, float x) { v[i] = from_f<T>(x); }

@@ -79,6 +79,39 @@ int sgemm_experts_combine_grad(int type, int T, int k, int E, int H, const void 
                                const int *offsets, const float *weights, void *drows, int ldd,
                                float *dweights, void *stream);
 
+/* A whole expert layer for a few tokens (a decoding step), in two kernels,
+ * from the choices as they are: no sort, no rows in expert order.
+ *
+ *   h[t][j] = silu(x[t] G_e^T) * (x[t] U_e^T)        e = ids[t][j]
+ *   out[t]  = sum_j weights[t][j] * (h[t][j] D_e^T)  (kept j)
+ *
+ * W1 holds G_e (rows 0 .. F-1) and U_e (rows F .. 2F-1) of every expert, 2F x H
+ * at W1 + e * stride1 elements, W2 D_e, H x F at W2 + e * stride2; their type:
+ *   SGEMM_EXPERTS_I8    8-bit integers with a scale per row, scale1 (E x 2F)
+ *                       and scale2 (E x H), as sgemm_i8_experts takes them
+ *   SGEMM_EXPERTS_SAME  the row type; scale1 and scale2 are not read
+ * type is SGEMM_TYPE_BF16 or SGEMM_TYPE_FP16.  x, out: T x H, any alignment;
+ * ids: T x k (an id outside 0 .. E-1 is a dropped choice; a token may choose
+ * an expert twice); weights: T x k fp32, NULL means 1 everywhere.  Rows of W1
+ * and W2 start on 16-byte boundaries (bases, leading dimensions and strides).
+ * T * k <= 512, H and F <= 65536.
+ * Products are exact where weights are 8-bit; sums are fp32; h is rounded to
+ * the row type between the products (an fp16 h beyond 65504 is an infinity);
+ * out is summed over the experts in fp32, in an order fixed by ids and the
+ * sizes, and rounded once.  Only experts that a kept choice names are read.  A
+ * token without kept choices gets zeros.  out may not overlap x.
+ * workspace: 16-byte aligned, at least the size below; a call does not read
+ * what it did not write there; calls that may run at the same time need one
+ * each. */
+#define SGEMM_EXPERTS_I8 0
+#define SGEMM_EXPERTS_SAME 1
+size_t sgemm_experts_layer_workspace_size(int T, int k, int H, int F);
+int sgemm_experts_layer(int type, int wtype, int T, int k, int E, int H, int F, const void *x,
+                        int ldx, const int *ids, const float *weights, const void *W1, int ld1,
+                        long long stride1, const float *scale1, const void *W2, int ld2,
+                        long long stride2, const float *scale2, void *out, int ldo,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
