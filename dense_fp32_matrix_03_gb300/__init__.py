@@ -51,6 +51,13 @@ SGEMM_FP4_MX = 0
 SGEMM_FP4_NV = 1
 FP4_FORMATS = {"mx": SGEMM_FP4_MX, "nv": SGEMM_FP4_NV}
 
+SGEMM_FP4_KERNEL_AUTO = 0
+SGEMM_FP4_KERNEL_FEW = 1
+SGEMM_FP4_KERNEL_NARROW = 2
+SGEMM_FP4_KERNEL_WIDE = 3
+FP4_KERNELS = {"auto": SGEMM_FP4_KERNEL_AUTO, "few": SGEMM_FP4_KERNEL_FEW,
+               "narrow": SGEMM_FP4_KERNEL_NARROW, "wide": SGEMM_FP4_KERNEL_WIDE}
+
 SGEMM_EXPERTS_I8 = 0
 SGEMM_EXPERTS_SAME = 1
 EXPERT_WEIGHTS = {"i8": SGEMM_EXPERTS_I8, "same": SGEMM_EXPERTS_SAME}
@@ -141,6 +148,9 @@ SIGNATURES = {
     "sgemm_fp4_scales_size": (ctypes.c_size_t, [_i, _i, _i]),
     "sgemm_fp4_quantize_rows": (_i, [_i, _i, _i, _i, _i, _p, _i, _p, _i, _p, _p, _p]),
     "sgemm_fp4": (_i, [_i, _i, _i, _i, _i, _p, _i, _p, _p, _p, _i, _p, _p, _p, _i, _p]),
+    "sgemm_fp4_tune_force": (_i, [_i]),
+    "sgemm_fp4_last_kernel": (_i, []),
+    "sgemm_fp4_last_split_count": (_i, []),
     # include/rms_norm.h
     "sgemm_rms_norm": (_i, [_i, _i, _i, _f, _p, _i, _p, _i, _p, _p, _i, _p, _i, _p]),
     "sgemm_rms_norm_i8": (_i, [_i, _i, _i, _f, _p, _i, _p, _i, _p, _p, _i, _p, _i, _p, _p]),
@@ -533,6 +543,22 @@ def sgemm_fp4(type_, format_, M, N, K, A, lda, sfA, scaleA, B, ldb, sfB, scaleB,
     return _lib.sgemm_fp4(_type(type_), _format(format_), M, N, K, _ptr(A), lda, _ptr(sfA),
                           _ptr(scaleA), _ptr(B), ldb, _ptr(sfB), _ptr(scaleB), _ptr(C), ldc,
                           _stream(stream))
+
+
+def sgemm_fp4_tune_force(kernel) -> int:
+    """Process-wide forced kernel of the products (tests and measurement; see
+    include/fp4_gemm.h)."""
+    if isinstance(kernel, str):
+        kernel = FP4_KERNELS[kernel]
+    return _lib.sgemm_fp4_tune_force(kernel)
+
+
+def sgemm_fp4_last_kernel() -> int:
+    return _lib.sgemm_fp4_last_kernel()
+
+
+def sgemm_fp4_last_split_count() -> int:
+    return _lib.sgemm_fp4_last_split_count()
 
 
 # ---- root-mean-square norm (include/rms_norm.h)

@@ -382,6 +382,18 @@ bool encode_operand8(CUtensorMap *map, const signed char *base, long long rows, 
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
+bool encode_block_scales(CUtensorMap *map, const unsigned char *base, long long tiles,
+                         long long row_blocks, int box_tiles, int box_row_blocks)
+{
+    cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(tiles),
+                          static_cast<cuuint64_t>(row_blocks)};
+    cuuint64_t strides[2] = {512, 512 * dims[1]};
+    cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_tiles),
+                         static_cast<cuuint32_t>(box_row_blocks)};
+    return encode3(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, base, dims, strides, box,
+                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
 bool smem_attr_once(const void *kernel, int bytes)
 {
     int dev = 0;

@@ -1,8 +1,11 @@
 // fp4_gemm.cu -- products in microscaled 4-bit floating point
 // (include/fp4_gemm.h): argument checks and kernels.
+#include <atomic>
+
 #include "../../include/fp4_gemm.h"
 #include "dependent.cuh"
 #include "fp4.cuh"
+#include "fp4_tc.cuh"
 #include "rows.cuh"
 
 namespace sg {
@@ -10,94 +13,95 @@ namespace fp4 {
 
 constexpr int kMaxSide = 0x7FFFFFFF - 511;  // an index a tile past the last row or channel still is an int
 
-struct Args {
-    int M, N, K;
-    const unsigned char *A, *sfA, *B, *sfB;
-    long long lda, ldb;  // bytes
-    long long tiles;     // of block scales, per row
-    const float *scaleA, *scaleB;
-    void *C;
-    long long ldc;
-    unsigned int *status;
-    int num_sms;
-};
-
-// ------------------------------------------------------------ plain kernel
-//
-// C tiles of 64 x 64 by 256 threads, 4 x 4 each, over steps of 32 k decoded to
-// fp32 in shared memory.
-constexpr int kPT = 64, kPK = 32;
-
-__device__ __forceinline__ float decode(unsigned code)
+// K == 0: zeros times the scales.
+template <class T>
+__global__ void __launch_bounds__(256) empty_kernel(const Args a)
 {
-    const float m[8] = {0.f, 0.5f, 1.f, 1.5f, 2.f, 3.f, 4.f, 6.f};
-    const float v = m[code & 7];
-    return code & 8 ? -v : v;
+    dependent_release();
+    dependent_wait();
+    const long long all = static_cast<long long>(a.M) * a.N;
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < all; i += gridDim.x * 256LL) {
+        const long long m = i / a.N, n = i - m * a.N;
+        const float sa = a.scaleA != nullptr ? a.scaleA[m] : 1.f;
+        const float sb = a.scaleB != nullptr ? a.scaleB[n] : 1.f;
+        static_cast<T *>(a.C)[m * a.ldc + n] = rows::from_f<T>(0.f * sa * sb);
+    }
 }
 
-template <int FORMAT>
-__device__ __forceinline__ float block_scale(const unsigned char *sf, long long row,
-                                             long long tiles, int block)
+// Clusters of `size` CTAs of the narrow kernel that the GPU runs at once: cached
+// per device.
+int narrow_room(int size, int num_sms)
 {
-    const unsigned b = sf[scale_row(row, tiles) + static_cast<long long>(block / 4) * kTileBytes +
-                          block % 4];
-    if (FORMAT == SGEMM_FP4_MX)
-        return b == 255u ? __int_as_float(0x7FFFFFFF)
-                         : (b == 0u ? 5.877471754111438e-39f : __uint_as_float(b << 23));
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b),
-                                                       __NV_E4M3)));
+    static std::atomic<int> room[64][4];  // sizes 1, 2, 4, 8; 0: not asked yet
+    const int i = size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : 3;
+    int dev = 0;
+    if (size == 1) return num_sms;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms / size / 2;
+    int n = room[dev][i].load();
+    if (n == 0) {
+        auto kern = fp4_kernel<Narrow, float, SGEMM_FP4_NV>;
+        if (smem_attr_once(reinterpret_cast<const void *>(kern), Narrow::SMEM)) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(static_cast<unsigned>(num_sms / size * size));
+            cfg.blockDim = dim3(Narrow::THREADS);
+            cfg.dynamicSmemBytes = Narrow::SMEM;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+        }
+        cudaGetLastError();
+        if (n < 1) n = 1;
+        room[dev][i].store(n);
+    }
+    return n;
+}
+
+std::atomic<int> g_force{SGEMM_FP4_KERNEL_AUTO};
+std::atomic<int> g_last_kernel{SGEMM_FP4_KERNEL_AUTO}, g_last_split{1};
+
+void note_product(int kernel, int split)
+{
+    g_last_kernel.store(kernel, std::memory_order_relaxed);
+    g_last_split.store(split, std::memory_order_relaxed);
 }
 
 template <class T, int FORMAT>
-__global__ void __launch_bounds__(256) plain_kernel(const Args a)
+int run(const Args &a, cudaStream_t st)
 {
-    __shared__ float As[kPK][kPT + 1], Bs[kPK][kPT + 1];
-    dependent_release();
-    dependent_wait();
-    const int tid = threadIdx.x;
-    const long long m0 = static_cast<long long>(blockIdx.y) * kPT;
-    const long long n0 = static_cast<long long>(blockIdx.x) * kPT;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < a.K; k0 += kPK) {
-        for (int i = tid; i < kPT * kPK; i += 256) {
-            const int r = i / kPK, c = i % kPK, k = k0 + c;
-            float x = 0.f, y = 0.f;
-            if (k < a.K && m0 + r < a.M)
-                x = decode(a.A[(m0 + r) * a.lda + k / 2] >> (k % 2 * 4)) *
-                    block_scale<FORMAT>(a.sfA, m0 + r, a.tiles, k / block_of(FORMAT));
-            if (k < a.K && n0 + r < a.N)
-                y = decode(a.B[(n0 + r) * a.ldb + k / 2] >> (k % 2 * 4)) *
-                    block_scale<FORMAT>(a.sfB, n0 + r, a.tiles, k / block_of(FORMAT));
-            As[c][r] = x;
-            Bs[c][r] = y;
-        }
-        __syncthreads();
-        for (int k = 0; k < kPK; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = fmaf(As[k][tid / 16 + 16 * i], Bs[k][tid % 16 + 16 * j], acc[i][j]);
-        __syncthreads();
+    if (a.K == 0) {
+        note_product(SGEMM_FP4_KERNEL_AUTO, 1);
+        return launch_dependent(empty_kernel<T>, dim3(static_cast<unsigned>(2 * a.num_sms)),
+                                dim3(256), 0, 1, st, a);
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const long long m = m0 + tid / 16 + 16 * i, n = n0 + tid % 16 + 16 * j;
-            if (m >= a.M || n >= a.N) continue;
-            const float sa = a.scaleA != nullptr ? a.scaleA[m] : 1.f;
-            const float sb = a.scaleB != nullptr ? a.scaleB[n] : 1.f;
-            static_cast<T *>(a.C)[m * a.ldc + n] = rows::from_f<T>(acc[i][j] * sa * sb);
-        }
+    const int c_bytes = rows::Width().add(a.C).add(a.ldc * sizeof(T)).bytes();
+    const int stages = (a.K + kStageK - 1) / kStageK;
+    const int pairs = ss_slots(a.num_sms);
+    const long long narrow_tiles = ((a.M + Narrow::NT - 1LL) / Narrow::NT) * ((a.N + kCh - 1LL) / kCh);
+    const long long wide_tiles =
+        ((a.M + Wide::NT - 1LL) / Wide::NT) * ((a.N + 2LL * kCh - 1) / (2 * kCh));
+    int split = 1;
+    while (split < 8 && narrow_tiles <= narrow_room(2 * split, a.num_sms) && stages >= 2 * split)
+        split *= 2;
+    int kernel = g_force.load(std::memory_order_relaxed);
+    if (kernel == SGEMM_FP4_KERNEL_AUTO)
+        kernel = narrow_tiles > a.num_sms ? SGEMM_FP4_KERNEL_WIDE : SGEMM_FP4_KERNEL_NARROW;
+    note_product(kernel, kernel == SGEMM_FP4_KERNEL_NARROW ? split : 1);
+    if (kernel == SGEMM_FP4_KERNEL_WIDE)
+        return launch_tc<Wide, T, FORMAT>(a, wide_tiles < pairs ? wide_tiles : pairs, 1, c_bytes, st);
+    // a cluster that shares a tile's k has one tile
+    const long long clusters = split > 1 || narrow_tiles < a.num_sms ? narrow_tiles : a.num_sms;
+    return launch_tc<Narrow, T, FORMAT>(a, clusters, split, c_bytes, st);
 }
 
 template <class T>
 int run(const Args &a, int format, cudaStream_t st)
 {
-    const dim3 grid(static_cast<unsigned>((a.N + kPT - 1LL) / kPT),
-                    static_cast<unsigned>((a.M + kPT - 1LL) / kPT));
-    return launch_dependent(format == SGEMM_FP4_MX ? plain_kernel<T, SGEMM_FP4_MX>
-                                                   : plain_kernel<T, SGEMM_FP4_NV>,
-                            grid, dim3(256), 0, 1, st, a);
+    return format == SGEMM_FP4_MX ? run<T, SGEMM_FP4_MX>(a, st) : run<T, SGEMM_FP4_NV>(a, st);
 }
 
 }  // namespace fp4
@@ -105,7 +109,21 @@ int run(const Args &a, int format, cudaStream_t st)
 
 using namespace sg;
 
-extern "C" int sgemm_fp4(int type, int format, int M, int N, int K, const unsigned char *A,
+extern "C" {
+
+int sgemm_fp4_tune_force(int kernel)
+{
+    if (kernel < SGEMM_FP4_KERNEL_AUTO || kernel > SGEMM_FP4_KERNEL_WIDE)
+        return SGEMM_ERR_INVALID_ARG;
+    fp4::g_force.store(kernel);
+    return SGEMM_OK;
+}
+
+int sgemm_fp4_last_kernel(void) { return fp4::g_last_kernel.load(); }
+
+int sgemm_fp4_last_split_count(void) { return fp4::g_last_split.load(); }
+
+int sgemm_fp4(int type, int format, int M, int N, int K, const unsigned char *A,
                          int lda, const unsigned char *sfA, const float *scaleA,
                          const unsigned char *B, int ldb, const unsigned char *sfB,
                          const float *scaleB, void *C, int ldc, void *stream)
@@ -146,3 +164,5 @@ extern "C" int sgemm_fp4(int type, int format, int M, int N, int K, const unsign
         return fp4::run<float>(a, format, st);
     });
 }
+
+}  // extern "C"

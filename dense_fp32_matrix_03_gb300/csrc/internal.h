@@ -213,6 +213,10 @@ bool encode_operand16(CUtensorMap *map, const void *base, bool bf16, long long r
 // values apart): boxes of 128 k by box_rows rows with the 128-byte swizzle.
 bool encode_operand8(CUtensorMap *map, const signed char *base, long long rows, long long K,
                      long long ld, int E, long long stride, int box_rows);
+// Tensor map of a 4-bit operand's block scales: row blocks of `tiles` tiles of
+// 512 bytes (as 128 32-bit words), in boxes of box_tiles x box_row_blocks tiles.
+bool encode_block_scales(CUtensorMap *map, const unsigned char *base, long long tiles,
+                         long long row_blocks, int box_tiles, int box_row_blocks);
 // Copies Q matrices of 16-bit values into dst as rows x cols K-inner
 // matrices (row pitch ldd, batch stride dstride): dst[r][c] = src[c][r] when
 // trans (src stored cols x rows), else src[r][c] (src row pitch lds).

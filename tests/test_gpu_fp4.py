@@ -333,3 +333,55 @@ def test_quantised_then_multiplied_on_streams_and_in_a_graph(format_, M):
         assert np.all(np.abs(got - ref) <= bound("bf16", K, ref, mag))
         for bufs, _ in eager:
             assert torch.equal(bufs[3], captured[3])
+
+
+@pytest.fixture
+def forced(request):
+    """Every product of the test on one kernel."""
+    import dense_fp32_matrix_03_gb300 as lib
+    lib.check(lib.sgemm_fp4_tune_force(request.param))
+    yield request.param
+    lib.check(lib.sgemm_fp4_tune_force("auto"))
+
+
+# tiles of 128 and 256, one short of them and one past them; k of less than a
+# stage (256), of several times the ring; many tiles a cluster (both
+# accumulators, their shared columns, several rounds)
+KERNEL_SIZES = [(1, 128, 256), (16, 130, 64), (33, 127, 700), (127, 129, 512), (128, 256, 1280),
+                (129, 255, 257), (255, 257, 1536), (256, 256, 2048), (257, 513, 768),
+                (700, 640, 4096), (2100, 1900, 300), (3000, 4100, 128), (64, 30000, 100),
+                (6000, 300, 520)]
+
+
+@pytest.mark.parametrize("type_", ["bf16", "fp32"])
+@pytest.mark.parametrize("format_", FORMATS)
+@pytest.mark.parametrize("forced", ["narrow", "wide"], indirect=True)
+@pytest.mark.parametrize("M,N,K", KERNEL_SIZES)
+def test_every_kernel(forced, type_, format_, M, N, K):
+    import dense_fp32_matrix_03_gb300 as lib
+    rng = np.random.default_rng(M + N + K)
+    a, b = Operand(M, K, format_, rng, wide=False), Operand(N, K, format_, rng, wide=False)
+    got = product(type_, a, b)
+    assert lib.sgemm_fp4_last_kernel() == lib.FP4_KERNELS[forced]
+    ref, mag = ff.product4(a.values, a.sc, b.values, b.sc)
+    assert np.all(np.abs(got - ref) <= bound(type_, K, ref, mag))
+
+
+@pytest.mark.parametrize("forced", ["narrow"], indirect=True)
+@pytest.mark.parametrize("M,N,K", [(40, 128, 512), (100, 300, 1024), (16, 256, 4096),
+                                   (7, 130, 4352), (128, 1000, 2049)])
+def test_clusters_that_share_k(forced, M, N, K):
+    import dense_fp32_matrix_03_gb300 as lib
+    rng = np.random.default_rng(K)
+    for format_ in FORMATS:
+        a, b = Operand(M, K, format_, rng, wide=False), Operand(N, K, format_, rng, wide=False)
+        got = product("fp32", a, b, ldc=N + 1)
+        assert lib.sgemm_fp4_last_split_count() > 1
+        ref, mag = ff.product4(a.values, a.sc, b.values, b.sc)
+        assert np.all(np.abs(got - ref) <= bound("fp32", K, ref, mag))
+
+
+def test_hooks_refuse_what_they_do_not_know():
+    import dense_fp32_matrix_03_gb300 as lib
+    assert lib.sgemm_fp4_tune_force(-1) == lib.SGEMM_ERR_INVALID_ARG
+    assert lib.sgemm_fp4_tune_force(4) == lib.SGEMM_ERR_INVALID_ARG
