@@ -97,25 +97,39 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr)
 // One tile of block scales into four columns of all four lane quarters (of both
 // CTAs of a pair, each from its own shared memory).
 template <int CG>
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc)
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc, uint32_t one)
 {
     if constexpr (CG == 2)
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+                     "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tmem),
+                     "l"(desc), "r"(one)
                      : "memory");
     else
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+                     "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tmem),
+                     "l"(desc), "r"(one)
                      : "memory");
+}
+// Whether this thread is the one of its (converged) warp that issues.
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(one));
+    return one;
 }
 // d (+)= 64 values of k of weights times tokens; it overwrites d unless acc.
 template <int CG, int FORMAT>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t w, uint64_t t, uint32_t idesc,
-                                    uint32_t sw, uint32_t st, uint32_t acc)
+                                    uint32_t sw, uint32_t st, uint32_t acc, uint32_t one)
 {
 #define SG_FP4_MMA(GROUP, VEC)                                                                   \
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                               \
-                 "tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC   \
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\t"                            \
+                 "setp.ne.b32 q, %7, 0;\n\t"                                                     \
+                 "@q tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC   \
                  " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                              \
-                 "l"(w), "l"(t), "r"(idesc), "r"(sw), "r"(st), "r"(acc)                          \
+                 "l"(w), "l"(t), "r"(idesc), "r"(sw), "r"(st), "r"(acc), "r"(one)                \
                  : "memory")
     if constexpr (CG == 2 && FORMAT == SGEMM_FP4_NV)
         SG_FP4_MMA("2", "4X");
@@ -188,7 +202,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint32_t *tmem_base = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_base + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
+    const int lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
     const uint32_t half = CG == 2 ? rank : 0u, krank = CG == 2 ? 0u : rank;
     const int cluster = CG == 2 ? 2 : split;
@@ -228,7 +243,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     tc::tc_fence_before();
     tcp::cluster_sync();
     tc::tc_fence_after();
-    const uint32_t tmem = *tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_base, 0);
     const Abort ab{abort_flag, a.status, kWaitLimitCycles};
     float *part = reinterpret_cast<float *>(base);  // split: [token][channel]
 
@@ -281,30 +296,35 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
     } else if (warp == 1) {
         // -------------------------------------------------------- MMA issuer
-        if (issuer && lane == 0) {
+        // The whole warp walks the loop, so that descriptors and addresses live in
+        // uniform registers, and one elected thread issues: issued by a lane of its
+        // own, each instruction costs some 50 clocks of moves to uniform registers.
+        if (issuer) {
+            const uint32_t one = elect_one();
             Ring<C::STAGES> sr;
             bool ok = true, any = false;
             const uint32_t s0 = smem_u32(base);
             const uint64_t wd = tc::kmajor_sw128_desc(s0), td = tc::kmajor_sw128_desc(s0 + C::OFF_T);
             const uint64_t swd = scale_desc(s0 + C::OFF_SW), std_ = scale_desc(s0 + C::OFF_ST);
-            long long n = 0;  // tiles done
+            int n = 0;  // tiles done
             for (long long u = cid; ok && u < tiles; u += ncl, ++n) {
                 const Job j = job<C>(a, u, half);
                 // the accumulator of two tiles ago is read (and, of a pair, the
                 // columns that the last tile's shares with it)
-                const int buf = static_cast<int>(n & 1);
+                const int buf = n & 1;
                 if (CG == 2 ? n > 0 : n > 1) {
-                    const long long w = CG == 2 ? n - 1 : n - 2;  // the tile waited for
-                    if (!i8::wait_pair<CG>(&acc_free[w & 1], static_cast<uint32_t>(w >> 1) & 1u, ab,
-                                           kStatusWaitAcc)) {
+                    const int w = CG == 2 ? n - 1 : n - 2;  // the tile waited for
+                    if (!i8::warp_wait_pair<CG>(&acc_free[w & 1], static_cast<uint32_t>(w >> 1) & 1u,
+                                                ab, kStatusWaitAcc)) {
                         ok = false;
                         break;
                     }
                 }
                 tc::tc_fence_after();
                 const uint32_t d = tmem + static_cast<uint32_t>(buf) * C::ACC_STEP;
+                const uint32_t idesc = inst_desc<FORMAT>(kCh * CG, j.neff, 0);
                 for (int ks = ks_lo; ks < ks_hi; ++ks) {
-                    if (!i8::wait_pair<CG>(&full[sr.s], sr.ph, ab, kStatusWaitFull)) {
+                    if (!i8::warp_wait_pair<CG>(&full[sr.s], sr.ph, ab, kStatusWaitFull)) {
                         ok = false;
                         break;
                     }
@@ -312,30 +332,31 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     const uint64_t off = static_cast<uint64_t>(sr.s) * (C::STAGE >> 4);
 #pragma unroll
                     for (int i = 0; i < TILES; ++i) {
-                        copy_scales<CG>(tmem + C::SW_COL + 4 * i, swd + off + i * (kTileBytes >> 4));
+                        copy_scales<CG>(tmem + C::SW_COL + 4 * i, swd + off + i * (kTileBytes >> 4),
+                                        one);
 #pragma unroll
                         for (int b = 0; b < C::RB; ++b)
                             copy_scales<CG>(tmem + C::ST_COL + 4 * (i * C::RB + b),
-                                            std_ + off + (b * TILES + i) * (kTileBytes >> 4));
+                                            std_ + off + (b * TILES + i) * (kTileBytes >> 4), one);
                     }
 #pragma unroll
                     for (int i = 0; i < kSteps; ++i) {
                         const int t = FORMAT == SGEMM_FP4_NV ? i : i / 2;
                         const uint32_t id = FORMAT == SGEMM_FP4_NV ? 0u : 2u * (i & 1);
                         mma<CG, FORMAT>(d, wd + off + 2 * i, td + off + 2 * i,
-                                        inst_desc<FORMAT>(kCh * CG, j.neff, id),
-                                        tmem + C::SW_COL + 4 * t, tmem + C::ST_COL + 4 * t * C::RB,
-                                        ks > ks_lo || i > 0 ? 1u : 0u);
+                                        idesc | (id << 4) | (id << 29), tmem + C::SW_COL + 4 * t,
+                                        tmem + C::ST_COL + 4 * t * C::RB,
+                                        ks > ks_lo || i > 0 ? 1u : 0u, one);
                     }
                     any = true;
-                    i8::commit<CG>(&empty[sr.s]);
+                    if (one) i8::commit<CG>(&empty[sr.s]);
                     sr.next();
                 }
                 if (!ok) break;
-                i8::commit<CG>(&acc_full[buf]);
+                if (one) i8::commit<CG>(&acc_full[buf]);
             }
             if (any) {
-                i8::commit<CG>(mma_done);
+                if (one) i8::commit<CG>(mma_done);
                 drain_cl(mma_done, 0, ab.limit);
             }
         }
