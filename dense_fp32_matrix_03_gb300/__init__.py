@@ -55,8 +55,10 @@ SGEMM_FP4_KERNEL_AUTO = 0
 SGEMM_FP4_KERNEL_FEW = 1
 SGEMM_FP4_KERNEL_NARROW = 2
 SGEMM_FP4_KERNEL_WIDE = 3
+SGEMM_FP4_KERNEL_SLIM = 4
 FP4_KERNELS = {"auto": SGEMM_FP4_KERNEL_AUTO, "few": SGEMM_FP4_KERNEL_FEW,
-               "narrow": SGEMM_FP4_KERNEL_NARROW, "wide": SGEMM_FP4_KERNEL_WIDE}
+               "narrow": SGEMM_FP4_KERNEL_NARROW, "wide": SGEMM_FP4_KERNEL_WIDE,
+               "slim": SGEMM_FP4_KERNEL_SLIM}
 
 SGEMM_EXPERTS_I8 = 0
 SGEMM_EXPERTS_SAME = 1

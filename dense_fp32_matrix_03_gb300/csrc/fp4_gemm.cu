@@ -1,10 +1,12 @@
 // fp4_gemm.cu -- products in microscaled 4-bit floating point
 // (include/fp4_gemm.h): argument checks and kernels.
 #include <atomic>
+#include <cstdlib>
 
 #include "../../include/fp4_gemm.h"
 #include "dependent.cuh"
 #include "fp4.cuh"
+#include "fp4_few.cuh"
 #include "fp4_tc.cuh"
 #include "rows.cuh"
 
@@ -28,23 +30,25 @@ __global__ void __launch_bounds__(256) empty_kernel(const Args a)
     }
 }
 
-// Clusters of `size` CTAs of the narrow kernel that the GPU runs at once: cached
-// per device.
-int narrow_room(int size, int num_sms)
+// Clusters of `size` CTAs of C's kernel that the GPU runs at once: cached per
+// device.  (A cluster stays within a processor group, so 152 multiprocessors hold
+// fewer than 19 of 8.)
+template <class C>
+int room(int size, int num_sms)
 {
-    static std::atomic<int> room[64][4];  // sizes 1, 2, 4, 8; 0: not asked yet
+    static std::atomic<int> known[64][4];  // sizes 1, 2, 4, 8; 0: not asked yet
     const int i = size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : 3;
     int dev = 0;
     if (size == 1) return num_sms;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms / size / 2;
-    int n = room[dev][i].load();
+    int n = known[dev][i].load();
     if (n == 0) {
-        auto kern = fp4_kernel<Narrow, float, SGEMM_FP4_NV>;
-        if (smem_attr_once(reinterpret_cast<const void *>(kern), Narrow::SMEM)) {
+        auto kern = fp4_kernel<C, float, SGEMM_FP4_NV>;
+        if (smem_attr_once(reinterpret_cast<const void *>(kern), C::SMEM)) {
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(static_cast<unsigned>(num_sms / size * size));
-            cfg.blockDim = dim3(Narrow::THREADS);
-            cfg.dynamicSmemBytes = Narrow::SMEM;
+            cfg.blockDim = dim3(C::THREADS);
+            cfg.dynamicSmemBytes = C::SMEM;
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
             attr[0].val.clusterDim.x = static_cast<unsigned>(size);
@@ -56,7 +60,7 @@ int narrow_room(int size, int num_sms)
         }
         cudaGetLastError();
         if (n < 1) n = 1;
-        room[dev][i].store(n);
+        known[dev][i].store(n);
     }
     return n;
 }
@@ -70,6 +74,20 @@ void note_product(int kernel, int split)
     g_last_split.store(split, std::memory_order_relaxed);
 }
 
+// One CTA a tile, or a cluster that shares the tile's k.
+template <class C, class T, int FORMAT>
+int launch_split(const Args &a, int kernel, int c_bytes, cudaStream_t st)
+{
+    const int stages = (a.K + kStageK - 1) / kStageK;
+    const long long tiles = ((a.M + C::NT - 1LL) / C::NT) * ((a.N + kCh - 1LL) / kCh);
+    int split = 1;
+    static const int per = getenv("SG_PER") ? atoi(getenv("SG_PER")) : 1, ms = getenv("SG_MS") ? atoi(getenv("SG_MS")) : 8;
+    while (split < ms && tiles <= room<C>(2 * split, a.num_sms) && stages >= 2 * split * per) split *= 2;
+    note_product(kernel, split);
+    const long long all = room<C>(1, a.num_sms);
+    return launch_tc<C, T, FORMAT>(a, split > 1 || tiles < all ? tiles : all, split, c_bytes, st);
+}
+
 template <class T, int FORMAT>
 int run(const Args &a, cudaStream_t st)
 {
@@ -79,23 +97,31 @@ int run(const Args &a, cudaStream_t st)
                                 dim3(256), 0, 1, st, a);
     }
     const int c_bytes = rows::Width().add(a.C).add(a.ldc * sizeof(T)).bytes();
-    const int stages = (a.K + kStageK - 1) / kStageK;
     const int pairs = ss_slots(a.num_sms);
     const long long narrow_tiles = ((a.M + Narrow::NT - 1LL) / Narrow::NT) * ((a.N + kCh - 1LL) / kCh);
     const long long wide_tiles =
         ((a.M + Wide::NT - 1LL) / Wide::NT) * ((a.N + 2LL * kCh - 1) / (2 * kCh));
-    int split = 1;
-    while (split < 8 && narrow_tiles <= narrow_room(2 * split, a.num_sms) && stages >= 2 * split)
-        split *= 2;
+    const bool few_can = a.M <= kFewTokens;
     int kernel = g_force.load(std::memory_order_relaxed);
+    // (one token tile: its scales begin with a tile of theirs)
+    const bool slim_can = a.M <= Slim::NT;
+    if ((kernel == SGEMM_FP4_KERNEL_FEW && !few_can) || (kernel == SGEMM_FP4_KERNEL_SLIM && !slim_can))
+        kernel = SGEMM_FP4_KERNEL_AUTO;
+    if (kernel == SGEMM_FP4_KERNEL_AUTO && few_can) kernel = SGEMM_FP4_KERNEL_FEW;
     if (kernel == SGEMM_FP4_KERNEL_AUTO)
-        kernel = narrow_tiles > a.num_sms ? SGEMM_FP4_KERNEL_WIDE : SGEMM_FP4_KERNEL_NARROW;
-    note_product(kernel, kernel == SGEMM_FP4_KERNEL_NARROW ? split : 1);
-    if (kernel == SGEMM_FP4_KERNEL_WIDE)
-        return launch_tc<Wide, T, FORMAT>(a, wide_tiles < pairs ? wide_tiles : pairs, 1, c_bytes, st);
-    // a cluster that shares a tile's k has one tile
-    const long long clusters = split > 1 || narrow_tiles < a.num_sms ? narrow_tiles : a.num_sms;
-    return launch_tc<Narrow, T, FORMAT>(a, clusters, split, c_bytes, st);
+        kernel = narrow_tiles > a.num_sms ? SGEMM_FP4_KERNEL_WIDE
+                                          : (slim_can ? SGEMM_FP4_KERNEL_SLIM : SGEMM_FP4_KERNEL_NARROW);
+    if (kernel == SGEMM_FP4_KERNEL_SLIM)
+        return launch_split<Slim, T, FORMAT>(a, kernel, c_bytes, st);
+    if (kernel == SGEMM_FP4_KERNEL_NARROW)
+        return launch_split<Narrow, T, FORMAT>(a, kernel, c_bytes, st);
+    note_product(kernel, 1);
+    if (kernel == SGEMM_FP4_KERNEL_FEW) {
+        if (a.M == 1) return launch_few<T, FORMAT, 1>(a, st);
+        if (a.M == 2) return launch_few<T, FORMAT, 2>(a, st);
+        return launch_few<T, FORMAT, 4>(a, st);
+    }
+    return launch_tc<Wide, T, FORMAT>(a, wide_tiles < pairs ? wide_tiles : pairs, 1, c_bytes, st);
 }
 
 template <class T>
@@ -113,7 +139,7 @@ extern "C" {
 
 int sgemm_fp4_tune_force(int kernel)
 {
-    if (kernel < SGEMM_FP4_KERNEL_AUTO || kernel > SGEMM_FP4_KERNEL_WIDE)
+    if (kernel < SGEMM_FP4_KERNEL_AUTO || kernel > SGEMM_FP4_KERNEL_SLIM)
         return SGEMM_ERR_INVALID_ARG;
     fp4::g_force.store(kernel);
     return SGEMM_OK;

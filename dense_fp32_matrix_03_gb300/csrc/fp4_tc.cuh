@@ -14,6 +14,7 @@
 //   narrow  one CTA, 128 channels x up to 128 tokens; a cluster of up to 8 CTAs
 //           may share a tile, each a part of k, whose partial sums meet in
 //           distributed shared memory, in CTA order
+//   slim    the same for up to 32 tokens in all, with a deeper ring
 //   wide    a CTA pair (cta_group::2), 256 channels x 256 tokens
 //
 // Tensor memory, wide: two accumulators of 256 columns do not fit beside the
@@ -55,9 +56,11 @@ constexpr int kMmaK = 64;
 constexpr int kSteps = kStageK / kMmaK;
 constexpr int kEWarp0 = 4;
 
-template <int CG_, int NT_, int STAGES_, int EWARPS_>
+// TCOLS: columns of tensor memory to allocate.
+template <int CG_, int NT_, int STAGES_, int EWARPS_, uint32_t TCOLS_>
 struct Cfg {
     static constexpr int CG = CG_, NT = NT_, STAGES = STAGES_, EWARPS = EWARPS_;
+    static constexpr uint32_t TCOLS = TCOLS_;
     static constexpr int NTC = NT / CG;         // tokens per CTA's half
     static constexpr int RB = (NT + 127) / 128; // row blocks of the tokens' scales
     static constexpr int W_BYTES = kCh * 128, T_BYTES = NTC * 128;
@@ -75,13 +78,29 @@ struct Cfg {
     // columns of tensor memory: accumulators, then the scales of a stage
     static constexpr uint32_t ACC_STEP = NT == 256 ? 208 : NT;
     static constexpr uint32_t SW_COL = ACC_STEP + NT, ST_COL = SW_COL + 4 * kSteps;
-    static_assert(ST_COL + 4 * kSteps * RB <= 512, "tensor-memory columns");
+    static_assert(ST_COL + 4 * kSteps * RB <= TCOLS && TCOLS <= 512, "tensor-memory columns");
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
     static_assert(STAGE % 1024 == 0, "swizzled boxes on 1024 bytes");
     static_assert(CG == 2 || NT * kCh * 4 <= STAGES * STAGE, "partial sums fit the stages");
 };
-using Narrow = Cfg<1, 128, 5, 4>;
-using Wide = Cfg<2, 256, 5, 8>;
+using Slim = Cfg<1, 32, 8, 4, 128>;
+using Narrow = Cfg<1, 128, 5, 4, 512>;
+using Wide = Cfg<2, 256, 5, 8, 512>;
+
+// As tcs::tma_load_pair, to the same place of both CTAs of the pair.  (Two pairs
+// that shared their tokens this way too moved a quarter fewer bytes in the same
+// time a stage, and 36 clusters of four leave eight multiprocessors idle.)
+__device__ __forceinline__ void tma_load_both(void *smem_dst, const CUtensorMap *m, uint32_t bar,
+                                              int c0, int c1, int c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".multicast::cluster.cta_group::2 [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(
+            smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
 
 // A copy's source: 32 rows of 16 bytes without swizzle, eight rows 128 bytes
 // apart from the next eight.
@@ -177,8 +196,8 @@ __device__ __forceinline__ Job job(const Args &a, long long u, uint32_t half)
 }
 
 // tmW, tmT: codes as bytes (K / 2, rows) in boxes of 128 bytes by 128 rows,
-// 128-byte swizzle; tmSW, tmST: block scales in boxes of a stage's tiles by one
-// row block (tokens: RB).  What a box holds past the last row, value or scale is
+// 128-byte swizzle; tmSW, tmST: block scales in boxes of a stage's tiles of one
+// row block.  What a box holds past the last row, value or scale is
 // zeros.  split: CTAs of the cluster that share a tile's k (narrow only); then
 // each cluster has one tile.  c_bytes: accesses that C's rows allow.
 template <class C, class T, int FORMAT>
@@ -215,6 +234,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int ks_hi = static_cast<int>(static_cast<long long>(stages) * (krank + 1) / split);
     const long long tiles = ((a.M + C::NT - 1LL) / C::NT) * ((a.N + kCh * CG - 1LL) / (kCh * CG));
 
+
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1u);
@@ -234,14 +254,26 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     if (warp == 1) {
         if constexpr (CG == 2)
-            tcp::tmem_alloc_pair(tmem_base, 512);
+            tcp::tmem_alloc_pair(tmem_base, C::TCOLS);
         else
-            tc::tmem_alloc(tmem_base, 512);
+            tc::tmem_alloc(tmem_base, C::TCOLS);
     }
     dependent_release();
+    // few tokens: the weights start on their way into L2 while the kernel before
+    // (the quantiser, as a rule) runs; nothing is read yet
+    if (CG == 1 && warp == 3 && lane == 0 && cid < tiles) {
+        const int ch0 = job<C>(a, cid, 0).ch0;
+        for (int ks = ks_lo; ks < ks_hi && ks < ks_lo + 16; ++ks) {
+            i8::tma_prefetch_3d(&tmW, ks * 128, ch0, 0);
+            i8::tma_prefetch_3d(&tmSW, 0, ks * TILES, ch0 / kTileRows);
+        }
+    }
     dependent_wait();
     tc::tc_fence_before();
-    tcp::cluster_sync();
+    if constexpr (CG == 2)
+        tcp::cluster_sync();
+    else
+        __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_base, 0);
     const Abort ab{abort_flag, a.status, kWaitLimitCycles};
@@ -268,8 +300,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         tcs::tma_load_pair(st, &tmW, fb, ks * 128, j.ch0, 0);
                         tcs::tma_load_pair(st + C::OFF_T, &tmT, fb, ks * 128, first, 0);
                         tcs::tma_load_pair(st + C::OFF_SW, &tmSW, fb, 0, ks * TILES, j.ch0 / kTileRows);
-                        tcs::tma_load_pair(st + C::OFF_ST, &tmST, fb, 0, ks * TILES,
-                                           static_cast<int>(j.row0 / kTileRows));
+                        // both CTAs need all tokens' scales: each loads a row block
+                        tma_load_both(st + C::OFF_ST + static_cast<int>(half) * TILES * kTileBytes,
+                                      &tmST, fb, 0, ks * TILES,
+                                      static_cast<int>(j.row0 / kTileRows) + static_cast<int>(half));
                     } else {
                         mbar_arrive_expect_tx(&full[rr.s], BYTES);
                         tma_load_3d(st, &tmW, &full[rr.s], ks * 128, j.ch0, 0);
@@ -593,13 +627,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // ---- teardown: no CTA leaves while another may touch its shared memory
     tc::tc_fence_before();
     __syncwarp();
-    tcp::cluster_sync();
+    if (CG == 2 || split > 1) {
+        tcp::cluster_sync();
+    } else {
+        __syncthreads();
+    }
     if (warp == 1) {
         tc::tc_fence_after();
         if constexpr (CG == 2)
-            tcp::tmem_dealloc_pair(tmem, 512);
+            tcp::tmem_dealloc_pair(tmem, C::TCOLS);
         else
-            tc::tmem_dealloc(tmem, 512);
+            tc::tmem_dealloc(tmem, C::TCOLS);
     }
 }
 
@@ -615,8 +653,7 @@ int launch_tc(const Args &a, long long clusters, int split, int c_bytes, cudaStr
         !encode_operand8(&tmT, reinterpret_cast<const signed char *>(a.A), a.M, bytes, a.lda, 1, 0,
                          C::NTC) ||
         !encode_block_scales(&tmSW, a.sfB, a.tiles, (a.N + kTileRows - 1LL) / kTileRows, TILES, 1) ||
-        !encode_block_scales(&tmST, a.sfA, a.tiles, (a.M + kTileRows - 1LL) / kTileRows, TILES,
-                             C::RB))
+        !encode_block_scales(&tmST, a.sfA, a.tiles, (a.M + kTileRows - 1LL) / kTileRows, TILES, 1))
         return SGEMM_ERR_LAUNCH;
     auto kern = fp4_kernel<C, T, FORMAT>;
     if (!smem_attr_once(reinterpret_cast<const void *>(kern), C::SMEM)) return SGEMM_ERR_LAUNCH;

@@ -85,12 +85,13 @@ int sgemm_fp4(int type, int format, int M, int N, int K, const unsigned char *A,
               const unsigned char *sfA, const float *scaleA, const unsigned char *B, int ldb,
               const unsigned char *sfB, const float *scaleB, void *C, int ldc, void *stream);
 
-/* Hooks for tests and measurement.  A product runs on one of three kernels,
+/* Hooks for tests and measurement.  A product runs on one of four kernels,
  * chosen by a rule on its sizes:
- *   FEW     few tokens
+ *   FEW     up to four tokens
  *   NARROW  tensor cores, 128 channels x 128 tokens a CTA; the CTAs of a
  *           cluster may share a tile's k ("split")
  *   WIDE    tensor cores, 256 channels x 256 tokens a CTA pair
+ *   SLIM    as NARROW, up to 32 tokens
  * sgemm_fp4_tune_force(kernel) makes every later product in the process take
  * that kernel (AUTO: the rule again; a product the kernel cannot take follows
  * the rule); SGEMM_ERR_INVALID_ARG for an unknown one.  It is a process-wide
@@ -103,6 +104,7 @@ int sgemm_fp4(int type, int format, int M, int N, int K, const unsigned char *A,
 #define SGEMM_FP4_KERNEL_FEW 1
 #define SGEMM_FP4_KERNEL_NARROW 2
 #define SGEMM_FP4_KERNEL_WIDE 3
+#define SGEMM_FP4_KERNEL_SLIM 4
 int sgemm_fp4_tune_force(int kernel);
 int sgemm_fp4_last_kernel(void);
 int sgemm_fp4_last_split_count(void);

@@ -347,7 +347,7 @@ def forced(request):
 # tiles of 128 and 256, one short of them and one past them; k of less than a
 # stage (256), of several times the ring; many tiles a cluster (both
 # accumulators, their shared columns, several rounds)
-KERNEL_SIZES = [(1, 128, 256), (16, 130, 64), (33, 127, 700), (127, 129, 512), (128, 256, 1280),
+KERNEL_SIZES = [(1, 128, 256), (16, 130, 64), (32, 1000, 3000), (3, 60000, 300), (64, 200, 2600), (33, 127, 700), (127, 129, 512), (128, 256, 1280),
                 (129, 255, 257), (255, 257, 1536), (256, 256, 2048), (257, 513, 768),
                 (700, 640, 4096), (2100, 1900, 300), (3000, 4100, 128), (64, 30000, 100),
                 (6000, 300, 520)]
@@ -355,19 +355,36 @@ KERNEL_SIZES = [(1, 128, 256), (16, 130, 64), (33, 127, 700), (127, 129, 512), (
 
 @pytest.mark.parametrize("type_", ["bf16", "fp32"])
 @pytest.mark.parametrize("format_", FORMATS)
-@pytest.mark.parametrize("forced", ["narrow", "wide"], indirect=True)
+@pytest.mark.parametrize("forced", ["slim", "narrow", "wide"], indirect=True)
 @pytest.mark.parametrize("M,N,K", KERNEL_SIZES)
 def test_every_kernel(forced, type_, format_, M, N, K):
     import dense_fp32_matrix_03_gb300 as lib
     rng = np.random.default_rng(M + N + K)
     a, b = Operand(M, K, format_, rng, wide=False), Operand(N, K, format_, rng, wide=False)
     got = product(type_, a, b)
-    assert lib.sgemm_fp4_last_kernel() == lib.FP4_KERNELS[forced]
+    if forced != "slim" or M <= 32:  # (it takes no more)
+        assert lib.sgemm_fp4_last_kernel() == lib.FP4_KERNELS[forced]
     ref, mag = ff.product4(a.values, a.sc, b.values, b.sc)
     assert np.all(np.abs(got - ref) <= bound(type_, K, ref, mag))
 
 
-@pytest.mark.parametrize("forced", ["narrow"], indirect=True)
+@pytest.mark.parametrize("type_", TYPES)
+@pytest.mark.parametrize("format_", FORMATS)
+@pytest.mark.parametrize("forced", ["few"], indirect=True)
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 33, 1023), (2, 128, 1024), (3, 129, 1025),
+                                   (4, 250, 4096), (1, 1000, 5000), (2, 4, 9001), (4, 97, 31),
+                                   (3, 640, 2048), (1, 130, 64)])
+def test_few_tokens(forced, type_, format_, M, N, K):
+    import dense_fp32_matrix_03_gb300 as lib
+    rng = np.random.default_rng(M + N + K)
+    a, b = Operand(M, K, format_, rng, wide=False), Operand(N, K, format_, rng, wide=False)
+    got = product(type_, a, b, ldc=N + 3)
+    assert lib.sgemm_fp4_last_kernel() == lib.SGEMM_FP4_KERNEL_FEW
+    ref, mag = ff.product4(a.values, a.sc, b.values, b.sc)
+    assert np.all(np.abs(got - ref) <= bound(type_, K, ref, mag))
+
+
+@pytest.mark.parametrize("forced", ["slim", "narrow"], indirect=True)
 @pytest.mark.parametrize("M,N,K", [(40, 128, 512), (100, 300, 1024), (16, 256, 4096),
                                    (7, 130, 4352), (128, 1000, 2049)])
 def test_clusters_that_share_k(forced, M, N, K):
@@ -384,4 +401,4 @@ def test_clusters_that_share_k(forced, M, N, K):
 def test_hooks_refuse_what_they_do_not_know():
     import dense_fp32_matrix_03_gb300 as lib
     assert lib.sgemm_fp4_tune_force(-1) == lib.SGEMM_ERR_INVALID_ARG
-    assert lib.sgemm_fp4_tune_force(4) == lib.SGEMM_ERR_INVALID_ARG
+    assert lib.sgemm_fp4_tune_force(5) == lib.SGEMM_ERR_INVALID_ARG
