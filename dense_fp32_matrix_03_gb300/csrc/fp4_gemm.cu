@@ -1,7 +1,6 @@
 // fp4_gemm.cu -- products in microscaled 4-bit floating point
 // (include/fp4_gemm.h): argument checks and kernels.
 #include <atomic>
-#include <cstdlib>
 
 #include "../../include/fp4_gemm.h"
 #include "dependent.cuh"
@@ -74,18 +73,19 @@ void note_product(int kernel, int split)
     g_last_split.store(split, std::memory_order_relaxed);
 }
 
-// One CTA a tile, or a cluster that shares the tile's k.
-template <class C, class T, int FORMAT>
-int launch_split(const Args &a, int kernel, int c_bytes, cudaStream_t st)
+// CTAs that share a tile's k: worth their cluster (launched and met twice, 1.7 us)
+// where k is long and tiles are few, and each keeps four stages or more.  us, alone /
+// shared: 1 token 4096 x 1024 3.6 / 4.4, x 2048 4.8 / 4.8, x 4096 7.3 / 5.8; 48 tokens
+// 2048 x 1024 3.8 / 4.7, 4096 x 4096 7.7 / 7.3, 8192 x 8192 13.5 / 11.9; the sums of
+// two token tiles cost more than they save: 256 x 4096 x 4096 8.6 / 9.9.
+template <class C>
+int shared_k(const Args &a, long long tiles)
 {
     const int stages = (a.K + kStageK - 1) / kStageK;
-    const long long tiles = ((a.M + C::NT - 1LL) / C::NT) * ((a.N + kCh - 1LL) / kCh);
     int split = 1;
-    static const int per = getenv("SG_PER") ? atoi(getenv("SG_PER")) : 1, ms = getenv("SG_MS") ? atoi(getenv("SG_MS")) : 8;
-    while (split < ms && tiles <= room<C>(2 * split, a.num_sms) && stages >= 2 * split * per) split *= 2;
-    note_product(kernel, split);
-    const long long all = room<C>(1, a.num_sms);
-    return launch_tc<C, T, FORMAT>(a, split > 1 || tiles < all ? tiles : all, split, c_bytes, st);
+    if (a.M > C::NT || stages < (C::NT <= 32 ? 12 : 16)) return 1;
+    while (split < 8 && tiles <= room<C>(2 * split, a.num_sms) && stages >= 8 * split) split *= 2;
+    return split;
 }
 
 template <class T, int FORMAT>
@@ -97,31 +97,55 @@ int run(const Args &a, cudaStream_t st)
                                 dim3(256), 0, 1, st, a);
     }
     const int c_bytes = rows::Width().add(a.C).add(a.ldc * sizeof(T)).bytes();
-    const int pairs = ss_slots(a.num_sms);
-    const long long narrow_tiles = ((a.M + Narrow::NT - 1LL) / Narrow::NT) * ((a.N + kCh - 1LL) / kCh);
-    const long long wide_tiles =
-        ((a.M + Wide::NT - 1LL) / Wide::NT) * ((a.N + 2LL * kCh - 1) / (2 * kCh));
+    const int stages = (a.K + kStageK - 1) / kStageK, pairs = ss_slots(a.num_sms);
+    const long long cts = (a.N + kCh - 1LL) / kCh;  // channel tiles of one CTA
+    const long long tiles = (a.M + Narrow::NT - 1LL) / Narrow::NT * cts;
     const bool few_can = a.M <= kFewTokens;
-    int kernel = g_force.load(std::memory_order_relaxed);
     // (one token tile: its scales begin with a tile of theirs)
     const bool slim_can = a.M <= Slim::NT;
+    int kernel = g_force.load(std::memory_order_relaxed);
     if ((kernel == SGEMM_FP4_KERNEL_FEW && !few_can) || (kernel == SGEMM_FP4_KERNEL_SLIM && !slim_can))
         kernel = SGEMM_FP4_KERNEL_AUTO;
-    if (kernel == SGEMM_FP4_KERNEL_AUTO && few_can) kernel = SGEMM_FP4_KERNEL_FEW;
+    int split = 1;
+    if (kernel == SGEMM_FP4_KERNEL_AUTO || kernel == SGEMM_FP4_KERNEL_SLIM) {
+        if (slim_can) split = shared_k<Slim>(a, cts);
+        if (slim_can && kernel == SGEMM_FP4_KERNEL_AUTO) {
+            kernel = SGEMM_FP4_KERNEL_SLIM;
+            if (few_can) {
+                // The kernels' times in us, as measured on GB300: few / slim, 1 token 1024
+                // x 1024 2.8 / 3.7, 2048 x 1024 3.1 / 3.7, 2048 x 2048 3.6 / 4.8, 8192 x 512
+                // 4.3 / 3.3, 4096 x 4096 8.1 / 5.8; 4 tokens 1024 x 1024 4.6 / 3.7
+                const double per = a.M == 1 ? 0.33 : a.M == 2 ? 0.41 : 0.78;
+                const double few = 2.4 + per * 1e-6 * a.N * a.K;
+                const double waves = static_cast<double>((cts * split + a.num_sms - 1) / a.num_sms);
+                const double slim = 2.5 + 0.31 * stages / split * waves + (split > 1 ? 1.7 : 0.);
+                if (few < slim) kernel = SGEMM_FP4_KERNEL_FEW;
+            }
+        }
+    }
+    // us, narrow / wide: 128 x 4096 x 4096 8.2 / 9.6, 512 9.3 / 10.9, 1024 (256 tiles of the
+    // narrow kernel) 14.2 / 11.3, 512 x 8192 x 8192 23.2 / 17.2, 2048 x 2048 x 1024 8.0 /
+    // 7.3, 1024 x 4092 x 256 7.1 / 6.7: one wave of narrow tiles, or wide ones
     if (kernel == SGEMM_FP4_KERNEL_AUTO)
-        kernel = narrow_tiles > a.num_sms ? SGEMM_FP4_KERNEL_WIDE
-                                          : (slim_can ? SGEMM_FP4_KERNEL_SLIM : SGEMM_FP4_KERNEL_NARROW);
-    if (kernel == SGEMM_FP4_KERNEL_SLIM)
-        return launch_split<Slim, T, FORMAT>(a, kernel, c_bytes, st);
-    if (kernel == SGEMM_FP4_KERNEL_NARROW)
-        return launch_split<Narrow, T, FORMAT>(a, kernel, c_bytes, st);
-    note_product(kernel, 1);
-    if (kernel == SGEMM_FP4_KERNEL_FEW) {
+        kernel = tiles > a.num_sms ? SGEMM_FP4_KERNEL_WIDE : SGEMM_FP4_KERNEL_NARROW;
+    if (kernel == SGEMM_FP4_KERNEL_NARROW) split = shared_k<Narrow>(a, tiles);
+    note_product(kernel, kernel == SGEMM_FP4_KERNEL_SLIM || kernel == SGEMM_FP4_KERNEL_NARROW ? split : 1);
+    switch (kernel) {
+    case SGEMM_FP4_KERNEL_FEW:
         if (a.M == 1) return launch_few<T, FORMAT, 1>(a, st);
         if (a.M == 2) return launch_few<T, FORMAT, 2>(a, st);
         return launch_few<T, FORMAT, 4>(a, st);
+    case SGEMM_FP4_KERNEL_SLIM:
+        return launch_tc<Slim, T, FORMAT>(a, split > 1 || cts < a.num_sms ? cts : a.num_sms, split,
+                                          c_bytes, st);
+    case SGEMM_FP4_KERNEL_NARROW:
+        return launch_tc<Narrow, T, FORMAT>(a, split > 1 || tiles < a.num_sms ? tiles : a.num_sms,
+                                            split, c_bytes, st);
+    default: {
+        const long long wide = (a.M + Wide::NT - 1LL) / Wide::NT * ((a.N + 2LL * kCh - 1) / (2 * kCh));
+        return launch_tc<Wide, T, FORMAT>(a, wide < pairs ? wide : pairs, 1, c_bytes, st);
     }
-    return launch_tc<Wide, T, FORMAT>(a, wide_tiles < pairs ? wide_tiles : pairs, 1, c_bytes, st);
+    }
 }
 
 template <class T>

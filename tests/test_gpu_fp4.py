@@ -385,8 +385,8 @@ def test_few_tokens(forced, type_, format_, M, N, K):
 
 
 @pytest.mark.parametrize("forced", ["slim", "narrow"], indirect=True)
-@pytest.mark.parametrize("M,N,K", [(40, 128, 512), (100, 300, 1024), (16, 256, 4096),
-                                   (7, 130, 4352), (128, 1000, 2049)])
+@pytest.mark.parametrize("M,N,K", [(16, 128, 4096), (30, 300, 5000), (16, 256, 8192),
+                                   (7, 130, 4352), (32, 1000, 9001), (3, 4000, 6145)])
 def test_clusters_that_share_k(forced, M, N, K):
     import dense_fp32_matrix_03_gb300 as lib
     rng = np.random.default_rng(K)
