@@ -14,10 +14,13 @@
 // the weights and token g; which k it holds is ours to choose as long as both
 // operands agree, so a lane takes 16 consecutive bytes of a weight row at a
 // time and the same k of the token: every load is 16 bytes, a quad reads 64
-// bytes of a row together, nothing passes through shared memory.
+// bytes of a row together.  The weights come by asynchronous copies into a ring
+// that each lane fills and reads for itself, so that many are on their way
+// without registers or barriers.
 #include <type_traits>
 
 #include "../../include/expert_layer.h"
+#include "common.cuh"
 #include "dependent.cuh"
 #include "rows.cuh"
 
@@ -188,24 +191,18 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 bytes of a row of ES-byte values from value k on; zeros past K, nothing
-// past K is read.  VEC: the row starts on a 16-byte boundary.
-template <int ES, bool VEC>
-__device__ __forceinline__ uint4 load16(const char *row, int k, int K)
+// Eight 16-bit values of a row from value k on; zeros past K, nothing past K is
+// read.  VEC: the row starts on a 16-byte boundary.
+template <bool VEC>
+__device__ __forceinline__ uint4 load_token(const char *row, int k, int K)
 {
-    constexpr int N = 16 / ES;
-    if (VEC && k + N <= K) return *reinterpret_cast<const uint4 *>(row + static_cast<long long>(k) * ES);
+    if (VEC && k + 8 <= K) return *reinterpret_cast<const uint4 *>(row + static_cast<long long>(k) * 2);
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (k + i < K) {
-            if (ES == 1)
-                w[i / 4] |= static_cast<uint32_t>(reinterpret_cast<const unsigned char *>(row)[k + i])
-                            << (8 * (i % 4));
-            else
-                w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[k + i])
-                            << (16 * (i % 2));
-        }
+    for (int i = 0; i < 8; ++i)
+        if (k + i < K)
+            w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[k + i])
+                        << (16 * (i % 2));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -234,118 +231,188 @@ struct Weights {
     }
 };
 
-// One step (STEP values of k from k0 on) of CF fragments of weights and NF of
-// tokens: acc += weights * tokens.  wrow: rows g and g + 8 of each fragment;
-// trow: token g of each.  Lane t takes k0 + N t + 4 N i + 0 .. N-1 of piece i.
-template <class T, bool I8, int CF, int NF, bool XV>
-__device__ __forceinline__ void step(float (&acc)[CF][NF][4], const char *const (&wrow)[CF][2],
-                                     const char *const (&trow)[NF], int k0, int K, int t,
-                                     int tokens)
-{
+// The lane's ring of weight pieces: DEPTH steps of 2 CF rows (g and g + 8 of each
+// fragment) times two pieces of 16 bytes.
+template <class T, bool I8, int CF, int DEPTH>
+struct Pieces {
     using W = Weights<T, I8>;
-    uint4 w[CF][2][2], x[NF][2][W::TOK];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int k = k0 + W::N * t + 4 * W::N * i;
+    static constexpr int PER = 4 * CF;                       // pieces a step
+    static constexpr int BYTES = DEPTH * PER * 32 * 16;      // a warp's ring
+    uint32_t base;  // of this lane
+    int t;
+    __device__ __forceinline__ Pieces(void *smem, int warp, int lane)
+        : base(smem_u32(smem) + static_cast<uint32_t>(warp * BYTES + lane * 16)), t(lane & 3)
+    {
+    }
+    // Copies the step from k0 on of the rows; zeros past K, nothing past K is read.
+    __device__ __forceinline__ void ask(int slot, const char *const (&row)[CF][2], int k0, int K)
+    {
 #pragma unroll
         for (int c = 0; c < CF; ++c)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) w[c][r][i] = load16<W::ES, true>(wrow[c][r], k, K);
-    }
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int k = k0 + W::N * t + 4 * W::N * i;
-#pragma unroll
-        for (int n = 0; n < NF; ++n)
-#pragma unroll
-            for (int j = 0; j < W::TOK; ++j) x[n][i][j] = load16<2, XV>(trow[n], k + 8 * j, K);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int c = 0; c < CF; ++c) {
-            uint32_t lo[W::N / 2], hi[W::N / 2];
-            W::pairs(w[c][0][i], lo);
-            W::pairs(w[c][1][i], hi);
-#pragma unroll
-            for (int n = 0; n < NF; ++n)
-                if (n == 0 || 8 * n < tokens) {
-#pragma unroll
-                    for (int j = 0; j < W::N / 4; ++j) {
-                        const uint4 &v = x[n][i][j / 2];
-                        mma<T>(acc[c][n], lo[2 * j], hi[2 * j], lo[2 * j + 1], hi[2 * j + 1],
-                               j % 2 ? v.z : v.x, j % 2 ? v.w : v.y);
-                    }
+                for (int i = 0; i < 2; ++i) {
+                    const int k = k0 + W::N * t + 4 * W::N * i;
+                    const int left = min(max((K - k) * W::ES, 0), 16);
+                    cp_async_16(base + static_cast<uint32_t>((slot * PER + (c * 2 + r) * 2 + i) * 512),
+                                row[c][r] + (left > 0 ? static_cast<long long>(k) * W::ES : 0LL),
+                                static_cast<uint32_t>(left));
                 }
-        }
+    }
+    static __device__ __forceinline__ void commit()
+    {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // All but the last DEPTH - 1 committed steps have arrived.
+    static __device__ __forceinline__ void arrived()
+    {
+        asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    }
+    __device__ __forceinline__ void take(int slot, uint4 (&w)[CF][2][2]) const
+    {
+#pragma unroll
+        for (int c = 0; c < CF; ++c)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint4 &v = w[c][r][i];
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                 : "r"(base + static_cast<uint32_t>(
+                                                  (slot * PER + (c * 2 + r) * 2 + i) * 512))
+                                 : "memory");
+                }
+    }
+};
+
+// acc += weights * tokens over the step from k0 on: CF fragments of weights, the
+// groups of eight tokens that there are.  trow: token g of each group; lane t
+// takes k0 + N t + 4 N i + 0 .. N-1 of piece i.
+template <class T, bool I8, int CF, int NF, bool XV>
+__device__ __forceinline__ void multiply(float (&acc)[CF][NF][4], const uint4 (&w)[CF][2][2],
+                                         const char *const (&trow)[NF], int k0, int K, int t,
+                                         int tokens)
+{
+    using W = Weights<T, I8>;
+#pragma unroll
+    for (int n = 0; n < NF; ++n) {
+        if (n > 0 && 8 * n >= tokens) break;
+        uint4 x[2][W::TOK];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < W::TOK; ++j)
+                x[i][j] = load_token<XV>(trow[n], k0 + W::N * t + 4 * W::N * i + 8 * j, K);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < CF; ++c) {
+                uint32_t lo[W::N / 2], hi[W::N / 2];
+                W::pairs(w[c][0][i], lo);
+                W::pairs(w[c][1][i], hi);
+#pragma unroll
+                for (int j = 0; j < W::N / 4; ++j) {
+                    const uint4 &v = x[i][j / 2];
+                    mma<T>(acc[c][n], lo[2 * j], hi[2 * j], lo[2 * j + 1], hi[2 * j + 1],
+                           j % 2 ? v.z : v.x, j % 2 ? v.w : v.y);
+                }
+            }
+    }
 }
 
 // ---------------------------------------------------------------------- up
 
-// grid: 16 rows of G and U (x), the used expert (y).
+constexpr int kUpDepth = 2;
+template <class T, bool I8, int NF>
+constexpr int up_smem()
+{
+    constexpr int ring = kWarps * Pieces<T, I8, 2, kUpDepth>::BYTES;
+    constexpr int part = kWarps * 8 * NF * (2 * kCh + 4) * 4;
+    return ring > part ? ring : part;
+}
+
+// grid: 16 rows of G and U (x), the used expert (y).  The warps share the steps
+// of k; their sums meet in shared memory, in the warps' order.
 template <class T, bool I8, int NF, bool XV>
-__global__ void __launch_bounds__(kThreads, NF == 4 ? 2 : 3) up_kernel(const Args a)
+__global__ void __launch_bounds__(kThreads, NF <= 2 ? 3 : 2) up_kernel(const Args a)
 {
     constexpr int TK = 8 * NF;
     using W = Weights<T, I8>;
+    using P = Pieces<T, I8, 2, kUpDepth>;
     __shared__ Choices c;
-    __shared__ float part[kWarps][TK][2 * kCh + 4];
+    extern __shared__ __align__(16) unsigned char dyn[];  // the rings, then the sums
     dependent_wait();
     dependent_release();  // (after the wait: the next kernel reads ids and weights early)
     find_choices(a, c);
     const int u = blockIdx.y;
     if (u >= c.used) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int e = c.expert[u], f0 = blockIdx.x * kCh;
-    const char *wrow[2][2];
+    const int e = c.expert[u], f0 = blockIdx.x * kCh, r0 = c.first[u], n = c.first[u + 1] - r0;
+    const char *wrow[2][2], *trow[NF];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
             wrow[i][r] = static_cast<const char *>(a.W1) + e * a.stride1 +
                          (static_cast<long long>(i) * a.F + min(f0 + g + 8 * r, a.F - 1)) * a.p1;
-    for (int r0 = c.first[u]; r0 < c.first[u + 1]; r0 += TK) {
-        const int n = min(TK, c.first[u + 1] - r0);
-        const char *trow[NF];
 #pragma unroll
-        for (int i = 0; i < NF; ++i)
-            trow[i] = static_cast<const char *>(a.x) +
-                      c.token[r0 + min(8 * i + g, n - 1)] * a.ldx * static_cast<int>(sizeof(T));
-        float acc[2][NF][4] = {};
-        for (int k = warp * W::STEP; k < a.H; k += kWarps * W::STEP)
-            step<T, I8, 2, NF, XV>(acc, wrow, trow, k, a.H, t, n);
-        __syncthreads();  // the last turn's readers are done
+    for (int i = 0; i < NF; ++i)
+        trow[i] = static_cast<const char *>(a.x) +
+                  c.token[r0 + min(8 * i + g, n - 1)] * a.ldx * static_cast<int>(sizeof(T));
+    P ring(dyn, warp, lane);
+    const int k_step = kWarps * W::STEP;
+    int ask = warp * W::STEP;
+    for (int d = 0; d < kUpDepth; ++d, ask += k_step) {
+        if (ask < a.H) ring.ask(d, wrow, ask, a.H);
+        P::commit();
+    }
+    float acc[2][NF][4] = {};
+    int slot = 0;
+    for (int k = warp * W::STEP; k < a.H; k += k_step, ask += k_step) {
+        uint4 w[2][2][2];
+        P::arrived();
+        ring.take(slot, w);
+        if (ask < a.H) ring.ask(slot, wrow, ask, a.H);
+        P::commit();
+        multiply<T, I8, 2, NF, XV>(acc, w, trow, k, a.H, t, n);
+        slot = slot + 1 == kUpDepth ? 0 : slot + 1;
+    }
+    __syncthreads();  // every ring is read: the sums take its place
+    float(*part)[TK][2 * kCh + 4] = reinterpret_cast<float(*)[TK][2 * kCh + 4]>(dyn);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int m = 0; m < NF; ++m)
+        for (int m = 0; m < NF; ++m)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    part[warp][8 * m + 2 * t + (j & 1)][kCh * i + 8 * (j >> 1) + g] = acc[i][m][j];
-        __syncthreads();
-        for (int i = threadIdx.x; i < n * kCh; i += kThreads) {
-            const int m = i / kCh, f = i % kCh;
-            float gate = 0.f, up = 0.f;
-            if (f0 + f < a.F) {
+            for (int j = 0; j < 4; ++j)
+                part[warp][8 * m + 2 * t + (j & 1)][kCh * i + 8 * (j >> 1) + g] = acc[i][m][j];
+    __syncthreads();
+    for (int i = threadIdx.x; i < n * kCh; i += kThreads) {
+        const int m = i / kCh, f = i % kCh;
+        float gate = 0.f, up = 0.f;
+        if (f0 + f < a.F) {
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    gate += part[w][m][f];
-                    up += part[w][m][kCh + f];
-                }
-                if (I8) {
-                    const float *s = a.scale1 + static_cast<long long>(e) * 2 * a.F + f0 + f;
-                    gate *= s[0];
-                    up *= s[a.F];
-                }
+            for (int w = 0; w < kWarps; ++w) {
+                gate += part[w][m][f];
+                up += part[w][m][kCh + f];
             }
-            // (values past F are zeros: gate is)
-            static_cast<T *>(a.h)[c.choice[r0 + m] * a.ldh + f0 + f] =
-                rows::from_f<T>(gate / (1.f + expf(-gate)) * up);
+            if (I8) {
+                const float *s = a.scale1 + static_cast<long long>(e) * 2 * a.F + f0 + f;
+                gate *= s[0];
+                up *= s[a.F];
+            }
         }
+        // (values past F are zeros: gate is)
+        static_cast<T *>(a.h)[c.choice[r0 + m] * a.ldh + f0 + f] =
+            rows::from_f<T>(gate / (1.f + expf(-gate)) * up);
     }
 }
 
 // -------------------------------------------------------------------- down
+
+constexpr int kDownDepth = 6;
 
 // grid: 16 channels of out.  The steps of all used experts form one list, a
 // part of which is each warp's; a warp adds an expert's results, weighted, to
@@ -353,59 +420,83 @@ __global__ void __launch_bounds__(kThreads, NF == 4 ? 2 : 3) up_kernel(const Arg
 template <class T, bool I8, int NF>
 __global__ void __launch_bounds__(kThreads, 2) down_kernel(const Args a)
 {
-    constexpr int TK = 8 * NF;
     using W = Weights<T, I8>;
+    using P = Pieces<T, I8, 1, kDownDepth>;
     __shared__ Choices c;
-    extern __shared__ float sums[];  // [warp][token][channel], rows of kCh + 1
+    extern __shared__ __align__(16) unsigned char dyn[];  // the rings, [warp][token][channel] sums
+    float *sums = reinterpret_cast<float *>(dyn + kWarps * P::BYTES);  // rows of kCh + 1
     dependent_release();
     // The up kernel releases its dependents after its own wait, so what it found
-    // complete, ids and weights among it, is complete here too.  (F == 0: there is
-    // no up kernel.)
+    // complete, ids and weights among it, is complete here too, and is read while
+    // it still runs.  (F == 0: there is no up kernel.)
     if (a.F == 0) dependent_wait();
     find_choices(a, c);
-    dependent_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int h0 = blockIdx.x * kCh;
     float *mine = sums + static_cast<long long>(warp) * a.T * (kCh + 1);
     for (int i = lane; i < a.T * (kCh + 1); i += 32) mine[i] = 0.f;
-    __syncwarp();
     const int steps = (a.F + W::STEP - 1) / W::STEP, total = c.used * steps;
     int at = static_cast<int>(static_cast<long long>(total) * warp / kWarps);
     const int end = static_cast<int>(static_cast<long long>(total) * (warp + 1) / kWarps);
-    while (at < end) {
-        const int u = at / steps, lo = at - u * steps, hi = min(steps, lo + end - at);
-        const int e = c.expert[u];
-        const char *wrow[1][2];
+    P ring(dyn, warp, lane);
+    // the step asked for next: expert au, its rows, step as
+    int ask = at, au = steps > 0 ? at / steps : 0, as = at - au * steps;
+    const char *arow[1][2];
+    auto ask_rows = [&]() {
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-            wrow[0][r] = static_cast<const char *>(a.W2) + e * a.stride2 +
+            arow[0][r] = static_cast<const char *>(a.W2) + c.expert[au] * a.stride2 +
                          min(h0 + g + 8 * r, a.H - 1) * a.p2;
+    };
+    auto ask_next = [&](int slot) {
+        if (ask < end) {
+            ring.ask(slot, arow, as * W::STEP, a.F);
+            ++ask;
+            if (++as == steps) {
+                as = 0;
+                ++au;
+                if (ask < end) ask_rows();
+            }
+        }
+        P::commit();
+    };
+    if (ask < end) ask_rows();
+    for (int d = 0; d < kDownDepth; ++d) ask_next(d);
+    dependent_wait();  // h is complete
+    __syncwarp();
+    int slot = 0;
+    while (at < end) {
+        const int u = at / steps, lo = at - u * steps, hi = min(steps, lo + end - at);
+        const int e = c.expert[u], r0 = c.first[u], n = c.first[u + 1] - r0;
         float scale[2] = {1.f, 1.f};
         if (I8)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
                 scale[r] = a.scale2[static_cast<long long>(e) * a.H + min(h0 + g + 8 * r, a.H - 1)];
-        for (int r0 = c.first[u]; r0 < c.first[u + 1]; r0 += TK) {
-            const int n = min(TK, c.first[u + 1] - r0);
-            const char *trow[NF];
+        const char *trow[NF];
 #pragma unroll
-            for (int i = 0; i < NF; ++i)
-                trow[i] = static_cast<const char *>(a.h) +
-                          c.choice[r0 + min(8 * i + g, n - 1)] * a.ldh * static_cast<int>(sizeof(T));
-            float acc[1][NF][4] = {};
-            for (int s = lo; s < hi; ++s)
-                step<T, I8, 1, NF, true>(acc, wrow, trow, s * W::STEP, a.F, t, n);
-#pragma unroll
-            for (int m = 0; m < NF; ++m)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int col = 8 * m + 2 * t + (j & 1);
-                    if (col < n)
-                        mine[c.token[r0 + col] * (kCh + 1) + 8 * (j >> 1) + g] +=
-                            c.weight[r0 + col] * (scale[j >> 1] * acc[0][m][j]);
-                }
-            __syncwarp();
+        for (int i = 0; i < NF; ++i)
+            trow[i] = static_cast<const char *>(a.h) +
+                      c.choice[r0 + min(8 * i + g, n - 1)] * a.ldh * static_cast<int>(sizeof(T));
+        float acc[1][NF][4] = {};
+        for (int s = lo; s < hi; ++s) {
+            uint4 w[1][2][2];
+            P::arrived();
+            ring.take(slot, w);
+            ask_next(slot);
+            multiply<T, I8, 1, NF, true>(acc, w, trow, s * W::STEP, a.F, t, n);
+            slot = slot + 1 == kDownDepth ? 0 : slot + 1;
         }
+#pragma unroll
+        for (int m = 0; m < NF; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int col = 8 * m + 2 * t + (j & 1);
+                if (col < n)
+                    mine[c.token[r0 + col] * (kCh + 1) + 8 * (j >> 1) + g] +=
+                        c.weight[r0 + col] * (scale[j >> 1] * acc[0][m][j]);
+            }
+        __syncwarp();
         at += hi - lo;
     }
     __syncthreads();
@@ -424,18 +515,20 @@ int launch(const Args &a, bool x_vec, cudaStream_t st)
 {
     const int rows_ = a.T * a.k, most = a.E < rows_ ? a.E : rows_;
     const dim3 grid(static_cast<unsigned>((a.F + kCh - 1) / kCh), static_cast<unsigned>(most));
-    if (a.F > 0 && a.H > 0) {
-        const int s = launch_dependent(x_vec ? up_kernel<T, I8, NF, true> : up_kernel<T, I8, NF, false>,
-                                       grid, dim3(kThreads), 0, 1, st, a);
+    if (a.F > 0) {
+        auto kern = x_vec ? up_kernel<T, I8, NF, true> : up_kernel<T, I8, NF, false>;
+        constexpr int smem = up_smem<T, I8, NF>();
+        if (!smem_attr_once(reinterpret_cast<const void *>(kern), smem)) return SGEMM_ERR_LAUNCH;
+        const int s = launch_dependent(kern, grid, dim3(kThreads), smem, 1, st, a);
         if (s != SGEMM_OK) return s;
     }
-    const size_t smem = sizeof(float) * kWarps * a.T * (kCh + 1);
+    constexpr int ring = kWarps * Pieces<T, I8, 1, kDownDepth>::BYTES;
+    constexpr int per_token = static_cast<int>(sizeof(float)) * kWarps * (kCh + 1);
     auto kern = down_kernel<T, I8, NF>;
-    if (!smem_attr_once(reinterpret_cast<const void *>(kern),
-                        static_cast<int>(sizeof(float)) * kWarps * kMaxTokens * (kCh + 1)))
+    if (!smem_attr_once(reinterpret_cast<const void *>(kern), ring + per_token * 8 * NF))
         return SGEMM_ERR_LAUNCH;
     return launch_dependent(kern, dim3(static_cast<unsigned>((a.H + kCh - 1) / kCh)),
-                            dim3(kThreads), smem, 1, st, a);
+                            dim3(kThreads), static_cast<size_t>(ring + per_token * a.T), 1, st, a);
 }
 
 template <class T, bool I8>
@@ -443,7 +536,8 @@ int run(const Args &a, bool x_vec, cudaStream_t st)
 {
     if (a.T <= 8) return launch<T, I8, 1>(a, x_vec, st);
     if (a.T <= 16) return launch<T, I8, 2>(a, x_vec, st);
-    return launch<T, I8, 4>(a, x_vec, st);
+    if (a.T <= 32) return launch<T, I8, 4>(a, x_vec, st);
+    return launch<T, I8, 8>(a, x_vec, st);
 }
 
 bool sizes_ok(int T, int k, int H, int F)

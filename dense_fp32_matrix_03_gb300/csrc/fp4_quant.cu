@@ -12,7 +12,7 @@
 namespace sg {
 namespace fp4 {
 
-using rows::Vec;
+using rows::Words;
 
 constexpr int kHeld = 4;  // vectors per thread kept in registers
 
@@ -32,31 +32,28 @@ struct QuantArgs {
 // One vector of the values to quantise, in fp32 (past the row: zeros).
 template <class T, int VB, int LB, bool GATED>
 __device__ __forceinline__ void load_values(const QuantArgs &a, const char *row, unsigned v,
-                                            float (&f)[Vec<T, VB>::N])
+                                            float (&f)[Words<T, VB>::N])
 {
-    constexpr unsigned EV = Vec<T, VB>::N;
+    constexpr unsigned EV = Words<T, VB>::N;
     const unsigned left =
         min(static_cast<unsigned>(a.K) - v * EV, EV) * static_cast<unsigned>(sizeof(T));
-    Vec<T, VB> g;
-    g.template load_pieces<LB>(row + static_cast<long long>(v) * VB, left);
+    Words<T, VB> g;
+    g.template load<LB>(row + static_cast<long long>(v) * VB, left);
+    g.unpack(f);
     if constexpr (GATED) {
-        Vec<T, VB> u;
-        u.template load_pieces<LB>(row + a.up + static_cast<long long>(v) * VB, left);
+        Words<T, VB> u;
+        u.template load<LB>(row + a.up + static_cast<long long>(v) * VB, left);
+        float h[EV];
+        u.unpack(h);
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(EV); ++i) {
-            const float x = g.get(i);
-            f[i] = x / (1.f + expf(-x)) * u.get(i);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < static_cast<int>(EV); ++i) f[i] = g.get(i);
+        for (int i = 0; i < static_cast<int>(EV); ++i) f[i] = f[i] / (1.f + expf(-f[i])) * h[i];
     }
 }
 
 template <class T, int VB, int LB, bool GATED, int FORMAT>
 __global__ void __launch_bounds__(256, 4) quantize_kernel(const QuantArgs a)
 {
-    constexpr int EV = Vec<T, VB>::N;
+    constexpr int EV = Words<T, VB>::N;
     __shared__ unsigned part[8];
     dependent_release();
     dependent_wait();
@@ -116,7 +113,7 @@ struct QuantLaunch {
     {
         // at least four values a vector: narrower loads make one up
         constexpr int V4 = 4 * static_cast<int>(sizeof(T)), VB = LB > V4 ? LB : V4;
-        constexpr int EV = Vec<T, VB>::N;
+        constexpr int EV = Words<T, VB>::N;
         QuantArgs a = args;
         a.nvec = a.K > 0 ? (static_cast<unsigned>(a.K) - 1) / EV + 1 : 0;
         const int held = a.M <= num_sms ? 1 : kHeld;  // few rows: more threads on each

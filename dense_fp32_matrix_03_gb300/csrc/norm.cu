@@ -14,7 +14,7 @@
 namespace sg {
 namespace norm {
 
-using rows::Vec;
+using rows::Words;
 
 constexpr float kI8Tiny = 7.888609052210118e-31f;  // 2^-100
 constexpr float kRound = 12582912.f;               // 1.5 * 2^23
@@ -39,33 +39,38 @@ struct Args {
 template <class T, int VB>
 __device__ __forceinline__ unsigned bytes_left(int H, unsigned v)
 {
-    constexpr unsigned EV = Vec<T, VB>::N;
+    constexpr unsigned EV = Words<T, VB>::N;
     return min(static_cast<unsigned>(H) - v * EV, EV) * static_cast<unsigned>(sizeof(T));
 }
 
 template <class T, int VB, int LB>
-__device__ __forceinline__ void load_weight(const Args &a, unsigned v, Vec<T, VB> &w)
+__device__ __forceinline__ void load_weight(const Args &a, unsigned v, Words<T, VB> &w)
 {
     if (a.w != nullptr) {
-        w.template load_pieces<LB>(a.w + static_cast<long long>(v) * VB,
-                                   bytes_left<T, VB>(a.H, v));
+        w.template load<LB>(a.w + static_cast<long long>(v) * VB, bytes_left<T, VB>(a.H, v));
     } else {
+        float one[Words<T, VB>::N];
 #pragma unroll
-        for (int i = 0; i < Vec<T, VB>::N; ++i) w.set(i, 1.f);
+        for (int i = 0; i < Words<T, VB>::N; ++i) one[i] = 1.f;
+        w.pack(one);
     }
 }
 // x + res as the row type keeps it.
 template <class T, int VB>
-__device__ __forceinline__ void add(Vec<T, VB> &x, const Vec<T, VB> &r)
+__device__ __forceinline__ void add(Words<T, VB> &x, const Words<T, VB> &r)
 {
+    float f[Words<T, VB>::N], g[Words<T, VB>::N];
+    x.unpack(f);
+    r.unpack(g);
 #pragma unroll
-    for (int i = 0; i < Vec<T, VB>::N; ++i) x.set(i, x.get(i) + r.get(i));
+    for (int i = 0; i < Words<T, VB>::N; ++i) f[i] += g[i];
+    x.pack(f);
 }
 
 template <class T, int VB, int LB, int OUT>
 __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
 {
-    constexpr int EV = Vec<T, VB>::N;
+    constexpr int EV = Words<T, VB>::N;
     __shared__ float part_sum[8];
     __shared__ unsigned part_max[8];
     dependent_release();
@@ -78,9 +83,9 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
     const unsigned tx = threadIdx.x, nx = blockDim.x, warps = nx >> 5;
     const unsigned nvec = live ? a.nvec : 0;
 
-    Vec<T, VB> s[kHeld], w[kHeld];
+    Words<T, VB> s[kHeld], w[kHeld];
     {
-        Vec<T, VB> t[kHeld];
+        Words<T, VB> t[kHeld];
 #pragma unroll
         for (int h = 0; h < kHeld; ++h) {
             const unsigned v = tx + h * nx;
@@ -90,8 +95,8 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
             if (v < nvec) {
                 const long long at = static_cast<long long>(v) * VB;
                 const unsigned left = bytes_left<T, VB>(a.H, v);
-                s[h].template load_pieces<LB>(x + at, left);
-                if (a.res != nullptr) t[h].template load_pieces<LB>(res + at, left);
+                s[h].template load<LB>(x + at, left);
+                if (a.res != nullptr) t[h].template load<LB>(res + at, left);
                 load_weight<T, VB, LB>(a, v, w[h]);
             }
         }
@@ -101,12 +106,14 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
     }
     float square = 0.f;
     unsigned big = 0;
-    auto gather = [&](const Vec<T, VB> &sv, const Vec<T, VB> &wv) {
+    auto gather = [&](const Words<T, VB> &sv, const Words<T, VB> &wv) {
+        float f[EV], g[EV];
+        sv.unpack(f);
+        if (OUT != kRow) wv.unpack(g);
 #pragma unroll
         for (int i = 0; i < EV; ++i) {
-            const float f = sv.get(i);
-            square = fmaf(f, f, square);
-            if (OUT != kRow) big = max(big, __float_as_uint(f * wv.get(i)) & 0x7FFFFFFFu);
+            square = fmaf(f[i], f[i], square);
+            if (OUT != kRow) big = max(big, __float_as_uint(f[i] * g[i]) & 0x7FFFFFFFu);
         }
     };
 #pragma unroll
@@ -115,33 +122,33 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
         if (v < nvec) {
             gather(s[h], w[h]);
             if (a.sum != nullptr)
-                s[h].template store_pieces<LB>(sum + static_cast<long long>(v) * VB,
+                s[h].template store<LB>(sum + static_cast<long long>(v) * VB,
                                                bytes_left<T, VB>(a.H, v));
         }
     }
     // a vector of a long row's tail; again: in the second pass, when the sum, if
     // it is kept, may have taken the place of x or res
-    auto tail = [&](unsigned v, bool again, Vec<T, VB> &sv, Vec<T, VB> &wv) {
+    auto tail = [&](unsigned v, bool again, Words<T, VB> &sv, Words<T, VB> &wv) {
         const long long at = static_cast<long long>(v) * VB;
         const unsigned left = bytes_left<T, VB>(a.H, v);
         load_weight<T, VB, LB>(a, v, wv);
         if (again && a.sum != nullptr) {
-            sv.template load_pieces<LB>(sum + at, left);
+            sv.template load<LB>(sum + at, left);
             return;
         }
-        sv.template load_pieces<LB>(x + at, left);
+        sv.template load<LB>(x + at, left);
         if (a.res != nullptr) {
-            Vec<T, VB> t;
-            t.template load_pieces<LB>(res + at, left);
+            Words<T, VB> t;
+            t.template load<LB>(res + at, left);
             add(sv, t);
         }
     };
     for (unsigned v = tx + kHeld * nx; v < nvec; v += nx) {
-        Vec<T, VB> sv, wv;
+        Words<T, VB> sv, wv;
         tail(v, false, sv, wv);
         gather(sv, wv);
         if (a.sum != nullptr)
-            sv.template store_pieces<LB>(sum + static_cast<long long>(v) * VB,
+            sv.template store<LB>(sum + static_cast<long long>(v) * VB,
                                          bytes_left<T, VB>(a.H, v));
     }
 #pragma unroll
@@ -165,18 +172,22 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
 
     if constexpr (OUT == kRow) {
         char *y = a.y + r * a.py;
-        auto put = [&](unsigned v, const Vec<T, VB> &sv, const Vec<T, VB> &wv) {
-            Vec<T, VB> o;
+        auto put = [&](unsigned v, const Words<T, VB> &sv, const Words<T, VB> &wv) {
+            float f[EV], g[EV];
+            sv.unpack(f);
+            wv.unpack(g);
 #pragma unroll
-            for (int i = 0; i < EV; ++i) o.set(i, sv.get(i) * rho * wv.get(i));
-            o.template store_pieces<LB>(y + static_cast<long long>(v) * VB,
+            for (int i = 0; i < EV; ++i) f[i] = f[i] * rho * g[i];
+            Words<T, VB> o;
+            o.pack(f);
+            o.template store<LB>(y + static_cast<long long>(v) * VB,
                                         bytes_left<T, VB>(a.H, v));
         };
 #pragma unroll
         for (int h = 0; h < kHeld; ++h)
             if (tx + h * nx < nvec) put(tx + h * nx, s[h], w[h]);
         for (unsigned v = tx + kHeld * nx; v < nvec; v += nx) {
-            Vec<T, VB> sv, wv;
+            Words<T, VB> sv, wv;
             tail(v, true, sv, wv);
             put(v, sv, wv);
         }
@@ -185,15 +196,16 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
         const bool finite = big < 0x7F800000u, some = finite && amax >= kI8Tiny;
         const float inv = some ? __fdiv_rn(127.f, amax) : 0.f;
         unsigned char *q = a.q + r * a.pq;
-        auto put = [&](unsigned v, const Vec<T, VB> &sv, const Vec<T, VB> &wv) {
+        auto put = [&](unsigned v, const Words<T, VB> &sv, const Words<T, VB> &wv) {
             // (the nearest integer, ties to even, is in the low byte after 1.5 * 2^23
             // is added)
+            float f[EV], g[EV];
+            sv.unpack(f);
+            wv.unpack(g);
             uint32_t c[EV];
 #pragma unroll
             for (int i = 0; i < EV; ++i)
-                c[i] = some ? __float_as_uint(
-                                  __fadd_rn(__fmul_rn(sv.get(i) * wv.get(i), inv), kRound))
-                            : 0u;
+                c[i] = some ? __float_as_uint(__fadd_rn(__fmul_rn(f[i] * g[i], inv), kRound)) : 0u;
             const unsigned n = bytes_left<T, VB>(a.H, v) / static_cast<unsigned>(sizeof(T));
             if (n == EV && a.sf_tiles != 0) {  // (8 bits: codes on boundaries of a vector's)
 #pragma unroll
@@ -215,7 +227,7 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
         for (int h = 0; h < kHeld; ++h)
             if (tx + h * nx < nvec) put(tx + h * nx, s[h], w[h]);
         for (unsigned v = tx + kHeld * nx; v < nvec; v += nx) {
-            Vec<T, VB> sv, wv;
+            Words<T, VB> sv, wv;
             tail(v, true, sv, wv);
             put(v, sv, wv);
         }
@@ -226,10 +238,12 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
         constexpr int FORMAT = OUT == kFp4Mx ? SGEMM_FP4_MX : SGEMM_FP4_NV;
         const fp4::RowScale rs = fp4::row_scale(FORMAT, big);
         unsigned char *q = a.q + r * a.pq, *sf = a.sf + fp4::scale_row(r, a.sf_tiles);
-        auto put = [&](unsigned v, const Vec<T, VB> &sv, const Vec<T, VB> &wv) {
-            float f[EV];
+        auto put = [&](unsigned v, const Words<T, VB> &sv, const Words<T, VB> &wv) {
+            float f[EV], g[EV];
+            sv.unpack(f);
+            wv.unpack(g);
 #pragma unroll
-            for (int i = 0; i < EV; ++i) f[i] = sv.get(i) * wv.get(i);
+            for (int i = 0; i < EV; ++i) f[i] *= g[i];
             fp4::store_vectors<FORMAT>(f, v, nvec, rs, q, sf);
         };
         // (every lane of a warp that has a vector: blocks span lanes)
@@ -238,7 +252,7 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
         for (int h = 0; h < kHeld; ++h)
             if (w0 + h * nx < nvec) put(tx + h * nx, s[h], w[h]);
         for (unsigned v = tx + kHeld * nx; (v & ~31u) < nvec; v += nx) {
-            Vec<T, VB> sv, wv;
+            Words<T, VB> sv, wv;
             sv.zero();
             wv.zero();
             if (v < nvec) tail(v, true, sv, wv);
@@ -257,7 +271,7 @@ struct Launch {
     {
         // at least four values a vector: narrower loads make one up
         constexpr int V4 = 4 * static_cast<int>(sizeof(T)), VB = LB > V4 ? LB : V4;
-        constexpr int EV = Vec<T, VB>::N;
+        constexpr int EV = Words<T, VB>::N;
         Args a = args;
         a.nvec = a.H > 0 ? (static_cast<unsigned>(a.H) - 1) / EV + 1 : 0;
         if (OUT == kI8) a.sf_tiles = rows::aligned_to(a.q, EV) && a.pq % EV == 0;
@@ -282,7 +296,11 @@ struct Launch {
 // A block takes every gridDim.x-th group of rows; a thread keeps its columns'
 // sums for dweight in registers over all of them, and the block writes one
 // partial row, which the second kernel adds in the blocks' order.  (Columns
-// past the registers' are added up in the partial row itself.)
+// past the registers' are added up in the partial row itself.)  With two vectors a
+// thread, the next rows are on their way while these are reduced: two blocks of
+// 256 threads a multiprocessor, 8192 x 4096 bf16 50.9 us (5.3 TB/s; without the rows
+// ahead 64, on three blocks, whose registers spill, 77, with one vector on 512
+// threads 72).
 
 constexpr int kGradRows = 608;  // partial rows, at most
 
@@ -296,76 +314,94 @@ struct GradArgs {
     float *part;  // null: dweight is not wanted
 };
 
-template <class T, int VB, int LB>
+// HELD: vectors of a row that a thread keeps.
+template <class T, int VB, int LB, int HELD>
 __global__ void __launch_bounds__(256, 2) grad_kernel(const GradArgs a)
 {
-    constexpr int EV = Vec<T, VB>::N;
+    constexpr int EV = Words<T, VB>::N;
     __shared__ float2 part[2][8];
-    extern __shared__ float columns[];  // ty > 1: a group's columns
+    extern __shared__ float columns[];  // half the groups' columns
     dependent_release();
     dependent_wait();
-    const unsigned tx = threadIdx.x, nx = blockDim.x, warps = nx >> 5;
+    const unsigned tx = threadIdx.x, nx = blockDim.x, ny = blockDim.y, warps = nx >> 5;
     const unsigned first = threadIdx.y * warps;
-    float acc[kHeld][EV];
-    Vec<T, VB> w[kHeld];
-    auto weight = [&](unsigned v, Vec<T, VB> &wv) {
+    float acc[HELD][EV];
+    Words<T, VB> w[HELD];
+    auto weight = [&](unsigned v, Words<T, VB> &wv) {
         if (a.w != nullptr) {
-            wv.template load_pieces<LB>(a.w + static_cast<long long>(v) * VB,
-                                        bytes_left<T, VB>(a.H, v));
+            wv.template load<LB>(a.w + static_cast<long long>(v) * VB, bytes_left<T, VB>(a.H, v));
         } else {
+            float one[EV];
 #pragma unroll
-            for (int i = 0; i < EV; ++i) wv.set(i, 1.f);
+            for (int i = 0; i < EV; ++i) one[i] = 1.f;
+            wv.pack(one);
         }
     };
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h) {
+    for (int h = 0; h < HELD; ++h) {
         w[h].zero();
         if (tx + h * nx < a.nvec) weight(tx + h * nx, w[h]);
 #pragma unroll
         for (int i = 0; i < EV; ++i) acc[h][i] = 0.f;
     }
     float *mine = a.part + static_cast<long long>(blockIdx.x) * a.H;
-    const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+    const long long step = static_cast<long long>(gridDim.x) * ny;
     const long long turns = (a.M + step - 1) / step;
+    auto row_of = [&](long long turn) { return (turn * gridDim.x + blockIdx.x) * ny + threadIdx.y; };
+    Words<T, VB> sv[HELD], gv[HELD], dv[HELD];
+    // this thread's vectors of row r (zeros past the last row)
+    auto load = [&](long long r, Words<T, VB> (&x)[HELD], Words<T, VB> (&g)[HELD],
+                    Words<T, VB> (&d)[HELD]) {
+#pragma unroll
+        for (int h = 0; h < HELD; ++h) {
+            const unsigned v = tx + h * nx;
+            x[h].zero();
+            g[h].zero();
+            d[h].zero();
+            if (r < a.M && v < a.nvec) {
+                const long long at = static_cast<long long>(v) * VB;
+                const unsigned left = bytes_left<T, VB>(a.H, v);
+                x[h].template load<LB>(a.s + r * a.ps + at, left);
+                g[h].template load<LB>(a.dy + r * a.pdy + at, left);
+                if (a.ds != nullptr) d[h].template load<LB>(a.ds + r * a.pds + at, left);
+            }
+        }
+    };
+    constexpr bool AHEAD = HELD <= 2;
+    if (AHEAD) load(row_of(0), sv, gv, dv);
     int buf = 0;
     for (long long turn = 0; turn < turns; ++turn, buf ^= 1) {
-        const long long r = (turn * gridDim.x + blockIdx.x) * blockDim.y + threadIdx.y;
+        const long long r = row_of(turn);
         const bool live = r < a.M;
         const long long row = live ? r : 0;
         const unsigned nvec = live ? a.nvec : 0;
         const char *s = a.s + row * a.ps, *dy = a.dy + row * a.pdy, *ds = a.ds + row * a.pds;
         char *dx = a.dx + row * a.pdx;
-        Vec<T, VB> sv[kHeld], gv[kHeld], dv[kHeld];
-#pragma unroll
-        for (int h = 0; h < kHeld; ++h) {
-            const unsigned v = tx + h * nx;
-            sv[h].zero();
-            gv[h].zero();
-            dv[h].zero();
-            if (v < nvec) {
-                const long long at = static_cast<long long>(v) * VB;
-                const unsigned left = bytes_left<T, VB>(a.H, v);
-                sv[h].template load_pieces<LB>(s + at, left);
-                gv[h].template load_pieces<LB>(dy + at, left);
-                if (a.ds != nullptr) dv[h].template load_pieces<LB>(ds + at, left);
-            }
-        }
+        Words<T, VB> ns[HELD], ng[HELD], nd[HELD];
+        if (AHEAD)
+            load(turn + 1 < turns ? row_of(turn + 1) : a.M, ns, ng, nd);
+        else
+            load(r, sv, gv, dv);
         float square = 0.f, inner = 0.f;
-        auto gather = [&](const Vec<T, VB> &x, const Vec<T, VB> &g, const Vec<T, VB> &wv) {
+        auto gather = [&](const Words<T, VB> &x, const Words<T, VB> &g, const Words<T, VB> &wv) {
+            float fx[EV], fg[EV], fw[EV];
+            x.unpack(fx);
+            g.unpack(fg);
+            wv.unpack(fw);
 #pragma unroll
             for (int i = 0; i < EV; ++i) {
-                square = fmaf(x.get(i), x.get(i), square);
-                inner = fmaf(wv.get(i) * g.get(i), x.get(i), inner);
+                square = fmaf(fx[i], fx[i], square);
+                inner = fmaf(fw[i] * fg[i], fx[i], inner);
             }
         };
 #pragma unroll
-        for (int h = 0; h < kHeld; ++h) gather(sv[h], gv[h], w[h]);
-        for (unsigned v = tx + kHeld * nx; v < nvec; v += nx) {
+        for (int h = 0; h < HELD; ++h) gather(sv[h], gv[h], w[h]);
+        for (unsigned v = tx + HELD * nx; v < nvec; v += nx) {
             const long long at = static_cast<long long>(v) * VB;
             const unsigned left = bytes_left<T, VB>(a.H, v);
-            Vec<T, VB> x, g, wv;
-            x.template load_pieces<LB>(s + at, left);
-            g.template load_pieces<LB>(dy + at, left);
+            Words<T, VB> x, g, wv;
+            x.template load<LB>(s + at, left);
+            g.template load<LB>(dy + at, left);
             weight(v, wv);
             gather(x, g, wv);
         }
@@ -378,72 +414,101 @@ __global__ void __launch_bounds__(256, 2) grad_kernel(const GradArgs a)
             // (two buffers: a thread still reads one while the next turn fills the other)
             if ((tx & 31) == 0) part[buf][first + (tx >> 5)] = make_float2(square, inner);
             __syncthreads();
-            square = inner = 0.f;
-            for (unsigned i = 0; i < warps; ++i) {
-                square += part[buf][first + i].x;
-                inner += part[buf][first + i].y;
+            // (a warp's lanes take the warps' sums: eight of them at most)
+            float2 p = make_float2(0.f, 0.f);
+            if ((tx & 31) < warps) p = part[buf][first + (tx & 31)];
+#pragma unroll
+            for (int d = 4; d > 0; d /= 2) {
+                p.x += __shfl_xor_sync(0xffffffffu, p.x, d);
+                p.y += __shfl_xor_sync(0xffffffffu, p.y, d);
             }
+            square = __shfl_sync(0xffffffffu, p.x, 0);
+            inner = __shfl_sync(0xffffffffu, p.y, 0);
         }
         const float n = static_cast<float>(a.H);
         const float rho = rsqrtf(__fdiv_rn(square, n) + a.eps);
         const float c = rho * rho * __fdiv_rn(inner, n);
-        auto put = [&](unsigned v, const Vec<T, VB> &x, const Vec<T, VB> &g, const Vec<T, VB> &wv,
-                       const Vec<T, VB> &d) {
-            Vec<T, VB> o;
+        auto put = [&](unsigned v, const Words<T, VB> &x, const Words<T, VB> &g, const Words<T, VB> &wv,
+                       const Words<T, VB> &d, float (&dyx)[EV]) {
+            float fx[EV], fg[EV], f[EV], fd[EV];
+            x.unpack(fx);
+            g.unpack(fg);
+            wv.unpack(f);
+            d.unpack(fd);
 #pragma unroll
-            for (int i = 0; i < EV; ++i)
-                o.set(i, fmaf(rho, wv.get(i) * g.get(i) - x.get(i) * c, d.get(i)));
-            o.template store_pieces<LB>(dx + static_cast<long long>(v) * VB,
+            for (int i = 0; i < EV; ++i) {
+                f[i] = fmaf(rho, f[i] * fg[i] - fx[i] * c, fd[i]);
+                dyx[i] = fg[i] * fx[i];
+            }
+            Words<T, VB> o;
+            o.pack(f);
+            o.template store<LB>(dx + static_cast<long long>(v) * VB,
                                         bytes_left<T, VB>(a.H, v));
         };
 #pragma unroll
-        for (int h = 0; h < kHeld; ++h)
-            if (tx + h * nx < nvec) {
-                put(tx + h * nx, sv[h], gv[h], w[h], dv[h]);
+        for (int h = 0; h < HELD; ++h) {
+            sv[h].forget();
+            gv[h].forget();
+            w[h].forget();
+        }
 #pragma unroll
-                for (int i = 0; i < EV; ++i)
-                    acc[h][i] = fmaf(gv[h].get(i) * sv[h].get(i), rho, acc[h][i]);
+        for (int h = 0; h < HELD; ++h)
+            if (tx + h * nx < nvec) {
+                float dyx[EV];
+                put(tx + h * nx, sv[h], gv[h], w[h], dv[h], dyx);
+#pragma unroll
+                for (int i = 0; i < EV; ++i) acc[h][i] = fmaf(dyx[i], rho, acc[h][i]);
             }
-        for (unsigned v = tx + kHeld * nx; v < nvec; v += nx) {
+        for (unsigned v = tx + HELD * nx; v < nvec; v += nx) {
             const long long at = static_cast<long long>(v) * VB;
             const unsigned left = bytes_left<T, VB>(a.H, v);
-            Vec<T, VB> x, g, wv, d;
-            x.template load_pieces<LB>(s + at, left);
-            g.template load_pieces<LB>(dy + at, left);
+            Words<T, VB> x, g, wv, d;
+            x.template load<LB>(s + at, left);
+            g.template load<LB>(dy + at, left);
             d.zero();
-            if (a.ds != nullptr) d.template load_pieces<LB>(ds + at, left);
+            if (a.ds != nullptr) d.template load<LB>(ds + at, left);
             weight(v, wv);
-            put(v, x, g, wv, d);
-            if (a.part != nullptr) {  // (a row of its own: ty == 1 here)
+            float dyx[EV];
+            put(v, x, g, wv, d, dyx);
+            if (a.part != nullptr) {  // (a row of its own: one group here)
                 const unsigned e = left / static_cast<unsigned>(sizeof(T));
                 float *to = mine + static_cast<long long>(v) * EV;
 #pragma unroll
                 for (int i = 0; i < EV; ++i)
                     if (static_cast<unsigned>(i) < e)
-                        to[i] = fmaf(g.get(i) * x.get(i), rho, turn > 0 ? to[i] : 0.f);
+                        to[i] = fmaf(dyx[i], rho, turn > 0 ? to[i] : 0.f);
             }
         }
+        if (AHEAD)
+#pragma unroll
+            for (int h = 0; h < HELD; ++h) {
+                sv[h] = ns[h];
+                gv[h] = ng[h];
+                dv[h] = nd[h];
+            }
     }
     if (a.part == nullptr) return;
-    // the groups' sums, added in their order, to the block's partial row
-    const unsigned ny = blockDim.y;
-    for (unsigned y = 1; y < ny; ++y) {
-        if (threadIdx.y == y)
+    // the groups' sums, the upper half added to the lower until one is left, to the
+    // block's partial row
+    for (unsigned half = ny / 2; half > 0; half /= 2) {
+        if (threadIdx.y >= half && threadIdx.y < 2 * half)
 #pragma unroll
-            for (int h = 0; h < kHeld; ++h)
+            for (int h = 0; h < HELD; ++h)
 #pragma unroll
-                for (int i = 0; i < EV; ++i) columns[(h * EV + i) * nx + tx] = acc[h][i];
+                for (int i = 0; i < EV; ++i)
+                    columns[((threadIdx.y - half) * HELD * EV + h * EV + i) * nx + tx] = acc[h][i];
         __syncthreads();
-        if (threadIdx.y == 0)
+        if (threadIdx.y < half)
 #pragma unroll
-            for (int h = 0; h < kHeld; ++h)
+            for (int h = 0; h < HELD; ++h)
 #pragma unroll
-                for (int i = 0; i < EV; ++i) acc[h][i] += columns[(h * EV + i) * nx + tx];
+                for (int i = 0; i < EV; ++i)
+                    acc[h][i] += columns[(threadIdx.y * HELD * EV + h * EV + i) * nx + tx];
         __syncthreads();
     }
     if (threadIdx.y == 0)
 #pragma unroll
-        for (int h = 0; h < kHeld; ++h) {
+        for (int h = 0; h < HELD; ++h) {
             const unsigned v = tx + h * nx;
 #pragma unroll
             for (int i = 0; i < EV; ++i)
@@ -483,24 +548,31 @@ struct GradLaunch {
     int num_sms;
     float *dweight;
     cudaStream_t st;
+    // The kernel for a.nvec vectors a row; parts: its blocks.
+    template <class T, int VB, int LB, int HELD>
+    int rows_pass(const GradArgs &a, int &parts) const
+    {
+        constexpr int EV = Words<T, VB>::N;
+        const int tx = rows::pow2_threads((a.nvec + HELD - 1) / HELD, 32, 256), ty = 256 / tx;
+        const long long groups = (static_cast<long long>(a.M) + ty - 1) / ty;
+        parts = static_cast<int>(groups < 2LL * num_sms ? groups : 2LL * num_sms);
+        if (parts > partial_rows(a.M)) parts = partial_rows(a.M);
+        const dim3 block(static_cast<unsigned>(tx), static_cast<unsigned>(ty));
+        const size_t smem = sizeof(float) * HELD * EV * tx * (ty / 2);
+        return launch_dependent(grad_kernel<T, VB, LB, HELD>,
+                                dim3(static_cast<unsigned>(parts)), block, smem, 1, st, a);
+    }
     template <class T, int LB>
     int run() const
     {
         constexpr int V4 = 4 * static_cast<int>(sizeof(T)), VB = LB > V4 ? LB : V4;
-        constexpr int EV = Vec<T, VB>::N;
+        constexpr int EV = Words<T, VB>::N;
         GradArgs a = args;
         a.nvec = (static_cast<unsigned>(a.H) - 1) / EV + 1;
         int parts = 0;
         if (a.M > 0) {
-            const int tx = rows::pow2_threads((a.nvec + kHeld - 1) / kHeld, 32, 256), ty = 256 / tx;
-            const long long groups = (static_cast<long long>(a.M) + ty - 1) / ty;
-            parts = static_cast<int>(groups < 2LL * num_sms ? groups : 2LL * num_sms);
-            if (parts > partial_rows(a.M)) parts = partial_rows(a.M);
-            const dim3 block(static_cast<unsigned>(tx), static_cast<unsigned>(ty));
-            const size_t smem = ty > 1 ? sizeof(float) * kHeld * EV * tx : 0;
-            const int st_ = launch_dependent(grad_kernel<T, VB, LB>,
-                                             dim3(static_cast<unsigned>(parts)), block, smem, 1,
-                                             st, a);
+            const int st_ = a.nvec <= 512 ? rows_pass<T, VB, LB, 2>(a, parts)
+                                          : rows_pass<T, VB, LB, 4>(a, parts);
             if (st_ != SGEMM_OK) return st_;
         }
         if (dweight == nullptr) return SGEMM_OK;

@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -116,23 +117,119 @@ struct Vec {
     {
         *static_cast<typename Raw<VB>::T *>(p) = raw;
     }
-    // In pieces of LB bytes, the first `bytes` of them (a multiple of LB).
-    template <int LB>
-    __device__ __forceinline__ void store_pieces(char *p, unsigned bytes) const
-    {
-        if constexpr (LB == VB) {
-            store(p);
-        } else {
-            using P = typename Raw<LB>::T;
-#pragma unroll
-            for (int i = 0; i < VB / LB; ++i)
-                if (static_cast<unsigned>(i * LB) < bytes)
-                    *reinterpret_cast<P *>(p + i * LB) = reinterpret_cast<const P *>(&raw)[i];
-        }
-    }
     __device__ __forceinline__ void zero() { raw = typename Raw<VB>::T{}; }
     __device__ __forceinline__ float get(int i) const { return to_f<T>(v[i]); }
     __device__ __forceinline__ void set(int i, float x) { v[i] = from_f<T>(x); }
+};
+
+// A vector of VB bytes (8 or 16) as 32-bit words that are unpacked to fp32 and
+// packed from it as a whole: values taken one by one out of a Vec of 16-bit
+// values that lives in registers for long cost some five times the instructions.
+template <class T, int VB>
+struct Words {
+    static constexpr int N = VB / static_cast<int>(sizeof(T));
+    uint32_t w[VB / 4];
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < VB / 4; ++i) w[i] = 0u;
+    }
+    // In pieces of LB bytes, the first `bytes` of them (a multiple of LB; all of
+    // them where LB is VB); zeros for the rest.
+    template <int LB>
+    __device__ __forceinline__ void load(const char *p, unsigned bytes)
+    {
+        if constexpr (LB == 16) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            w[0] = v.x;
+            w[1] = v.y;
+            w[2] = v.z;
+            w[3] = v.w;
+        } else if constexpr (LB == 8) {
+#pragma unroll
+            for (int i = 0; i < VB / 8; ++i) {
+                uint2 v = make_uint2(0u, 0u);
+                if (VB == 8 || 8u * i < bytes) v = *reinterpret_cast<const uint2 *>(p + 8 * i);
+                w[2 * i] = v.x;
+                w[2 * i + 1] = v.y;
+            }
+        } else if constexpr (LB == 4) {
+#pragma unroll
+            for (int i = 0; i < VB / 4; ++i)
+                w[i] = 4u * i < bytes ? *reinterpret_cast<const uint32_t *>(p + 4 * i) : 0u;
+        } else {
+#pragma unroll
+            for (int i = 0; i < VB / 4; ++i) {
+                const uint32_t lo =
+                    4u * i < bytes ? *reinterpret_cast<const uint16_t *>(p + 4 * i) : 0u;
+                const uint32_t hi =
+                    4u * i + 2u < bytes ? *reinterpret_cast<const uint16_t *>(p + 4 * i + 2) : 0u;
+                w[i] = lo | hi << 16;
+            }
+        }
+    }
+    template <int LB>
+    __device__ __forceinline__ void store(char *p, unsigned bytes) const
+    {
+        if constexpr (LB == 16) {
+            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if constexpr (LB == 8) {
+#pragma unroll
+            for (int i = 0; i < VB / 8; ++i)
+                if (VB == 8 || 8u * i < bytes)
+                    *reinterpret_cast<uint2 *>(p + 8 * i) = make_uint2(w[2 * i], w[2 * i + 1]);
+        } else if constexpr (LB == 4) {
+#pragma unroll
+            for (int i = 0; i < VB / 4; ++i)
+                if (4u * i < bytes) *reinterpret_cast<uint32_t *>(p + 4 * i) = w[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < VB / 4; ++i) {
+                if (4u * i < bytes)
+                    *reinterpret_cast<uint16_t *>(p + 4 * i) = static_cast<uint16_t>(w[i]);
+                if (4u * i + 2u < bytes)
+                    *reinterpret_cast<uint16_t *>(p + 4 * i + 2) = static_cast<uint16_t>(w[i] >> 16);
+            }
+        }
+    }
+    // From here on unpacked anew: keeps the compiler from holding the values as
+    // floats, twice the registers, over a wait.
+    __device__ __forceinline__ void forget()
+    {
+#pragma unroll
+        for (int i = 0; i < VB / 4; ++i) asm volatile("" : "+r"(w[i]));
+    }
+    __device__ __forceinline__ void unpack(float (&f)[N]) const
+    {
+#pragma unroll
+        for (int i = 0; i < VB / 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                f[i] = __uint_as_float(w[i]);
+            } else if constexpr (std::is_same<T, __half>::value) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                f[2 * i] = v.x;
+                f[2 * i + 1] = v.y;
+            } else {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        }
+    }
+    __device__ __forceinline__ void pack(const float (&f)[N])
+    {
+#pragma unroll
+        for (int i = 0; i < VB / 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                w[i] = __float_as_uint(f[i]);
+            } else if constexpr (std::is_same<T, __half>::value) {
+                const __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&v);
+            } else {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&v);
+            }
+        }
+    }
 };
 
 // Vectors of VB bytes that a thread moves at a time: up to 16 bytes, at most
