@@ -1,7 +1,7 @@
 // expert_few.cu -- a whole expert layer for a few tokens in two kernels
 // (include/expert_layer.h):
-//   up    h[t,j] = silu(x G_e^T) * (x U_e^T), a block for each chosen expert
-//         and 16 of its rows of G and of U
+//   up    h[t,j] = silu(x G_e^T) * (x U_e^T), in units of a chosen expert and 16
+//         of its rows of G and of U
 //   down  out[t] = sum_e w D_e h[t,e], a block for 16 channels of out and ALL
 //         chosen experts, so that nothing is added across blocks
 // Both find the chosen experts and their tokens from the ids themselves (at
@@ -30,7 +30,6 @@ namespace few {
 constexpr int kMaxRows = 512;   // T * k
 constexpr int kMaxTokens = 64;  // T
 constexpr int kMaxSide = 65536; // H, F
-constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kCh = 16;         // channels of a fragment
 
 struct Args {
@@ -54,88 +53,97 @@ struct Args {
 struct Choices {
     int ids[kMaxRows];
     float w[kMaxRows];
-    short first[kMaxRows + 1];    // first row of used expert u
-    short expert[kMaxRows];       // its id
-    short token[kMaxRows];        // of a row
-    short choice[kMaxRows];       // t * k + the first j
+    unsigned map[kMaxExperts / 32];  // chosen experts
+    short first[kMaxRows + 1];       // first row of used expert u
+    short expert[kMaxRows];          // its id
+    short token[kMaxRows];           // of a row
+    short choice[kMaxRows];          // t * k + the first j
     float weight[kMaxRows];
     int used;
 };
 
-// Fills `c` (all threads of the block call).  The loads pass L1 by: the down
-// kernel is here while the up kernel still runs.
+// Fills `c` (all threads of the block call; WARPS: of them).  The loads pass L1
+// by: the down kernel is here while the up kernel still runs.
+template <int WARPS>
 __device__ __forceinline__ void find_choices(const Args &a, Choices &c)
 {
-    const int S = a.T * a.k, tid = threadIdx.x;
-    for (int s = tid; s < S; s += kThreads) {
+    const int S = a.T * a.k, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid < kMaxExperts / 32) c.map[tid] = 0u;
+    __syncthreads();
+    for (int s = tid; s < S; s += WARPS * 32) {
         const int e = __ldcg(a.ids + s);
-        c.ids[s] = e >= 0 && e < a.E ? e : -1;
+        const bool kept = e >= 0 && e < a.E;
+        c.ids[s] = kept ? e : -1;
         c.w[s] = a.weights != nullptr ? __ldcg(a.weights + s) : 1.f;
+        if (kept) atomicOr(&c.map[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
-    // a choice's row: how many distinct (expert, token) pairs come before it
-    int keep[kMaxRows / kThreads], pos[kMaxRows / kThreads];
-    float sum[kMaxRows / kThreads];
+    // lane l: the experts of word l, and how many there are before them
+    unsigned word = c.map[lane];
+    const int mine = __popc(word);
+    int before = mine;
 #pragma unroll
-    for (int i = 0; i < kMaxRows / kThreads; ++i) {
-        const int s = tid + i * kThreads;
-        keep[i] = 0;
-        pos[i] = 0;
-        sum[i] = 0.f;
-        if (s >= S || c.ids[s] < 0) continue;
-        const int t0 = s / a.k * a.k, e = c.ids[s];
-        keep[i] = 1;
-        for (int j = t0; j < t0 + a.k; ++j)
-            if (c.ids[j] == e) {
-                if (j < s) keep[i] = 0;
-                sum[i] += c.w[j];
-            }
+    for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xffffffffu, before, d);
+        if (lane >= d) before += o;
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMaxRows / kThreads; ++i) {
-        const int s = tid + i * kThreads;
-        if (s < S && c.ids[s] >= 0 && !keep[i]) c.ids[s] = -2 - c.ids[s];  // not a row
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMaxRows / kThreads; ++i) {
-        const int s = tid + i * kThreads;
-        if (!keep[i]) continue;
-        const int e = c.ids[s];
-        for (int j = 0; j < S; ++j) {
-            const int o = c.ids[j];
-            pos[i] += o >= 0 && (o < e || (o == e && j < s));
+    const int used = __shfl_sync(0xffffffffu, before, 31);
+    before -= mine;
+    if (warp == 0) {
+        if (lane == 0) c.used = used;
+        while (word != 0u) {
+            c.expert[before++] = static_cast<short>(lane * 32 + __ffs(word) - 1);
+            word &= word - 1u;
         }
-        c.token[pos[i]] = static_cast<short>(s / a.k);
-        c.choice[pos[i]] = static_cast<short>(s);
-        c.weight[pos[i]] = sum[i];
     }
-    // rows, and where a new expert begins
-    int rows_ = 0;
-    for (int s0 = 0; s0 < S; s0 += kThreads)
-        rows_ += __syncthreads_count(s0 + tid < S && c.ids[s0 + tid] >= 0);
-    if (tid < 32) {
-        int used = 0;
-        for (int p0 = 0; p0 < rows_; p0 += 32) {
-            const int p = p0 + tid;
-            int e = -1;
-            bool begins = false;
-            if (p < rows_) {
-                e = c.ids[c.choice[p]];
-                begins = p == 0 || c.ids[c.choice[p - 1]] != e;
+    __syncthreads();
+    // this token's first choice of expert e, or -1
+    auto choice_of = [&](int t, int e) {
+        if (t < a.T)
+            for (int j = 0; j < a.k; ++j)
+                if (c.ids[t * a.k + j] == e) return t * a.k + j;
+        return -1;
+    };
+    // a warp an expert, a lane a token: count the rows, then place them
+    for (int u = warp; u < used; u += WARPS) {
+        const int e = c.expert[u];
+        int n = 0;
+        for (int t0 = 0; t0 < a.T; t0 += 32)
+            n += __popc(__ballot_sync(0xffffffffu, choice_of(t0 + lane, e) >= 0));
+        if (lane == 0) c.first[u + 1] = static_cast<short>(n);
+    }
+    if (tid == 0) c.first[0] = 0;
+    __syncthreads();
+    if (warp == 0) {  // counts to first rows
+        int sum = 0;
+        for (int u0 = 0; u0 < used; u0 += 32) {
+            int n = u0 + lane < used ? c.first[u0 + lane + 1] : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int o = __shfl_up_sync(0xffffffffu, n, d);
+                if (lane >= d) n += o;
             }
-            const unsigned m = __ballot_sync(0xffffffffu, begins);
-            if (begins) {
-                const int u = used + __popc(m & ((1u << tid) - 1u));
-                c.first[u] = static_cast<short>(p);
-                c.expert[u] = static_cast<short>(e);
-            }
-            used += __popc(m);
+            if (u0 + lane < used) c.first[u0 + lane + 1] = static_cast<short>(sum + n);
+            sum += __shfl_sync(0xffffffffu, n, 31);
         }
-        if (tid == 0) {
-            c.first[used] = static_cast<short>(rows_);
-            c.used = used;
+    }
+    __syncthreads();
+    for (int u = warp; u < used; u += WARPS) {
+        const int e = c.expert[u];
+        int at = c.first[u];
+        for (int t0 = 0; t0 < a.T; t0 += 32) {
+            const int t = t0 + lane, s = choice_of(t, e);
+            const unsigned has = __ballot_sync(0xffffffffu, s >= 0);
+            if (s >= 0) {
+                float sum = 0.f;
+                for (int j = s; j < (t + 1) * a.k; ++j)
+                    if (c.ids[j] == e) sum += c.w[j];
+                const int p = at + __popc(has & ((1u << lane) - 1u));
+                c.token[p] = static_cast<short>(t);
+                c.choice[p] = static_cast<short>(s);
+                c.weight[p] = sum;
+            }
+            at += __popc(has);
         }
     }
     __syncthreads();
@@ -244,20 +252,28 @@ struct Pieces {
         : base(smem_u32(smem) + static_cast<uint32_t>(warp * BYTES + lane * 16)), t(lane & 3)
     {
     }
-    // Copies the step from k0 on of the rows; zeros past K, nothing past K is read.
+    // Copies the step from k0 on of the rows, given from this lane's first piece
+    // on; zeros past K, nothing past K is read.
     __device__ __forceinline__ void ask(int slot, const char *const (&row)[CF][2], int k0, int K)
     {
+        const bool whole = k0 + W::STEP <= K;
 #pragma unroll
         for (int c = 0; c < CF; ++c)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int k = k0 + W::N * t + 4 * W::N * i;
-                    const int left = min(max((K - k) * W::ES, 0), 16);
-                    cp_async_16(base + static_cast<uint32_t>((slot * PER + (c * 2 + r) * 2 + i) * 512),
-                                row[c][r] + (left > 0 ? static_cast<long long>(k) * W::ES : 0LL),
-                                static_cast<uint32_t>(left));
+                    const uint32_t to =
+                        base + static_cast<uint32_t>((slot * PER + (c * 2 + r) * 2 + i) * 512);
+                    const char *from = row[c][r] + k0 * W::ES + 64 * i;
+                    if (whole) {
+                        cp_async_16(to, from, 16u);
+                    } else {
+                        const int k = k0 + W::N * t + 4 * W::N * i;
+                        const int left = min(max((K - k) * W::ES, 0), 16);
+                        cp_async_16(to, left > 0 ? from : row[c][r] - W::N * W::ES * t,
+                                    static_cast<uint32_t>(left));
+                    }
                 }
     }
     static __device__ __forceinline__ void commit()
@@ -287,24 +303,40 @@ struct Pieces {
     }
 };
 
+// A token's values for the step from k0 on: row from lane t's first value on.
+template <class T, bool I8, bool XV>
+__device__ __forceinline__ void load_step(uint4 (&x)[2][Weights<T, I8>::TOK], const char *row,
+                                          int k0, int K, int t)
+{
+    using W = Weights<T, I8>;
+    const bool whole = XV && k0 + W::STEP <= K;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < W::TOK; ++j) {
+            const int k = k0 + 4 * W::N * i + 8 * j;
+            if (whole)
+                x[i][j] = *reinterpret_cast<const uint4 *>(row + 2 * k);
+            else
+                x[i][j] = load_token<XV>(row, k, K - W::N * t);
+        }
+}
+
 // acc += weights * tokens over the step from k0 on: CF fragments of weights, the
-// groups of eight tokens that there are.  trow: token g of each group; lane t
-// takes k0 + N t + 4 N i + 0 .. N-1 of piece i.
+// groups of eight tokens that there are, the first one's values in x.
 template <class T, bool I8, int CF, int NF, bool XV>
 __device__ __forceinline__ void multiply(float (&acc)[CF][NF][4], const uint4 (&w)[CF][2][2],
+                                         uint4 (&x)[2][Weights<T, I8>::TOK],
                                          const char *const (&trow)[NF], int k0, int K, int t,
                                          int tokens)
 {
     using W = Weights<T, I8>;
 #pragma unroll
     for (int n = 0; n < NF; ++n) {
-        if (n > 0 && 8 * n >= tokens) break;
-        uint4 x[2][W::TOK];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < W::TOK; ++j)
-                x[i][j] = load_token<XV>(trow[n], k0 + W::N * t + 4 * W::N * i + 8 * j, K);
+        if (n > 0) {
+            if (8 * n >= tokens) break;
+            load_step<T, I8, XV>(x, trow[n], k0, K, t);
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -324,120 +356,147 @@ __device__ __forceinline__ void multiply(float (&acc)[CF][NF][4], const uint4 (&
 
 // ---------------------------------------------------------------------- up
 
-constexpr int kUpDepth = 2;
+constexpr int kUpWarps = 8, kUpDepth = 2;
 template <class T, bool I8, int NF>
-constexpr int up_smem()
-{
-    constexpr int ring = kWarps * Pieces<T, I8, 2, kUpDepth>::BYTES;
-    constexpr int part = kWarps * 8 * NF * (2 * kCh + 4) * 4;
-    return ring > part ? ring : part;
-}
-
-// grid: 16 rows of G and U (x), the used expert (y).  The warps share the steps
-// of k; their sums meet in shared memory, in the warps' order.
-template <class T, bool I8, int NF, bool XV>
-__global__ void __launch_bounds__(kThreads, NF <= 2 ? 3 : 2) up_kernel(const Args a)
-{
-    constexpr int TK = 8 * NF;
-    using W = Weights<T, I8>;
+struct Up {
     using P = Pieces<T, I8, 2, kUpDepth>;
+    static constexpr int TK = 8 * NF, RING = kUpWarps * P::BYTES;
+    static constexpr int SMEM = RING + kUpWarps * TK * (2 * kCh + 4) * 4;
+    static constexpr int BLOCKS = NF <= 4 ? 2 : 1;  // of a multiprocessor
+};
+
+// A unit is 16 rows of G and of U of one used expert; a block takes every
+// gridDim.x-th.  The warps share a unit's steps of k, and the next unit's weights
+// are on their way before this one's sums meet in shared memory, in the warps'
+// order.
+template <class T, bool I8, int NF, bool XV>
+__global__ void __launch_bounds__(kUpWarps * 32, Up<T, I8, NF>::BLOCKS) up_kernel(const Args a)
+{
+    using W = Weights<T, I8>;
+    using U = Up<T, I8, NF>;
+    using P = typename U::P;
     __shared__ Choices c;
     extern __shared__ __align__(16) unsigned char dyn[];  // the rings, then the sums
+    float(*part)[U::TK][2 * kCh + 4] =
+        reinterpret_cast<float(*)[U::TK][2 * kCh + 4]>(dyn + U::RING);
     dependent_wait();
     dependent_release();  // (after the wait: the next kernel reads ids and weights early)
-    find_choices(a, c);
-    const int u = blockIdx.y;
-    if (u >= c.used) return;
+    find_choices<kUpWarps>(a, c);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int e = c.expert[u], f0 = blockIdx.x * kCh, r0 = c.first[u], n = c.first[u + 1] - r0;
-    const char *wrow[2][2], *trow[NF];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-            wrow[i][r] = static_cast<const char *>(a.W1) + e * a.stride1 +
-                         (static_cast<long long>(i) * a.F + min(f0 + g + 8 * r, a.F - 1)) * a.p1;
-#pragma unroll
-    for (int i = 0; i < NF; ++i)
-        trow[i] = static_cast<const char *>(a.x) +
-                  c.token[r0 + min(8 * i + g, n - 1)] * a.ldx * static_cast<int>(sizeof(T));
+    const int slices = (a.F + kCh - 1) / kCh, units = c.used * slices;
+    constexpr int k_step = kUpWarps * W::STEP;
     P ring(dyn, warp, lane);
-    const int k_step = kWarps * W::STEP;
-    int ask = warp * W::STEP;
-    for (int d = 0; d < kUpDepth; ++d, ask += k_step) {
-        if (ask < a.H) ring.ask(d, wrow, ask, a.H);
-        P::commit();
-    }
-    float acc[2][NF][4] = {};
-    int slot = 0;
-    for (int k = warp * W::STEP; k < a.H; k += k_step, ask += k_step) {
-        uint4 w[2][2][2];
-        P::arrived();
-        ring.take(slot, w);
-        if (ask < a.H) ring.ask(slot, wrow, ask, a.H);
-        P::commit();
-        multiply<T, I8, 2, NF, XV>(acc, w, trow, k, a.H, t, n);
-        slot = slot + 1 == kUpDepth ? 0 : slot + 1;
-    }
-    __syncthreads();  // every ring is read: the sums take its place
-    float(*part)[TK][2 * kCh + 4] = reinterpret_cast<float(*)[TK][2 * kCh + 4]>(dyn);
+    // the step asked for next: of unit au, from ak on
+    int au = blockIdx.x, ak = warp * W::STEP;
+    const char *arow[2][2];
+    auto ask_rows = [&]() {
+        const int u = au / slices, f0 = (au - u * slices) * kCh;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int m = 0; m < NF; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                part[warp][8 * m + 2 * t + (j & 1)][kCh * i + 8 * (j >> 1) + g] = acc[i][m][j];
-    __syncthreads();
-    for (int i = threadIdx.x; i < n * kCh; i += kThreads) {
-        const int m = i / kCh, f = i % kCh;
-        float gate = 0.f, up = 0.f;
-        if (f0 + f < a.F) {
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                gate += part[w][m][f];
-                up += part[w][m][kCh + f];
-            }
-            if (I8) {
-                const float *s = a.scale1 + static_cast<long long>(e) * 2 * a.F + f0 + f;
-                gate *= s[0];
-                up *= s[a.F];
+            for (int r = 0; r < 2; ++r)
+                arow[i][r] = static_cast<const char *>(a.W1) + c.expert[u] * a.stride1 +
+                             (static_cast<long long>(i) * a.F + min(f0 + g + 8 * r, a.F - 1)) * a.p1 +
+                             W::N * W::ES * t;
+    };
+    auto ask_next = [&](int slot) {
+        if (au < units && warp * W::STEP < a.H) {
+            ring.ask(slot, arow, ak, a.H);
+            ak += k_step;
+            if (ak >= a.H) {
+                ak = warp * W::STEP;
+                au += gridDim.x;
+                if (au < units) ask_rows();
             }
         }
-        // (values past F are zeros: gate is)
-        static_cast<T *>(a.h)[c.choice[r0 + m] * a.ldh + f0 + f] =
-            rows::from_f<T>(gate / (1.f + expf(-gate)) * up);
+        P::commit();
+    };
+    if (au < units) ask_rows();
+    for (int d = 0; d < kUpDepth; ++d) ask_next(d);
+    int slot = 0;
+    for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int u = unit / slices, f0 = (unit - u * slices) * kCh;
+        const int e = c.expert[u], r0 = c.first[u], n = c.first[u + 1] - r0;
+        const char *trow[NF];
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+            trow[i] = static_cast<const char *>(a.x) +
+                      c.token[r0 + min(8 * i + g, n - 1)] * a.ldx * 2 + 2 * W::N * t;
+        float acc[2][NF][4] = {};
+        uint4 x[2][W::TOK];
+        if (warp * W::STEP < a.H) load_step<T, I8, XV>(x, trow[0], warp * W::STEP, a.H, t);
+        for (int k = warp * W::STEP; k < a.H; k += k_step) {
+            uint4 w[2][2][2], nx[2][W::TOK];
+            if (k + k_step < a.H) load_step<T, I8, XV>(nx, trow[0], k + k_step, a.H, t);
+            P::arrived();
+            ring.take(slot, w);
+            ask_next(slot);
+            multiply<T, I8, 2, NF, XV>(acc, w, x, trow, k, a.H, t, n);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < W::TOK; ++j) x[i][j] = nx[i][j];
+            slot = slot + 1 == kUpDepth ? 0 : slot + 1;
+        }
+        __syncthreads();  // the last unit's sums are read
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int m = 0; m < NF; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    part[warp][8 * m + 2 * t + (j & 1)][kCh * i + 8 * (j >> 1) + g] = acc[i][m][j];
+        __syncthreads();
+        for (int i = threadIdx.x; i < n * kCh; i += kUpWarps * 32) {
+            const int m = i / kCh, f = i % kCh;
+            float gate = 0.f, up = 0.f;
+            if (f0 + f < a.F) {
+#pragma unroll
+                for (int w = 0; w < kUpWarps; ++w) {
+                    gate += part[w][m][f];
+                    up += part[w][m][kCh + f];
+                }
+                if (I8) {
+                    const float *s = a.scale1 + static_cast<long long>(e) * 2 * a.F + f0 + f;
+                    gate *= s[0];
+                    up *= s[a.F];
+                }
+            }
+            // (values past F are zeros: gate is)
+            static_cast<T *>(a.h)[c.choice[r0 + m] * a.ldh + f0 + f] =
+                rows::from_f<T>(gate / (1.f + expf(-gate)) * up);
+        }
     }
 }
 
 // -------------------------------------------------------------------- down
 
-constexpr int kDownDepth = 6;
+constexpr int kDownWarps = 16, kDownDepth = 4;
 
 // grid: 16 channels of out.  The steps of all used experts form one list, a
 // part of which is each warp's; a warp adds an expert's results, weighted, to
 // sums of its own, and the block adds those in the warps' order.
 template <class T, bool I8, int NF>
-__global__ void __launch_bounds__(kThreads, 2) down_kernel(const Args a)
+__global__ void __launch_bounds__(kDownWarps * 32, 1) down_kernel(const Args a)
 {
     using W = Weights<T, I8>;
     using P = Pieces<T, I8, 1, kDownDepth>;
     __shared__ Choices c;
     extern __shared__ __align__(16) unsigned char dyn[];  // the rings, [warp][token][channel] sums
-    float *sums = reinterpret_cast<float *>(dyn + kWarps * P::BYTES);  // rows of kCh + 1
+    float *sums = reinterpret_cast<float *>(dyn + kDownWarps * P::BYTES);  // rows of kCh + 1
     dependent_release();
     // The up kernel releases its dependents after its own wait, so what it found
     // complete, ids and weights among it, is complete here too, and is read while
     // it still runs.  (F == 0: there is no up kernel.)
     if (a.F == 0) dependent_wait();
-    find_choices(a, c);
+    find_choices<kDownWarps>(a, c);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int h0 = blockIdx.x * kCh;
     float *mine = sums + static_cast<long long>(warp) * a.T * (kCh + 1);
     for (int i = lane; i < a.T * (kCh + 1); i += 32) mine[i] = 0.f;
     const int steps = (a.F + W::STEP - 1) / W::STEP, total = c.used * steps;
-    int at = static_cast<int>(static_cast<long long>(total) * warp / kWarps);
-    const int end = static_cast<int>(static_cast<long long>(total) * (warp + 1) / kWarps);
+    int at = static_cast<int>(static_cast<long long>(total) * warp / kDownWarps);
+    const int end = static_cast<int>(static_cast<long long>(total) * (warp + 1) / kDownWarps);
     P ring(dyn, warp, lane);
     // the step asked for next: expert au, its rows, step as
     int ask = at, au = steps > 0 ? at / steps : 0, as = at - au * steps;
@@ -446,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const Args a)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
             arow[0][r] = static_cast<const char *>(a.W2) + c.expert[au] * a.stride2 +
-                         min(h0 + g + 8 * r, a.H - 1) * a.p2;
+                         min(h0 + g + 8 * r, a.H - 1) * a.p2 + W::N * W::ES * t;
     };
     auto ask_next = [&](int slot) {
         if (ask < end) {
@@ -477,14 +536,21 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const Args a)
 #pragma unroll
         for (int i = 0; i < NF; ++i)
             trow[i] = static_cast<const char *>(a.h) +
-                      c.choice[r0 + min(8 * i + g, n - 1)] * a.ldh * static_cast<int>(sizeof(T));
+                      c.choice[r0 + min(8 * i + g, n - 1)] * a.ldh * 2 + 2 * W::N * t;
         float acc[1][NF][4] = {};
+        uint4 x[2][W::TOK];
+        load_step<T, I8, true>(x, trow[0], lo * W::STEP, a.F, t);
         for (int s = lo; s < hi; ++s) {
-            uint4 w[1][2][2];
+            uint4 w[1][2][2], nx[2][W::TOK];
+            if (s + 1 < hi) load_step<T, I8, true>(nx, trow[0], (s + 1) * W::STEP, a.F, t);
             P::arrived();
             ring.take(slot, w);
             ask_next(slot);
-            multiply<T, I8, 1, NF, true>(acc, w, trow, s * W::STEP, a.F, t, n);
+            multiply<T, I8, 1, NF, true>(acc, w, x, trow, s * W::STEP, a.F, t, n);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < W::TOK; ++j) x[i][j] = nx[i][j];
             slot = slot + 1 == kDownDepth ? 0 : slot + 1;
         }
 #pragma unroll
@@ -500,44 +566,47 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const Args a)
         at += hi - lo;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.T * kCh; i += kThreads) {
+    for (int i = threadIdx.x; i < a.T * kCh; i += kDownWarps * 32) {
         const int m = i / kCh, ch = i % kCh;
         if (h0 + ch >= a.H) continue;
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) s += sums[(w * a.T + m) * (kCh + 1) + ch];
+        for (int w = 0; w < kDownWarps; ++w) s += sums[(w * a.T + m) * (kCh + 1) + ch];
         static_cast<T *>(a.out)[m * a.ldo + h0 + ch] = rows::from_f<T>(s);
     }
 }
 
 template <class T, bool I8, int NF>
-int launch(const Args &a, bool x_vec, cudaStream_t st)
+int launch(const Args &a, bool x_vec, int num_sms, cudaStream_t st)
 {
-    const int rows_ = a.T * a.k, most = a.E < rows_ ? a.E : rows_;
-    const dim3 grid(static_cast<unsigned>((a.F + kCh - 1) / kCh), static_cast<unsigned>(most));
     if (a.F > 0) {
+        using U = Up<T, I8, NF>;
         auto kern = x_vec ? up_kernel<T, I8, NF, true> : up_kernel<T, I8, NF, false>;
-        constexpr int smem = up_smem<T, I8, NF>();
-        if (!smem_attr_once(reinterpret_cast<const void *>(kern), smem)) return SGEMM_ERR_LAUNCH;
-        const int s = launch_dependent(kern, grid, dim3(kThreads), smem, 1, st, a);
+        if (!smem_attr_once(reinterpret_cast<const void *>(kern), U::SMEM)) return SGEMM_ERR_LAUNCH;
+        const long long rows_ = static_cast<long long>(a.T) * a.k;
+        const long long units = (a.E < rows_ ? a.E : rows_) * ((a.F + kCh - 1) / kCh);
+        const long long room = static_cast<long long>(U::BLOCKS) * num_sms;
+        const int s = launch_dependent(kern, dim3(static_cast<unsigned>(units < room ? units : room)),
+                                       dim3(kUpWarps * 32), U::SMEM, 1, st, a);
         if (s != SGEMM_OK) return s;
     }
-    constexpr int ring = kWarps * Pieces<T, I8, 1, kDownDepth>::BYTES;
-    constexpr int per_token = static_cast<int>(sizeof(float)) * kWarps * (kCh + 1);
+    constexpr int ring = kDownWarps * Pieces<T, I8, 1, kDownDepth>::BYTES;
+    constexpr int per_token = static_cast<int>(sizeof(float)) * kDownWarps * (kCh + 1);
     auto kern = down_kernel<T, I8, NF>;
     if (!smem_attr_once(reinterpret_cast<const void *>(kern), ring + per_token * 8 * NF))
         return SGEMM_ERR_LAUNCH;
     return launch_dependent(kern, dim3(static_cast<unsigned>((a.H + kCh - 1) / kCh)),
-                            dim3(kThreads), static_cast<size_t>(ring + per_token * a.T), 1, st, a);
+                            dim3(kDownWarps * 32), static_cast<size_t>(ring + per_token * a.T), 1, st,
+                            a);
 }
 
 template <class T, bool I8>
-int run(const Args &a, bool x_vec, cudaStream_t st)
+int run(const Args &a, bool x_vec, int num_sms, cudaStream_t st)
 {
-    if (a.T <= 8) return launch<T, I8, 1>(a, x_vec, st);
-    if (a.T <= 16) return launch<T, I8, 2>(a, x_vec, st);
-    if (a.T <= 32) return launch<T, I8, 4>(a, x_vec, st);
-    return launch<T, I8, 8>(a, x_vec, st);
+    if (a.T <= 8) return launch<T, I8, 1>(a, x_vec, num_sms, st);
+    if (a.T <= 16) return launch<T, I8, 2>(a, x_vec, num_sms, st);
+    if (a.T <= 32) return launch<T, I8, 4>(a, x_vec, num_sms, st);
+    return launch<T, I8, 8>(a, x_vec, num_sms, st);
 }
 
 bool sizes_ok(int T, int k, int H, int F)
@@ -618,9 +687,9 @@ int sgemm_experts_layer(int type, int wtype, int T, int k, int E, int H, int F, 
         const bool x_vec = rows::aligned_to(x, 16) && ldx % 8 == 0;
         cudaStream_t st = static_cast<cudaStream_t>(stream);
         if (type == SGEMM_TYPE_BF16)
-            return i8 ? few::run<__nv_bfloat16, true>(a, x_vec, st)
-                      : few::run<__nv_bfloat16, false>(a, x_vec, st);
-        return i8 ? few::run<__half, true>(a, x_vec, st) : few::run<__half, false>(a, x_vec, st);
+            return i8 ? few::run<__nv_bfloat16, true>(a, x_vec, num_sms, st)
+                      : few::run<__nv_bfloat16, false>(a, x_vec, num_sms, st);
+        return i8 ? few::run<__half, true>(a, x_vec, num_sms, st) : few::run<__half, false>(a, x_vec, num_sms, st);
     });
 }
 
