@@ -68,6 +68,54 @@ template <int WARPS>
 __device__ __forceinline__ void find_choices(const Args &a, Choices &c)
 {
     const int S = a.T * a.k, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (S <= 32) {  // one warp, a lane a choice
+        if (warp == 0) {
+            constexpr unsigned all = 0xffffffffu;
+            int e = -1;
+            float w = 1.f;
+            if (lane < S) {
+                e = __ldcg(a.ids + lane);
+                if (a.weights != nullptr) w = __ldcg(a.weights + lane);
+            }
+            const bool kept = e >= 0 && e < a.E;
+            const unsigned none = 0x80000000u | lane;  // like no other lane's
+            const int t = lane / a.k;
+            const unsigned same = __match_any_sync(all, kept ? static_cast<unsigned>(t << 16 | e) : none);
+            const bool row = kept && __ffs(same) - 1 == lane;
+            float sum = w;
+            if (__any_sync(all, kept && (same & (same - 1u)) != 0u)) {
+                sum = 0.f;
+                for (int o = 0; o < S; ++o) {
+                    const float v = __shfl_sync(all, w, o);
+                    if (same >> o & 1u) sum += v;
+                }
+            }
+            const unsigned of_e = __match_any_sync(all, row ? static_cast<unsigned>(e) : none);
+            const bool begins = row && __ffs(of_e) - 1 == lane;
+            const unsigned rows_ = __ballot_sync(all, row), starts = __ballot_sync(all, begins);
+            int pos = 0, u = 0;
+            for (unsigned m = rows_; m != 0u; m &= m - 1u) {
+                const int o = __ffs(m) - 1, eo = __shfl_sync(all, e, o);
+                pos += eo < e || (eo == e && o < lane);
+                u += eo < e && (starts >> o & 1u);
+            }
+            if (row) {
+                c.token[pos] = static_cast<short>(t);
+                c.choice[pos] = static_cast<short>(lane);
+                c.weight[pos] = sum;
+            }
+            if (begins) {
+                c.expert[u] = static_cast<short>(e);
+                c.first[u] = static_cast<short>(pos);
+            }
+            if (lane == 0) {
+                c.used = __popc(starts);
+                c.first[__popc(starts)] = static_cast<short>(__popc(rows_));
+            }
+        }
+        __syncthreads();
+        return;
+    }
     if (tid < kMaxExperts / 32) c.map[tid] = 0u;
     __syncthreads();
     for (int s = tid; s < S; s += WARPS * 32) {
@@ -166,17 +214,21 @@ __device__ __forceinline__ void widen4(uint32_t x, uint32_t &lo, uint32_t &hi)
         lo = *reinterpret_cast<const uint32_t *>(&ha);
         hi = *reinterpret_cast<const uint32_t *>(&hb);
     } else {
-        // bf16 has seven bits below the leading one: the low seven bits of x above
-        // 128, plus -128 or, of a negative x (its top bit stands for -128), -256
-        auto pair = [](uint32_t w) {
-            const uint32_t a = (w & 0x007F007Fu) | 0x43004300u;  // 128 + low bits
-            const uint32_t b = (w & 0x00800080u) | 0xC300C300u;  // -128 or -256
-            const __nv_bfloat162 s = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
-                                             *reinterpret_cast<const __nv_bfloat162 *>(&b));
+        // 0x43uu is bf16's 128 + u below u = 128 and 2 u from there on: less 256, that
+        // is x where x is negative and 2 x where it is not, from which max(0, x) is
+        // taken.  (Every step is exact.  Logic on the bits instead, which runs at half
+        // the rate of packed arithmetic: 128 + low seven bits, plus -128 or -256.)
+        const uint32_t u = x ^ 0x80808080u;
+        const __nv_bfloat162 half = __float2bfloat162_rn(0.5f), minus = __float2bfloat162_rn(-1.f);
+        auto pair = [&](uint32_t w) {
+            const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162 *>(&w);
+            const __nv_bfloat162 r = __hadd2(f, __float2bfloat162_rn(-256.f));
+            const __nv_bfloat162 p = __hfma2_relu(f, half, __float2bfloat162_rn(-128.f));
+            const __nv_bfloat162 s = __hfma2(p, minus, r);
             return *reinterpret_cast<const uint32_t *>(&s);
         };
-        lo = pair(__byte_perm(x, 0u, 0x4140));
-        hi = pair(__byte_perm(x, 0u, 0x4342));
+        lo = pair(__byte_perm(u, 0x43434343u, 0x4140));
+        hi = pair(__byte_perm(u, 0x43434343u, 0x4342));
     }
 }
 
@@ -422,6 +474,16 @@ __global__ void __launch_bounds__(kUpWarps * 32, Up<T, I8, NF>::BLOCKS) up_kerne
         for (int i = 0; i < NF; ++i)
             trow[i] = static_cast<const char *>(a.x) +
                       c.token[r0 + min(8 * i + g, n - 1)] * a.ldx * 2 + 2 * W::N * t;
+        // the scales of the results that this thread will make, all of one row of
+        // G and U
+        const int f = threadIdx.x % kCh;
+        const bool live = f0 + f < a.F;
+        float sg = 1.f, su = 1.f;
+        if (I8 && live && threadIdx.x < n * kCh) {
+            const float *s = a.scale1 + static_cast<long long>(e) * 2 * a.F + f0 + f;
+            sg = s[0];
+            su = s[a.F];
+        }
         float acc[2][NF][4] = {};
         uint4 x[2][W::TOK];
         if (warp * W::STEP < a.H) load_step<T, I8, XV>(x, trow[0], warp * W::STEP, a.H, t);
@@ -448,19 +510,16 @@ __global__ void __launch_bounds__(kUpWarps * 32, Up<T, I8, NF>::BLOCKS) up_kerne
                     part[warp][8 * m + 2 * t + (j & 1)][kCh * i + 8 * (j >> 1) + g] = acc[i][m][j];
         __syncthreads();
         for (int i = threadIdx.x; i < n * kCh; i += kUpWarps * 32) {
-            const int m = i / kCh, f = i % kCh;
+            const int m = i / kCh;
             float gate = 0.f, up = 0.f;
-            if (f0 + f < a.F) {
+            if (live) {
 #pragma unroll
                 for (int w = 0; w < kUpWarps; ++w) {
                     gate += part[w][m][f];
                     up += part[w][m][kCh + f];
                 }
-                if (I8) {
-                    const float *s = a.scale1 + static_cast<long long>(e) * 2 * a.F + f0 + f;
-                    gate *= s[0];
-                    up *= s[a.F];
-                }
+                gate *= sg;
+                up *= su;
             }
             // (values past F are zeros: gate is)
             static_cast<T *>(a.h)[c.choice[r0 + m] * a.ldh + f0 + f] =
@@ -471,7 +530,7 @@ __global__ void __launch_bounds__(kUpWarps * 32, Up<T, I8, NF>::BLOCKS) up_kerne
 
 // -------------------------------------------------------------------- down
 
-constexpr int kDownWarps = 16, kDownDepth = 4;
+constexpr int kDownWarps = 16, kDownDepth = 3;
 
 // grid: 16 channels of out.  The steps of all used experts form one list, a
 // part of which is each warp's; a warp adds an expert's results, weighted, to
