@@ -10,8 +10,8 @@
 // logic instructions decode two codes.  (The conversion instruction for codes has
 // a fraction of their rate: decoded by it and multiplied by mma.sync, one token
 // through 4096 x 4096 took 7.9 us.)  Packed fp16 FMAs add the products of 16
-// values exactly: each half of the sum takes eight, at most 288 in units of a
-// quarter.  Then it is fp32: a block's two halves times both block scales.
+// values exactly: each half of the sum takes eight, at most 1152 units of a
+// quarter's product.  Then it is fp32: a block's two halves times both block scales.
 //
 // A warp takes four channels 32 apart, whose scales for 64 values are 16
 // consecutive bytes of the layout, and 1024 k a step, 32 a lane.  The warps of a
@@ -141,16 +141,19 @@ __global__ void __launch_bounds__(kFewWarps * 32, MT == 1 ? 6 : MT == 2 ? 5 : 3)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {  // 16 values: two words
             __half2 xv[MT][8];
-            const __half2 up = __half2half2(__ushort_as_half(0x7400));  // 2^14
+            // tokens times 2^13, so that a product is half of what it stands for and
+            // sums of small scales keep off fp32's end
+            const __half2 up = __half2half2(__ushort_as_half(0x7400));   // 2^14
+            const __half2 up2 = __half2half2(__ushort_as_half(0x7000));  // 2^13
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 __half2 h[4];
                 decode8(b ? x[m].z : x[m].x, h);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) xv[m][i] = __hmul2(h[i], up);
+                for (int i = 0; i < 4; ++i) xv[m][i] = __hmul2(__hmul2(h[i], up), up2);
                 decode8(b ? x[m].w : x[m].y, h);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) xv[m][4 + i] = __hmul2(h[i], up);
+                for (int i = 0; i < 4; ++i) xv[m][4 + i] = __hmul2(__hmul2(h[i], up), up2);
             }
 #pragma unroll
             for (int c = 0; c < kFewCh; ++c) {
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, MT == 1 ? 6 : MT == 2 ? 5 : 3)
             for (int j = 0; j < wk; ++j) s += part[gr * wk + j][m * kFewCh + c];
             const float sa = a.scaleA != nullptr ? a.scaleA[m] : 1.f;
             const float sb = a.scaleB != nullptr ? a.scaleB[n] : 1.f;
-            static_cast<T *>(a.C)[m * a.ldc + n] = rows::from_f<T>(s * 16384.f * sa * sb);
+            static_cast<T *>(a.C)[m * a.ldc + n] = rows::from_f<T>(2.f * s * sa * sb);
         }
     }
 }

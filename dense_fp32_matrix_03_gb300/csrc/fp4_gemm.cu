@@ -13,6 +13,7 @@ namespace sg {
 namespace fp4 {
 
 constexpr int kMaxSide = 0x7FFFFFFF - 511;  // an index a tile past the last row or channel still is an int
+constexpr int kMaxK = 0x7FFFFFFF - 8191;    // and one a step of a whole block past the last value
 
 // K == 0: zeros times the scales.
 template <class T>
@@ -182,7 +183,7 @@ int sgemm_fp4(int type, int format, int M, int N, int K, const unsigned char *A,
         if (!rows::valid_type(type) || !fp4::valid_format(format) || M < 0 || N < 0 || K < 0 ||
             lda < 1 || ldb < 1 || ldc < 1 || lda < K || ldb < K || ldc < N ||
             lda % fp4::kLdStep != 0 || ldb % fp4::kLdStep != 0 || M > fp4::kMaxSide ||
-            N > fp4::kMaxSide)
+            N > fp4::kMaxSide || K > fp4::kMaxK)
             return SGEMM_ERR_INVALID_ARG;
         if (M == 0 || N == 0) return SGEMM_OK;
         if (C == nullptr || !rows::aligned_to(C, rows::elem_size(type)) ||

@@ -80,7 +80,8 @@ int sgemm_fp4_quantize_rows(int type, int act, int format, int M, int K, const v
                             void *stream);
 
 /* C (M x N, `type`, ldc >= N) from A and B.  K == 0 writes zeros times the
- * scales.  C may not overlap the inputs.  M and N <= 2^31 - 512. */
+ * scales.  C may not overlap the inputs.  M and N <= 2^31 - 512,
+ * K <= 2^31 - 8192. */
 int sgemm_fp4(int type, int format, int M, int N, int K, const unsigned char *A, int lda,
               const unsigned char *sfA, const float *scaleA, const unsigned char *B, int ldb,
               const unsigned char *sfB, const float *scaleB, void *C, int ldc, void *stream);

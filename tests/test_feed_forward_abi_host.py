@@ -69,7 +69,8 @@ BAD = [
         dict(lda=40), dict(ldb=32), dict(ldb=72), dict(ldc=3), dict(A=0), dict(B=0), dict(C=0),
         dict(sfA=0), dict(sfB=0), dict(A=FAKE + 8), dict(B=FAKE + 8), dict(sfA=FAKE + 4),
         dict(sfB=FAKE + 4), dict(C=FAKE + 1), dict(scaleA=FAKE + 2), dict(scaleB=FAKE + 2),
-        dict(M=2 ** 31 - 511), dict(N=2 ** 31 - 511, ldc=2 ** 31 - 1))],
+        dict(M=2 ** 31 - 511), dict(N=2 ** 31 - 511, ldc=2 ** 31 - 1),
+        dict(K=2 ** 31 - 8191, lda=2 ** 31 - 32, ldb=2 ** 31 - 32))],
     *[("sgemm_experts_layer", b) for b in (
         dict(type_=2), dict(type_=3), dict(wtype=2), dict(T=-1), dict(T=65), dict(k=0),
         dict(T=64, k=9), dict(k=65), dict(E=0), dict(E=1025), dict(H=-1), dict(F=-1),

@@ -252,6 +252,29 @@ def test_product_of_whole_numbers_is_exact(format_, M):
     assert np.array_equal(product("fp32", *ops), ops[0].values @ ops[1].values.T)
 
 
+@pytest.mark.parametrize("forced", ["few", "slim", "narrow", "wide"], indirect=True)
+@pytest.mark.parametrize("lo", [62, 180])
+def test_products_of_very_small_and_very_large_scales(forced, lo):
+    """Block scales of some 2^-64 (2^54) in both operands: sums near fp32's ends
+    keep their last places (half a unit in the last place of 2^-149 besides)."""
+    import torch
+    rng = np.random.default_rng(lo)
+    K = 640
+    ops = []
+    for r in (4, 140):
+        o = Operand(r, K, "mx", rng, row_scale=False)
+        codes = rng.integers(0, 16, (r, K)).astype(np.uint8)
+        byte = rng.integers(lo, lo + 4, (r, K // 32)).astype(np.uint8)
+        o.codes = torch.from_numpy(ff.pack_codes(codes, o.ld)).cuda()
+        o.sf = torch.from_numpy(ff.pack_scales(byte)).cuda()
+        o.values = ff.values4(codes, byte, "mx")
+        ops.append(o)
+    ref, mag = ff.product4(ops[0].values, ops[0].sc, ops[1].values, ops[1].sc)
+    assert np.abs(ref).max() < 3e38
+    got = product("fp32", *ops)
+    assert np.all(np.abs(got - ref) <= bound("fp32", K, ref, mag) - SUB + K * 2.0 ** -149)
+
+
 @pytest.mark.parametrize("M", [1, 6, 50, 300])
 def test_scales_that_are_no_number(M):
     """A NaN scale of a token or a channel reaches its row or column alone, a

@@ -295,6 +295,27 @@ def test_rows_that_hold_no_number(type_):
         assert not ff.unpack_scales(sf.cpu().numpy(), M, -(-H // ff.BLOCK[format_]))[bad].any()
 
 
+def test_squares_past_the_range():
+    """A row whose sum of squares leaves fp32's range has rho 0: zeros, and the
+    gradient of the stream alone.  (fp16 cannot hold such values.)"""
+    import torch
+    import dense_fp32_matrix_03_gb300 as lib
+    M, H = 2, 64
+    x = torch.full((M, H), 2.0 ** 70, device="cuda")
+    x[1] = 1.0
+    y, sc = torch.empty_like(x), torch.empty(M, device="cuda")
+    q = torch.empty(M, H, dtype=torch.int8, device="cuda")
+    lib.check(lib.sgemm_rms_norm("fp32", M, H, EPS, x, H, None, 0, None, None, 0, y, H))
+    lib.check(lib.sgemm_rms_norm_i8("fp32", M, H, EPS, x, H, None, 0, None, None, 0, q, H, sc))
+    assert not y[0].cpu().numpy().any() and sc[0].item() == 0
+    assert np.allclose(y[1].cpu().numpy(), 1, atol=1e-4) and sc[1].item() > 0
+    ds = torch.randn(M, H, device="cuda")
+    dx = torch.empty_like(x)
+    lib.check(lib.sgemm_rms_norm_grad("fp32", M, H, EPS, x, H, None, ds, H, ds, H, dx, H, None,
+                                      None, 0))
+    assert torch.isfinite(dx[1]).all()
+
+
 def test_rows_without_values():
     import torch
     import dense_fp32_matrix_03_gb300 as lib
