@@ -112,8 +112,8 @@ __device__ __forceinline__ void store_vectors(const float (&v)[EV], unsigned vec
     if (!rs.finite) byte = 0;
     float u[EV];
 #pragma unroll
-    for (int i = 0; i < EV; ++i) u[i] = rs.finite ? v[i] * up : 0.f;
-    const uint32_t codes = pack_codes(u);
+    for (int i = 0; i < EV; ++i) u[i] = v[i] * up;
+    const uint32_t codes = rs.finite ? pack_codes(u) : 0u;
     if constexpr (EV == 8) {
         if (vec < nvec) reinterpret_cast<uint32_t *>(q_row)[vec] = codes;
     } else {  // (eight codes together: the second four past an odd last vector are zeros)

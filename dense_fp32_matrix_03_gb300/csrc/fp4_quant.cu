@@ -4,6 +4,10 @@
 // One pass, as the 8-bit quantiser (quant.cu): a row's values are held in
 // registers between the row's maximum and the rounding.  A block of 16 or 32
 // values spans two to eight lanes, which find its maximum by shuffles.
+//
+// Bound by instructions, not HBM: some 25 a value, among them NV's division for
+// every block.  Measured on GB300, bf16: 8192 x 4096 22.9 us (NV; its bytes take
+// 12.6) and 20.3 (MX), gated 40.4, one row 1.8.
 #include "../../include/fp4_gemm.h"
 #include "dependent.cuh"
 #include "fp4.cuh"
@@ -29,7 +33,10 @@ struct QuantArgs {
     float *scale;
 };
 
-// One vector of the values to quantise, in fp32 (past the row: zeros).
+// One vector of the values to quantise, in fp32 (past the row: zeros).  The gated
+// activation by the fast exponential and division: they are off by 2^-21 or so
+// of a value that is rounded to two or three bits (with the exact ones 8192 x
+// 4096 bf16 took 53 us, so 40).
 template <class T, int VB, int LB, bool GATED>
 __device__ __forceinline__ void load_values(const QuantArgs &a, const char *row, unsigned v,
                                             float (&f)[Words<T, VB>::N])
@@ -46,9 +53,47 @@ __device__ __forceinline__ void load_values(const QuantArgs &a, const char *row,
         float h[EV];
         u.unpack(h);
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(EV); ++i) f[i] = f[i] / (1.f + expf(-f[i])) * h[i];
+        for (int i = 0; i < static_cast<int>(EV); ++i)
+            f[i] = __fdividef(f[i], 1.f + __expf(-f[i])) * h[i];
     }
 }
+
+// A vector of values kept until the maximum is known: as loaded, or, gated,
+// as computed.
+template <class T, int VB, int LB, bool GATED>
+struct Held {
+    static constexpr int EV = Words<T, VB>::N;
+    Words<T, VB> w;
+    __device__ __forceinline__ void zero() { w.zero(); }
+    __device__ __forceinline__ void load(const QuantArgs &a, const char *row, unsigned v)
+    {
+        w.template load<LB>(row + static_cast<long long>(v) * VB,
+                            min(static_cast<unsigned>(a.K) - v * EV, static_cast<unsigned>(EV)) *
+                                static_cast<unsigned>(sizeof(T)));
+    }
+    __device__ __forceinline__ void get(float (&f)[EV]) const { w.unpack(f); }
+    __device__ __forceinline__ void forget() { w.forget(); }
+};
+template <class T, int VB, int LB>
+struct Held<T, VB, LB, true> {
+    static constexpr int EV = Words<T, VB>::N;
+    float f_[EV];
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < EV; ++i) f_[i] = 0.f;
+    }
+    __device__ __forceinline__ void load(const QuantArgs &a, const char *row, unsigned v)
+    {
+        load_values<T, VB, LB, true>(a, row, v, f_);
+    }
+    __device__ __forceinline__ void get(float (&f)[EV]) const
+    {
+#pragma unroll
+        for (int i = 0; i < EV; ++i) f[i] = f_[i];
+    }
+    __device__ __forceinline__ void forget() {}
+};
 
 template <class T, int VB, int LB, bool GATED, int FORMAT>
 __global__ void __launch_bounds__(256, 4) quantize_kernel(const QuantArgs a)
@@ -63,18 +108,21 @@ __global__ void __launch_bounds__(256, 4) quantize_kernel(const QuantArgs a)
     const unsigned tx = threadIdx.x, nx = blockDim.x, warps = nx >> 5;
     const unsigned nvec = live ? a.nvec : 0;
 
-    float held[kHeld][EV];
+    Held<T, VB, LB, GATED> held[kHeld];
     unsigned big = 0;
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
-#pragma unroll
-        for (int i = 0; i < EV; ++i) held[h][i] = 0.f;
-        if (tx + h * nx < nvec) load_values<T, VB, LB, GATED>(a, row, tx + h * nx, held[h]);
+        held[h].zero();
+        if (tx + h * nx < nvec) held[h].load(a, row, tx + h * nx);
     }
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h)
+    for (int h = 0; h < kHeld; ++h) {
+        float f[EV];
+        held[h].get(f);
 #pragma unroll
-        for (int i = 0; i < EV; ++i) big = max(big, __float_as_uint(held[h][i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < EV; ++i) big = max(big, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+        held[h].forget();
+    }
     for (unsigned v = tx + kHeld * nx; v < nvec; v += nx) {
         float f[EV];
         load_values<T, VB, LB, GATED>(a, row, v, f);
@@ -94,7 +142,11 @@ __global__ void __launch_bounds__(256, 4) quantize_kernel(const QuantArgs a)
     const unsigned w0 = tx & ~31u;
 #pragma unroll
     for (int h = 0; h < kHeld; ++h)
-        if (w0 + h * nx < nvec) store_vectors<FORMAT>(held[h], tx + h * nx, nvec, rs, q, sf);
+        if (w0 + h * nx < nvec) {
+            float f[EV];
+            held[h].get(f);
+            store_vectors<FORMAT>(f, tx + h * nx, nvec, rs, q, sf);
+        }
     for (unsigned v = tx + kHeld * nx; (v & ~31u) < nvec; v += nx) {
         float f[EV] = {};
         if (v < nvec) load_values<T, VB, LB, GATED>(a, row, v, f);
