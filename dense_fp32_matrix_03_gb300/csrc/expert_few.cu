@@ -17,6 +17,13 @@
 // bytes of a row together.  The weights come by asynchronous copies into a ring
 // that each lane fills and reads for itself, so that many are on their way
 // without registers or barriers.
+//
+// Measured on GB300, both kernels: one token, 4 of 32 experts of 2048 x 2048, 8 bits
+// (fp16 rows) 18.8 us (their 50 MB take 7.4), 16 bits 24.6; 16 tokens, 4 of 32 experts of
+// 2048 x 1024, 16 bits 62 (4.4 TB/s), 8 bits 48; 32 tokens, 4 of 64, 8 bits 102.  Few
+// tokens are bound by latency: ids, weights and sums in sequence, twice; more by
+// the loads in flight and, in 8 bits, by widening: weights are widened once for
+// each eight tokens of an expert.
 #include <type_traits>
 
 #include "../../include/expert_layer.h"
@@ -408,6 +415,8 @@ __device__ __forceinline__ void multiply(float (&acc)[CF][NF][4], const uint4 (&
 
 // ---------------------------------------------------------------------- up
 
+// Two blocks of eight warps a multiprocessor, two steps of 4 KB a warp on their way
+// (three leave room for one block: one token 24 us instead of 19).
 constexpr int kUpWarps = 8, kUpDepth = 2;
 template <class T, bool I8, int NF>
 struct Up {
@@ -530,6 +539,7 @@ __global__ void __launch_bounds__(kUpWarps * 32, Up<T, I8, NF>::BLOCKS) up_kerne
 
 // -------------------------------------------------------------------- down
 
+// (eight warps with twice the steps on their way: 16 tokens 69 us instead of 61)
 constexpr int kDownWarps = 16, kDownDepth = 3;
 
 // grid: 16 channels of out.  The steps of all used experts form one list, a
