@@ -258,12 +258,11 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Eight 16-bit values of a row from value k on; zeros past K, nothing past K is
-// read.  VEC: the row starts on a 16-byte boundary.
-template <bool VEC>
-__device__ __forceinline__ uint4 load_token(const char *row, int k, int K)
+// Eight 16-bit values of a row from value k on, one by one; zeros past K, nothing
+// past K is read.  (A call of its own: inlined, its comparisons are made at every
+// whole step as well.)
+__device__ __noinline__ uint4 load_token(const char *row, int k, int K)
 {
-    if (VEC && k + 8 <= K) return *reinterpret_cast<const uint4 *>(row + static_cast<long long>(k) * 2);
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -315,25 +314,30 @@ struct Pieces {
     // on; zeros past K, nothing past K is read.
     __device__ __forceinline__ void ask(int slot, const char *const (&row)[CF][2], int k0, int K)
     {
-        const bool whole = k0 + W::STEP <= K;
+        const uint32_t to = base + static_cast<uint32_t>(slot * PER * 512);
+        if (k0 + W::STEP <= K) {
 #pragma unroll
-        for (int c = 0; c < CF; ++c)
+            for (int c = 0; c < CF; ++c)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+                for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t to =
-                        base + static_cast<uint32_t>((slot * PER + (c * 2 + r) * 2 + i) * 512);
-                    const char *from = row[c][r] + k0 * W::ES + 64 * i;
-                    if (whole) {
-                        cp_async_16(to, from, 16u);
-                    } else {
-                        const int k = k0 + W::N * t + 4 * W::N * i;
-                        const int left = min(max((K - k) * W::ES, 0), 16);
-                        cp_async_16(to, left > 0 ? from : row[c][r] - W::N * W::ES * t,
+                    for (int i = 0; i < 2; ++i)
+                        cp_async_16(to + static_cast<uint32_t>(((c * 2 + r) * 2 + i) * 512),
+                                    row[c][r] + k0 * W::ES + 64 * i, 16u);
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                const int left = min(max((K - k0 - W::N * t - 4 * W::N * i) * W::ES, 0), 16);
+#pragma unroll
+                for (int c = 0; c < CF; ++c)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        cp_async_16(to + static_cast<uint32_t>(((c * 2 + r) * 2 + i) * 512),
+                                    left > 0 ? row[c][r] + k0 * W::ES + 64 * i
+                                             : row[c][r] - W::N * W::ES * t,
                                     static_cast<uint32_t>(left));
-                    }
-                }
+            }
+        }
     }
     static __device__ __forceinline__ void commit()
     {
@@ -377,7 +381,7 @@ __device__ __forceinline__ void load_step(uint4 (&x)[2][Weights<T, I8>::TOK], co
             if (whole)
                 x[i][j] = *reinterpret_cast<const uint4 *>(row + 2 * k);
             else
-                x[i][j] = load_token<XV>(row, k, K - W::N * t);
+                x[i][j] = load_token(row, k, K - W::N * t);
         }
 }
 
