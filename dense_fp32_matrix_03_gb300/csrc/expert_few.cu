@@ -20,7 +20,7 @@
 //
 // Measured on GB300, both kernels: one token, 4 of 32 experts of 2048 x 2048, 8 bits
 // (fp16 rows) 18.8 us (their 50 MB take 7.4), 16 bits 24.6; 16 tokens, 4 of 32 experts of
-// 2048 x 1024, 16 bits 62 (4.4 TB/s), 8 bits 48; 32 tokens, 4 of 64, 8 bits 102.  Few
+// 2048 x 1024, 16 bits 62 (4.4 TB/s), 8 bits 48; 32 tokens, 4 of 64, 8 bits 97.  Few
 // tokens are bound by latency: ids, weights and sums in sequence, twice; more by
 // the loads in flight and, in 8 bits, by widening: weights are widened once for
 // each eight tokens of an expert.

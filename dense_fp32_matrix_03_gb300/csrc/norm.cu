@@ -11,7 +11,9 @@
 // vectors of x, the residual and the weight (one of each where there are no more
 // rows than multiprocessors: more threads on a row, 8 x 4096 1.9 us).  Measured on
 // GB300, 8192 x 4096 bf16: row 40.0 us (6.7 TB/s), 8 bits 39.0 (6.0), 4 bits 42.5
-// (5.2, where the rounding's instructions count).  Values held as floats, or taken
+// (5.2, where the rounding's instructions count); rows on 8, 4 and 2 bytes (8192 x
+// 4092, 4094, 4095) 40.4, 41.8 and 78 us, their narrow pieces dealt to a warp's lanes
+// in turn (each lane its own vector's: 106 on 2 bytes).  Values held as floats, or taken
 // out of 16-bit vectors one by one, cost registers and instructions: 8 bits 42.9,
 // 4 bits 48.
 #include "../../include/rms_norm.h"
@@ -51,11 +53,45 @@ __device__ __forceinline__ unsigned bytes_left(int H, unsigned v)
     return min(static_cast<unsigned>(H) - v * EV, EV) * static_cast<unsigned>(sizeof(T));
 }
 
+// A vector of a row, and back: DEALT, with narrow pieces dealt to the warp's lanes.
+// (4 bits want neighbouring values in a lane.)
+template <class T, int VB, int LB, bool DEALT>
+__device__ __forceinline__ void get(Words<T, VB> &w, const char *row, unsigned v, int H)
+{
+    if constexpr (DEALT)
+        w.template load_dealt<LB>(row, v, static_cast<long long>(H) * static_cast<int>(sizeof(T)));
+    else
+        w.template load<LB>(row + static_cast<long long>(v) * VB, bytes_left<T, VB>(H, v));
+}
+template <class T, int VB, int LB, bool DEALT>
+__device__ __forceinline__ void set(const Words<T, VB> &w, char *row, unsigned v, int H)
+{
+    if constexpr (DEALT)
+        w.template store_dealt<LB>(row, v, static_cast<long long>(H) * static_cast<int>(sizeof(T)));
+    else
+        w.template store<LB>(row + static_cast<long long>(v) * VB, bytes_left<T, VB>(H, v));
+}
+// The column of a dealt vector's value i.
 template <class T, int VB, int LB>
+__device__ __forceinline__ long long column(unsigned v, int i)
+{
+    constexpr int PE = LB / static_cast<int>(sizeof(T));  // values of a piece
+    return Words<T, VB>::template piece_at<LB>(v, i / PE) / static_cast<int>(sizeof(T)) + i % PE;
+}
+// Vectors of a row: all lanes of the last warp where pieces are dealt.
+template <class T, int VB, int LB, bool DEALT>
+unsigned vectors(int H)
+{
+    constexpr unsigned EV = Words<T, VB>::N;
+    const unsigned n = H > 0 ? (static_cast<unsigned>(H) - 1) / EV + 1 : 0;
+    return DEALT && LB < VB ? (n + 31) / 32 * 32 : n;
+}
+
+template <class T, int VB, int LB, bool DEALT>
 __device__ __forceinline__ void load_weight(const Args &a, unsigned v, Words<T, VB> &w)
 {
     if (a.w != nullptr) {
-        w.template load<LB>(a.w + static_cast<long long>(v) * VB, bytes_left<T, VB>(a.H, v));
+        get<T, VB, LB, DEALT>(w, a.w, v, a.H);
     } else {
         float one[Words<T, VB>::N];
 #pragma unroll
@@ -79,6 +115,7 @@ template <class T, int VB, int LB, int OUT>
 __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
 {
     constexpr int EV = Words<T, VB>::N;
+    constexpr bool DEALT = OUT == kRow || OUT == kI8;
     __shared__ float part_sum[8];
     __shared__ unsigned part_max[8];
     dependent_release();
@@ -101,11 +138,9 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
             w[h].zero();
             t[h].zero();
             if (v < nvec) {
-                const long long at = static_cast<long long>(v) * VB;
-                const unsigned left = bytes_left<T, VB>(a.H, v);
-                s[h].template load<LB>(x + at, left);
-                if (a.res != nullptr) t[h].template load<LB>(res + at, left);
-                load_weight<T, VB, LB>(a, v, w[h]);
+                get<T, VB, LB, DEALT>(s[h], x, v, a.H);
+                if (a.res != nullptr) get<T, VB, LB, DEALT>(t[h], res, v, a.H);
+                load_weight<T, VB, LB, DEALT>(a, v, w[h]);
             }
         }
         if (a.res != nullptr)
@@ -129,25 +164,21 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
         const unsigned v = tx + h * nx;
         if (v < nvec) {
             gather(s[h], w[h]);
-            if (a.sum != nullptr)
-                s[h].template store<LB>(sum + static_cast<long long>(v) * VB,
-                                               bytes_left<T, VB>(a.H, v));
+            if (a.sum != nullptr) set<T, VB, LB, DEALT>(s[h], sum, v, a.H);
         }
     }
     // a vector of a long row's tail; again: in the second pass, when the sum, if
     // it is kept, may have taken the place of x or res
     auto tail = [&](unsigned v, bool again, Words<T, VB> &sv, Words<T, VB> &wv) {
-        const long long at = static_cast<long long>(v) * VB;
-        const unsigned left = bytes_left<T, VB>(a.H, v);
-        load_weight<T, VB, LB>(a, v, wv);
+        load_weight<T, VB, LB, DEALT>(a, v, wv);
         if (again && a.sum != nullptr) {
-            sv.template load<LB>(sum + at, left);
+            get<T, VB, LB, DEALT>(sv, sum, v, a.H);
             return;
         }
-        sv.template load<LB>(x + at, left);
+        get<T, VB, LB, DEALT>(sv, x, v, a.H);
         if (a.res != nullptr) {
             Words<T, VB> t;
-            t.template load<LB>(res + at, left);
+            get<T, VB, LB, DEALT>(t, res, v, a.H);
             add(sv, t);
         }
     };
@@ -155,9 +186,7 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
         Words<T, VB> sv, wv;
         tail(v, false, sv, wv);
         gather(sv, wv);
-        if (a.sum != nullptr)
-            sv.template store<LB>(sum + static_cast<long long>(v) * VB,
-                                         bytes_left<T, VB>(a.H, v));
+        if (a.sum != nullptr) set<T, VB, LB, DEALT>(sv, sum, v, a.H);
     }
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) square += __shfl_xor_sync(0xffffffffu, square, d);
@@ -188,8 +217,7 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
             for (int i = 0; i < EV; ++i) f[i] = f[i] * rho * g[i];
             Words<T, VB> o;
             o.pack(f);
-            o.template store<LB>(y + static_cast<long long>(v) * VB,
-                                        bytes_left<T, VB>(a.H, v));
+            set<T, VB, LB, DEALT>(o, y, v, a.H);
         };
 #pragma unroll
         for (int h = 0; h < kHeld; ++h)
@@ -214,8 +242,7 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
 #pragma unroll
             for (int i = 0; i < EV; ++i)
                 c[i] = some ? __float_as_uint(__fadd_rn(__fmul_rn(f[i] * g[i], inv), kRound)) : 0u;
-            const unsigned n = bytes_left<T, VB>(a.H, v) / static_cast<unsigned>(sizeof(T));
-            if (n == EV && a.sf_tiles != 0) {  // (8 bits: codes on boundaries of a vector's)
+            if (LB == VB && a.sf_tiles != 0) {  // (8 bits: codes on boundaries of a vector's)
 #pragma unroll
                 for (int i = 0; i < EV; i += 4)
                     c[i / 4] = __byte_perm(__byte_perm(c[i], c[i + 1], 0x0040),
@@ -226,9 +253,10 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
                     reinterpret_cast<uint32_t *>(q)[v] = c[0];
             } else {
 #pragma unroll
-                for (int i = 0; i < EV; ++i)
-                    if (static_cast<unsigned>(i) < n)
-                        q[static_cast<long long>(v) * EV + i] = static_cast<unsigned char>(c[i]);
+                for (int i = 0; i < EV; ++i) {
+                    const long long at = column<T, VB, LB>(v, i);
+                    if (at < a.H) q[at] = static_cast<unsigned char>(c[i]);
+                }
             }
         };
 #pragma unroll
@@ -277,11 +305,12 @@ struct Launch {
     template <class T, int LB, int OUT>
     int go() const
     {
-        // at least four values a vector: narrower loads make one up
-        constexpr int V4 = 4 * static_cast<int>(sizeof(T)), VB = LB > V4 ? LB : V4;
+        // narrower loads make up a vector of 16 bytes (4 bits: of four values)
+        constexpr int V4 = 4 * static_cast<int>(sizeof(T));
+        constexpr int VB = OUT == kRow || OUT == kI8 ? 16 : LB > V4 ? LB : V4;
         constexpr int EV = Words<T, VB>::N;
         Args a = args;
-        a.nvec = a.H > 0 ? (static_cast<unsigned>(a.H) - 1) / EV + 1 : 0;
+        a.nvec = vectors<T, VB, LB, OUT == kRow || OUT == kI8>(a.H);
         if (OUT == kI8) a.sf_tiles = rows::aligned_to(a.q, EV) && a.pq % EV == 0;
         const int held = a.M <= num_sms ? 1 : kHeld;  // few rows: more threads on each
         const int tx = rows::pow2_threads((a.nvec + held - 1) / held, 32, 256), ty = 256 / tx;
@@ -337,7 +366,7 @@ __global__ void __launch_bounds__(256, 2) grad_kernel(const GradArgs a)
     Words<T, VB> w[HELD];
     auto weight = [&](unsigned v, Words<T, VB> &wv) {
         if (a.w != nullptr) {
-            wv.template load<LB>(a.w + static_cast<long long>(v) * VB, bytes_left<T, VB>(a.H, v));
+            get<T, VB, LB, true>(wv, a.w, v, a.H);
         } else {
             float one[EV];
 #pragma unroll
@@ -367,11 +396,9 @@ __global__ void __launch_bounds__(256, 2) grad_kernel(const GradArgs a)
             g[h].zero();
             d[h].zero();
             if (r < a.M && v < a.nvec) {
-                const long long at = static_cast<long long>(v) * VB;
-                const unsigned left = bytes_left<T, VB>(a.H, v);
-                x[h].template load<LB>(a.s + r * a.ps + at, left);
-                g[h].template load<LB>(a.dy + r * a.pdy + at, left);
-                if (a.ds != nullptr) d[h].template load<LB>(a.ds + r * a.pds + at, left);
+                get<T, VB, LB, true>(x[h], a.s + r * a.ps, v, a.H);
+                get<T, VB, LB, true>(g[h], a.dy + r * a.pdy, v, a.H);
+                if (a.ds != nullptr) get<T, VB, LB, true>(d[h], a.ds + r * a.pds, v, a.H);
             }
         }
     };
@@ -405,11 +432,9 @@ __global__ void __launch_bounds__(256, 2) grad_kernel(const GradArgs a)
 #pragma unroll
         for (int h = 0; h < HELD; ++h) gather(sv[h], gv[h], w[h]);
         for (unsigned v = tx + HELD * nx; v < nvec; v += nx) {
-            const long long at = static_cast<long long>(v) * VB;
-            const unsigned left = bytes_left<T, VB>(a.H, v);
             Words<T, VB> x, g, wv;
-            x.template load<LB>(s + at, left);
-            g.template load<LB>(dy + at, left);
+            get<T, VB, LB, true>(x, s, v, a.H);
+            get<T, VB, LB, true>(g, dy, v, a.H);
             weight(v, wv);
             gather(x, g, wv);
         }
@@ -450,8 +475,7 @@ __global__ void __launch_bounds__(256, 2) grad_kernel(const GradArgs a)
             }
             Words<T, VB> o;
             o.pack(f);
-            o.template store<LB>(dx + static_cast<long long>(v) * VB,
-                                        bytes_left<T, VB>(a.H, v));
+            set<T, VB, LB, true>(o, dx, v, a.H);
         };
 #pragma unroll
         for (int h = 0; h < HELD; ++h) {
@@ -468,23 +492,20 @@ __global__ void __launch_bounds__(256, 2) grad_kernel(const GradArgs a)
                 for (int i = 0; i < EV; ++i) acc[h][i] = fmaf(dyx[i], rho, acc[h][i]);
             }
         for (unsigned v = tx + HELD * nx; v < nvec; v += nx) {
-            const long long at = static_cast<long long>(v) * VB;
-            const unsigned left = bytes_left<T, VB>(a.H, v);
             Words<T, VB> x, g, wv, d;
-            x.template load<LB>(s + at, left);
-            g.template load<LB>(dy + at, left);
+            get<T, VB, LB, true>(x, s, v, a.H);
+            get<T, VB, LB, true>(g, dy, v, a.H);
             d.zero();
-            if (a.ds != nullptr) d.template load<LB>(ds + at, left);
+            if (a.ds != nullptr) get<T, VB, LB, true>(d, ds, v, a.H);
             weight(v, wv);
             float dyx[EV];
             put(v, x, g, wv, d, dyx);
             if (a.part != nullptr) {  // (a row of its own: one group here)
-                const unsigned e = left / static_cast<unsigned>(sizeof(T));
-                float *to = mine + static_cast<long long>(v) * EV;
 #pragma unroll
-                for (int i = 0; i < EV; ++i)
-                    if (static_cast<unsigned>(i) < e)
-                        to[i] = fmaf(dyx[i], rho, turn > 0 ? to[i] : 0.f);
+                for (int i = 0; i < EV; ++i) {
+                    const long long at = column<T, VB, LB>(v, i);
+                    if (at < a.H) mine[at] = fmaf(dyx[i], rho, turn > 0 ? mine[at] : 0.f);
+                }
             }
         }
         if (AHEAD)
@@ -519,9 +540,10 @@ __global__ void __launch_bounds__(256, 2) grad_kernel(const GradArgs a)
         for (int h = 0; h < HELD; ++h) {
             const unsigned v = tx + h * nx;
 #pragma unroll
-            for (int i = 0; i < EV; ++i)
-                if (v < a.nvec && v * EV + i < static_cast<unsigned>(a.H))
-                    mine[static_cast<long long>(v) * EV + i] = acc[h][i];
+            for (int i = 0; i < EV; ++i) {
+                const long long at = column<T, VB, LB>(v, i);
+                if (v < a.nvec && at < a.H) mine[at] = acc[h][i];
+            }
         }
 }
 
@@ -573,10 +595,9 @@ struct GradLaunch {
     template <class T, int LB>
     int run() const
     {
-        constexpr int V4 = 4 * static_cast<int>(sizeof(T)), VB = LB > V4 ? LB : V4;
-        constexpr int EV = Words<T, VB>::N;
+        constexpr int VB = 16;
         GradArgs a = args;
-        a.nvec = (static_cast<unsigned>(a.H) - 1) / EV + 1;
+        a.nvec = vectors<T, VB, LB, true>(a.H);
         int parts = 0;
         if (a.M > 0) {
             const int st_ = a.nvec <= 512 ? rows_pass<T, VB, LB, 2>(a, parts)

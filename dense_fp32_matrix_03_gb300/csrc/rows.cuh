@@ -192,6 +192,59 @@ struct Words {
             }
         }
     }
+    // The warp's vectors together (lane l's is vector v of the row, v - l a multiple
+    // of 32), narrow pieces dealt to the lanes in turn: every access of the warp is
+    // one run of bytes.  Piece i of vector v is then at piece_at(v, i); LB == VB is
+    // vector v itself.  Zeros past the row's `bytes`.
+    template <int LB>
+    static __device__ __forceinline__ long long piece_at(unsigned v, int i)
+    {
+        return static_cast<long long>(v & ~31u) * VB + (i * 32 + static_cast<int>(v & 31u)) * LB;
+    }
+    template <int LB>
+    __device__ __forceinline__ void load_dealt(const char *row, unsigned v, long long bytes)
+    {
+        if constexpr (LB == VB) {
+            load<LB>(row + static_cast<long long>(v) * VB, VB);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VB / LB; ++i) {
+                const long long at = piece_at<LB>(v, i);
+                const bool in = at < bytes;
+                if constexpr (LB == 8) {
+                    uint2 x = make_uint2(0u, 0u);
+                    if (in) x = *reinterpret_cast<const uint2 *>(row + at);
+                    w[2 * i] = x.x;
+                    w[2 * i + 1] = x.y;
+                } else if constexpr (LB == 4) {
+                    w[i] = in ? *reinterpret_cast<const uint32_t *>(row + at) : 0u;
+                } else {
+                    const uint32_t x = in ? *reinterpret_cast<const uint16_t *>(row + at) : 0u;
+                    w[i / 2] = i % 2 ? w[i / 2] | x << 16 : x;
+                }
+            }
+        }
+    }
+    template <int LB>
+    __device__ __forceinline__ void store_dealt(char *row, unsigned v, long long bytes) const
+    {
+        if constexpr (LB == VB) {
+            store<LB>(row + static_cast<long long>(v) * VB, VB);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VB / LB; ++i) {
+                const long long at = piece_at<LB>(v, i);
+                if (at >= bytes) continue;
+                if constexpr (LB == 8)
+                    *reinterpret_cast<uint2 *>(row + at) = make_uint2(w[2 * i], w[2 * i + 1]);
+                else if constexpr (LB == 4)
+                    *reinterpret_cast<uint32_t *>(row + at) = w[i];
+                else
+                    *reinterpret_cast<uint16_t *>(row + at) =
+                        static_cast<uint16_t>(i % 2 ? w[i / 2] >> 16 : w[i / 2]);
+            }
+        }
+    }
     // From here on unpacked anew: keeps the compiler from holding the values as
     // floats, twice the registers, over a wait.
     __device__ __forceinline__ void forget()
