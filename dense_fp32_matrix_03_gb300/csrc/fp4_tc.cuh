@@ -22,12 +22,12 @@
 // the epilogue reads the 64 columns that hold the overlap before all others; the
 // next tile's MMAs wait for that, not for the whole accumulator.
 //
-// Warps: 0 TMA producer, 1 tensor memory and MMA issuer, 2-3 idle, then the
-// epilogue (tensor memory -> scales -> result type -> staging -> C).  Every wait
+// Warps: 0 TMA producer, 1 tensor memory and MMA issuer, 2 idle, 3 asks L2 for the
+// first weights (one CTA), then the epilogue (tensor memory -> scales -> result type -> staging -> C).  Every wait
 // is bounded.
 //
-// Measured on GB300, bf16 results: 8192 x 8192 x 4096 96 us (NV, 5700 TFLOP/s), x 8192
-// 179 (MX 176), 4096^3 29, 1024 x 4096 x 4096 11.3; narrow 128 x 4096 x 4096 8.2; slim
+// Measured on GB300, bf16 results: 8192 x 8192 x 4096 96 to 103 us (NV, 5300 to 5700
+// TFLOP/s, by box), x 8192 179 (MX 176), 4096^3 29, 1024 x 4096 x 4096 11.3; narrow 128 x 4096 x 4096 8.2; slim
 // 1 to 32 tokens x 4096 x 4096 5.8 to 6.4.  What bounds the wide form: at 8192^3 the
 // multiplies alone take 135 us and the loads alone 134 (19 TB/s out of L2, all five
 // stages on their way); together they share the multiprocessor's memory.  Four
