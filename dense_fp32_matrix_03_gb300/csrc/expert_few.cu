@@ -19,11 +19,11 @@
 // without registers or barriers.
 //
 // Measured on GB300, both kernels: one token, 4 of 32 experts of 2048 x 2048, 8 bits
-// (fp16 rows) 18.8 us (their 50 MB take 7.4), 16 bits 24.6; 16 tokens, 4 of 32 experts of
-// 2048 x 1024, 16 bits 62 (4.4 TB/s), 8 bits 48; 32 tokens, 4 of 64, 8 bits 97.  Few
+// (fp16 rows) 18.7 us (their 50 MB take 7.4), 16 bits 24.6; 16 tokens, 4 of 32 experts of
+// 2048 x 1024, 16 bits 66 (3.9 TB/s), 8 bits 54; 32 tokens, 4 of 64, 8 bits 126.  Few
 // tokens are bound by latency: ids, weights and sums in sequence, twice; more by
 // the loads in flight and, in 8 bits, by widening: weights are widened once for
-// each eight tokens of an expert.
+// each eight tokens of an expert (down: four, in two columns each).
 #include <type_traits>
 
 #include "../../include/expert_layer.h"
@@ -50,7 +50,7 @@ struct Args {
     const float *scale1, *scale2;
     void *out;
     long long ldo;
-    void *h;       // T * k rows of ldh values
+    void *h;       // T * k pairs of rows of ldh values: h rounded, and what that left
     long long ldh;
 };
 
@@ -534,9 +534,13 @@ __global__ void __launch_bounds__(kUpWarps * 32, Up<T, I8, NF>::BLOCKS) up_kerne
                 gate *= sg;
                 up *= su;
             }
-            // (values past F are zeros: gate is)
-            static_cast<T *>(a.h)[c.choice[r0 + m] * a.ldh + f0 + f] =
-                rows::from_f<T>(gate / (1.f + expf(-gate)) * up);
+            // (values past F are zeros: gate is; what an infinity leaves is nothing)
+            const float h = gate / (1.f + expf(-gate)) * up;
+            const T hi = rows::from_f<T>(h);
+            const float back = rows::to_f<T>(hi);
+            T *to = static_cast<T *>(a.h) + 2 * c.choice[r0 + m] * a.ldh + f0 + f;
+            to[0] = hi;
+            to[a.ldh] = rows::from_f<T>(isfinite(back) ? h - back : 0.f);
         }
     }
 }
@@ -544,32 +548,38 @@ __global__ void __launch_bounds__(kUpWarps * 32, Up<T, I8, NF>::BLOCKS) up_kerne
 // -------------------------------------------------------------------- down
 
 // (eight warps with twice the steps on their way: 16 tokens 69 us instead of 61)
-constexpr int kDownWarps = 16, kDownDepth = 3;
+// (sixteen groups of columns: their sums take the registers of half the threads)
+template <int NF>
+constexpr int kDownWarps = NF <= 8 ? 16 : 8;
+constexpr int kDownDepth = 3;
 
 // grid: 16 channels of out.  The steps of all used experts form one list, a
 // part of which is each warp's; a warp adds an expert's results, weighted, to
-// sums of its own, and the block adds those in the warps' order.
+// sums of its own, and the block adds those in the warps' order.  The two parts of
+// a row of h are neighbouring columns of the matrix unit, whose results one lane
+// holds: up to four tokens of an expert cost no more than their columns.
 template <class T, bool I8, int NF>
-__global__ void __launch_bounds__(kDownWarps * 32, 1) down_kernel(const Args a)
+__global__ void __launch_bounds__(kDownWarps<NF> * 32, 1) down_kernel(const Args a)
 {
+    constexpr int WARPS = kDownWarps<NF>;
     using W = Weights<T, I8>;
     using P = Pieces<T, I8, 1, kDownDepth>;
     __shared__ Choices c;
     extern __shared__ __align__(16) unsigned char dyn[];  // the rings, [warp][token][channel] sums
-    float *sums = reinterpret_cast<float *>(dyn + kDownWarps * P::BYTES);  // rows of kCh + 1
+    float *sums = reinterpret_cast<float *>(dyn + WARPS * P::BYTES);  // rows of kCh + 1
     dependent_release();
     // The up kernel releases its dependents after its own wait, so what it found
     // complete, ids and weights among it, is complete here too, and is read while
     // it still runs.  (F == 0: there is no up kernel.)
     if (a.F == 0) dependent_wait();
-    find_choices<kDownWarps>(a, c);
+    find_choices<WARPS>(a, c);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int h0 = blockIdx.x * kCh;
     float *mine = sums + static_cast<long long>(warp) * a.T * (kCh + 1);
     for (int i = lane; i < a.T * (kCh + 1); i += 32) mine[i] = 0.f;
     const int steps = (a.F + W::STEP - 1) / W::STEP, total = c.used * steps;
-    int at = static_cast<int>(static_cast<long long>(total) * warp / kDownWarps);
-    const int end = static_cast<int>(static_cast<long long>(total) * (warp + 1) / kDownWarps);
+    int at = static_cast<int>(static_cast<long long>(total) * warp / WARPS);
+    const int end = static_cast<int>(static_cast<long long>(total) * (warp + 1) / WARPS);
     P ring(dyn, warp, lane);
     // the step asked for next: expert au, its rows, step as
     int ask = at, au = steps > 0 ? at / steps : 0, as = at - au * steps;
@@ -609,7 +619,8 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) down_kernel(const Args a)
 #pragma unroll
         for (int i = 0; i < NF; ++i)
             trow[i] = static_cast<const char *>(a.h) +
-                      c.choice[r0 + min(8 * i + g, n - 1)] * a.ldh * 2 + 2 * W::N * t;
+                      (2 * c.choice[r0 + min(4 * i + g / 2, n - 1)] + (g & 1)) * a.ldh * 2 +
+                      2 * W::N * t;
         float acc[1][NF][4] = {};
         uint4 x[2][W::TOK];
         load_step<T, I8, true>(x, trow[0], lo * W::STEP, a.F, t);
@@ -619,7 +630,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) down_kernel(const Args a)
             P::arrived();
             ring.take(slot, w);
             ask_next(slot);
-            multiply<T, I8, 1, NF, true>(acc, w, x, trow, s * W::STEP, a.F, t, n);
+            multiply<T, I8, 1, NF, true>(acc, w, x, trow, s * W::STEP, a.F, t, 2 * n);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -627,34 +638,38 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) down_kernel(const Args a)
             slot = slot + 1 == kDownDepth ? 0 : slot + 1;
         }
 #pragma unroll
-        for (int m = 0; m < NF; ++m)
+        for (int m = 0; m < NF; ++m) {
+            const int row = 4 * m + t;
+            if (row < n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int col = 8 * m + 2 * t + (j & 1);
-                if (col < n)
-                    mine[c.token[r0 + col] * (kCh + 1) + 8 * (j >> 1) + g] +=
-                        c.weight[r0 + col] * (scale[j >> 1] * acc[0][m][j]);
-            }
+                for (int r = 0; r < 2; ++r)
+                    mine[c.token[r0 + row] * (kCh + 1) + 8 * r + g] +=
+                        c.weight[r0 + row] *
+                        (scale[r] * (acc[0][m][2 * r] + acc[0][m][2 * r + 1]));
+        }
         __syncwarp();
         at += hi - lo;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.T * kCh; i += kDownWarps * 32) {
+    for (int i = threadIdx.x; i < a.T * kCh; i += WARPS * 32) {
         const int m = i / kCh, ch = i % kCh;
         if (h0 + ch >= a.H) continue;
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kDownWarps; ++w) s += sums[(w * a.T + m) * (kCh + 1) + ch];
+        for (int w = 0; w < WARPS; ++w) s += sums[(w * a.T + m) * (kCh + 1) + ch];
         static_cast<T *>(a.out)[m * a.ldo + h0 + ch] = rows::from_f<T>(s);
     }
 }
 
+// NF: groups of eight tokens (up) and of four tokens' two columns (down: twice as
+// many).
 template <class T, bool I8, int NF>
 int launch(const Args &a, bool x_vec, int num_sms, cudaStream_t st)
 {
     if (a.F > 0) {
-        using U = Up<T, I8, NF>;
-        auto kern = x_vec ? up_kernel<T, I8, NF, true> : up_kernel<T, I8, NF, false>;
+        constexpr int UF = NF > 1 ? NF / 2 : 1;
+        using U = Up<T, I8, UF>;
+        auto kern = x_vec ? up_kernel<T, I8, UF, true> : up_kernel<T, I8, UF, false>;
         if (!smem_attr_once(reinterpret_cast<const void *>(kern), U::SMEM)) return SGEMM_ERR_LAUNCH;
         const long long rows_ = static_cast<long long>(a.T) * a.k;
         const long long units = (a.E < rows_ ? a.E : rows_) * ((a.F + kCh - 1) / kCh);
@@ -663,23 +678,24 @@ int launch(const Args &a, bool x_vec, int num_sms, cudaStream_t st)
                                        dim3(kUpWarps * 32), U::SMEM, 1, st, a);
         if (s != SGEMM_OK) return s;
     }
-    constexpr int ring = kDownWarps * Pieces<T, I8, 1, kDownDepth>::BYTES;
-    constexpr int per_token = static_cast<int>(sizeof(float)) * kDownWarps * (kCh + 1);
+    constexpr int WARPS = kDownWarps<NF>;
+    constexpr int ring = WARPS * Pieces<T, I8, 1, kDownDepth>::BYTES;
+    constexpr int per_token = static_cast<int>(sizeof(float)) * WARPS * (kCh + 1);
     auto kern = down_kernel<T, I8, NF>;
-    if (!smem_attr_once(reinterpret_cast<const void *>(kern), ring + per_token * 8 * NF))
+    if (!smem_attr_once(reinterpret_cast<const void *>(kern), ring + per_token * 4 * NF))
         return SGEMM_ERR_LAUNCH;
     return launch_dependent(kern, dim3(static_cast<unsigned>((a.H + kCh - 1) / kCh)),
-                            dim3(kDownWarps * 32), static_cast<size_t>(ring + per_token * a.T), 1, st,
-                            a);
+                            dim3(WARPS * 32), static_cast<size_t>(ring + per_token * a.T), 1, st, a);
 }
 
 template <class T, bool I8>
 int run(const Args &a, bool x_vec, int num_sms, cudaStream_t st)
 {
-    if (a.T <= 8) return launch<T, I8, 1>(a, x_vec, num_sms, st);
-    if (a.T <= 16) return launch<T, I8, 2>(a, x_vec, num_sms, st);
-    if (a.T <= 32) return launch<T, I8, 4>(a, x_vec, num_sms, st);
-    return launch<T, I8, 8>(a, x_vec, num_sms, st);
+    if (a.T <= 4) return launch<T, I8, 1>(a, x_vec, num_sms, st);
+    if (a.T <= 8) return launch<T, I8, 2>(a, x_vec, num_sms, st);
+    if (a.T <= 16) return launch<T, I8, 4>(a, x_vec, num_sms, st);
+    if (a.T <= 32) return launch<T, I8, 8>(a, x_vec, num_sms, st);
+    return launch<T, I8, 16>(a, x_vec, num_sms, st);
 }
 
 bool sizes_ok(int T, int k, int H, int F)
@@ -700,7 +716,7 @@ extern "C" {
 size_t sgemm_experts_layer_workspace_size(int T, int k, int H, int F)
 {
     if (!few::sizes_ok(T, k, H, F)) return 0;
-    return static_cast<size_t>(T) * k * static_cast<size_t>(few::row_of_h(F)) * 2;
+    return static_cast<size_t>(T) * k * static_cast<size_t>(few::row_of_h(F)) * 2 * 2;
 }
 
 int sgemm_experts_layer(int type, int wtype, int T, int k, int E, int H, int F, const void *x,

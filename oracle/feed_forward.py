@@ -176,7 +176,8 @@ def product4(a, sa, b, sb):
 
 def experts_layer(x, ids, weights, W1, s1, W2, s2, u):
     """(out, error bound without out's own rounding) of the layer; u: half a
-    unit in the last place of h's type, e: of a fp32 operation."""
+    unit in the last place of the row type, in which h is kept as a rounded value
+    and the rounded rest; e: of a fp32 operation."""
     T, k = ids.shape
     E, F2, H = W1.shape
     F = F2 // 2
@@ -195,7 +196,7 @@ def experts_layer(x, ids, weights, W1, s1, W2, s2, u):
             silu = g / (1 + np.exp(-g))
             h = silu * up
             # |silu'| <= 1.1; fp32 sums of H terms, a few operations for silu
-            dh = u * np.abs(h) + e24 * ((H + 16) * (1.1 * gm * np.abs(up) + np.abs(silu) * um) +
+            dh = u * u * np.abs(h) + e24 * ((H + 16) * (1.1 * gm * np.abs(up) + np.abs(silu) * um) +
                                         8 * np.abs(h)) + 2.0 ** -24
             wt = 1.0 if weights is None else float(weights[t, j])
             out[t] += wt * (w2 @ h)

@@ -31,7 +31,7 @@ SPECS = {
     "sgemm_experts_layer": dict(type_=0, wtype=0, T=4, k=2, E=3, H=16, F=32, x=FAKE, ldx=16,
                                 ids=FAKE, weights=FAKE, W1=FAKE, ld1=16, stride1=64 * 16,
                                 scale1=FAKE, W2=FAKE, ld2=32, stride2=16 * 32, scale2=FAKE,
-                                out=FAKE, ldo=16, workspace=FAKE, workspace_bytes=8 * 32 * 2),
+                                out=FAKE, ldo=16, workspace=FAKE, workspace_bytes=8 * 32 * 4),
 }
 NORMS = ["sgemm_rms_norm", "sgemm_rms_norm_i8", "sgemm_rms_norm_fp4"]
 
@@ -78,7 +78,7 @@ BAD = [
         dict(ld2=40), dict(stride1=64 * 16 - 16), dict(stride2=16 * 32 - 16),
         dict(stride1=64 * 16 + 8), dict(stride2=-16), dict(x=0), dict(ids=0), dict(out=0),
         dict(W1=0), dict(W2=0), dict(scale1=0), dict(scale2=0), dict(workspace=0),
-        dict(workspace_bytes=511), dict(x=FAKE + 1), dict(out=FAKE + 1), dict(ids=FAKE + 2),
+        dict(workspace_bytes=1023), dict(x=FAKE + 1), dict(out=FAKE + 1), dict(ids=FAKE + 2),
         dict(weights=FAKE + 2), dict(W1=FAKE + 8), dict(W2=FAKE + 8), dict(scale1=FAKE + 2),
         dict(workspace=FAKE + 8), dict(H=65537, ldx=65537, ldo=65537))],
 ]
@@ -114,7 +114,7 @@ def test_sizes(lib):
     assert lib.sgemm_rms_norm_grad_workspace_size(4, 8) == 4 * 8 * 4
     assert lib.sgemm_rms_norm_grad_workspace_size(10 ** 6, 8) == 608 * 8 * 4
     assert lib.sgemm_rms_norm_grad_workspace_size(-1, 8) == 0
-    assert lib.sgemm_experts_layer_workspace_size(4, 2, 16, 33) == 8 * 48 * 2
+    assert lib.sgemm_experts_layer_workspace_size(4, 2, 16, 33) == 8 * 48 * 4
     assert lib.sgemm_experts_layer_workspace_size(65, 1, 16, 16) == 0
 
 

@@ -1,7 +1,7 @@
 """GPU parity of the whole expert layer for a few tokens
 (sgemm_experts_layer, include/expert_layer.h) against the oracle
 (oracle/feed_forward.py), element by element, through the C ABI.  The bound is
-the oracle's (h rounded to the row type, fp32 sums) plus out's own rounding."""
+the oracle's (h kept in two parts of the row type, fp32 sums) plus out's own rounding."""
 import numpy as np
 import pytest
 
