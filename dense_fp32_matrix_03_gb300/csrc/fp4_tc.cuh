@@ -424,6 +424,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const int n = min(j.n - col0, C::ECOLS);
             float sb[4] = {};  // 16 bits: channels lane / 4 + 8 i; else channel lane
             if (split == 1) {
+                __syncwarp();  // the last tile's readers of sa are done (its stores may diverge)
                 for (int i = lane; i < C::ECOLS; i += 32)
                     sa[i] = i < n ? (a.scaleA != nullptr ? a.scaleA[j.row0 + col0 + i] : 1.f) : 0.f;
 #pragma unroll
