@@ -95,21 +95,6 @@ using Slim = Cfg<1, 32, 8, 4, 128>;
 using Narrow = Cfg<1, 128, 5, 4, 512>;
 using Wide = Cfg<2, 256, 5, 8, 512>;
 
-// As tcs::tma_load_pair, to the same place of both CTAs of the pair.  (Two pairs
-// that shared their tokens this way too moved a quarter fewer bytes in the same
-// time a stage, and 36 clusters of four leave eight multiprocessors idle.)
-__device__ __forceinline__ void tma_load_both(void *smem_dst, const CUtensorMap *m, uint32_t bar,
-                                              int c0, int c1, int c2)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".multicast::cluster.cta_group::2 [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(
-            smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-}
-
 // A copy's source: 32 rows of 16 bytes without swizzle, eight rows 128 bytes
 // apart from the next eight.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr)
@@ -308,10 +293,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         tcs::tma_load_pair(st, &tmW, fb, ks * 128, j.ch0, 0);
                         tcs::tma_load_pair(st + C::OFF_T, &tmT, fb, ks * 128, first, 0);
                         tcs::tma_load_pair(st + C::OFF_SW, &tmSW, fb, 0, ks * TILES, j.ch0 / kTileRows);
-                        // both CTAs need all tokens' scales: each loads a row block
-                        tma_load_both(st + C::OFF_ST + static_cast<int>(half) * TILES * kTileBytes,
-                                      &tmST, fb, 0, ks * TILES,
-                                      static_cast<int>(j.row0 / kTileRows) + static_cast<int>(half));
+                        // both CTAs need all tokens' scales
+#pragma unroll
+                        for (int b = 0; b < C::RB; ++b)
+                            tcs::tma_load_pair(st + C::OFF_ST + b * TILES * kTileBytes, &tmST, fb, 0,
+                                               ks * TILES, static_cast<int>(j.row0 / kTileRows) + b);
                     } else {
                         mbar_arrive_expect_tx(&full[rr.s], BYTES);
                         tma_load_3d(st, &tmW, &full[rr.s], ks * 128, j.ch0, 0);
