@@ -68,6 +68,9 @@ size_t sgemm_fp4_scales_size(int format, int rows, int K);
  *       scale e4m3(amax * (448 / a_r)) to nearest
  * Codes are the nearest 4-bit value of x times the scales' inverse, in fp32,
  * ties to the even code, 6 beyond 6.
+ * The gated activation is held in fp32, each value within 8 units of fp32's last
+ * place (gates below -87, whose exponential is subnormal: 2^-141 |X[r][K + k]|
+ * besides).
  *  - NV: a row whose largest magnitude is below 2^-100 (zeros among them) gets
  *    row scale 0, block scales 0 and codes 0.
  *  - A row that holds an infinity or NaN, or whose gated activation leaves
