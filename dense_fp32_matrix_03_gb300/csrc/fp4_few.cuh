@@ -11,7 +11,8 @@
 // a fraction of their rate: decoded by it and multiplied by mma.sync, one token
 // through 4096 x 4096 took 7.9 us.)  Packed fp16 FMAs add the products of 16
 // values exactly: each half of the sum takes eight, at most 1152 units of a
-// quarter's product.  Then it is fp32: a block's two halves times both block scales.
+// quarter's product.  Then it is fp32: a block's two halves times both block scales
+// (MX: in two steps).
 //
 // A warp takes four channels 32 apart, whose scales for 64 values are 16
 // consecutive bytes of the layout, and 1024 k a step, 32 a lane.  The warps of a
@@ -79,8 +80,10 @@ __device__ __forceinline__ void decode8(uint32_t w, __half2 (&h)[4])
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const __half2 *>(&r[i]);
 }
-// The scales of the two 16-value halves of 32 values from k on, out of the word of
-// four blocks that holds them.
+// The scales of 32 values from k on, out of the word of four blocks that holds them.
+// NV: of its two halves of 16 values.  MX: one scale 2^e as two factors 2^(e / 2),
+// rounded down and up, so that products of two operands' factors keep within fp32
+// where the product of the scales does not (2^70 twice, times a code that is zero).
 template <int FORMAT>
 __device__ __forceinline__ float2 scales_of(uint32_t word, int k)
 {
@@ -89,9 +92,9 @@ __device__ __forceinline__ float2 scales_of(uint32_t word, int k)
             static_cast<__nv_fp8x2_storage_t>(word >> (k % 64 / 2)), __NV_E4M3);
         return __half22float2(__half2(h));
     }
-    const uint32_t b = word >> (k % 128 / 4) & 255u;
-    const float s = __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7FC00000u : b << 23);
-    return make_float2(s, s);
+    const uint32_t b = word >> (k % 128 / 4) & 255u;  // e + 127
+    return make_float2(__uint_as_float(b == 255u ? 0x7FC00000u : (b + 127u) >> 1 << 23),
+                       __uint_as_float((b + 128u) >> 1 << 23));
 }
 constexpr int word_k(int format) { return kTileBlocks * (format == SGEMM_FP4_MX ? 32 : 16); }
 
@@ -171,8 +174,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, MT == 1 ? 6 : MT == 2 ? 5 : 3)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s = __hfma2(g[i], xv[m][4 + i], s);
                     const float2 f = __half22float2(s);
-                    const float sc = (b ? sw[c].y : sw[c].x) * (b ? sx[m].y : sx[m].x);
-                    acc[m][c] = fmaf(f.x + f.y, sc, acc[m][c]);
+                    if (FORMAT == SGEMM_FP4_NV) {
+                        const float sc = (b ? sw[c].y : sw[c].x) * (b ? sx[m].y : sx[m].x);
+                        acc[m][c] = fmaf(f.x + f.y, sc, acc[m][c]);
+                    } else {
+                        // (exact but for the sum, as all are powers of two of some 2^-127 to
+                        // 2^127; where the first product leaves fp32, the second would)
+                        acc[m][c] = fmaf((f.x + f.y) * (sw[c].x * sx[m].y), sw[c].y * sx[m].x,
+                                         acc[m][c]);
+                    }
                 }
             }
         }
