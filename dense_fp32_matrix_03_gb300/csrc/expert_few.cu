@@ -50,9 +50,14 @@ struct Args {
     const float *scale1, *scale2;
     void *out;
     long long ldo;
-    void *h;       // T * k pairs of rows of ldh values: h rounded, and what that left
+    void *h;       // T * k pairs of rows of ldh values: h rounded, and what that left, kRestUp times
     long long ldh;
 };
+
+// What h's rounding to T leaves is kept times this.  In fp16 the rest of an h near
+// 2^-14 would be below the least number; 2^11 times it is at most h itself.
+template <class T>
+constexpr float kRestUp = std::is_same<T, __half>::value ? 2048.f : 1.f;
 
 // The chosen experts in ascending order and, for each, its tokens in ascending
 // order.  A token that chose an expert more than once is one row, whose weight
@@ -540,7 +545,7 @@ __global__ void __launch_bounds__(kUpWarps * 32, Up<T, I8, NF>::BLOCKS) up_kerne
             const float back = rows::to_f<T>(hi);
             T *to = static_cast<T *>(a.h) + 2 * c.choice[r0 + m] * a.ldh + f0 + f;
             to[0] = hi;
-            to[a.ldh] = rows::from_f<T>(isfinite(back) ? h - back : 0.f);
+            to[a.ldh] = rows::from_f<T>(isfinite(back) ? (h - back) * kRestUp<T> : 0.f);
         }
     }
 }
@@ -645,7 +650,8 @@ __global__ void __launch_bounds__(kDownWarps<NF> * 32, 1) down_kernel(const Args
                 for (int r = 0; r < 2; ++r)
                     mine[c.token[r0 + row] * (kCh + 1) + 8 * r + g] +=
                         c.weight[r0 + row] *
-                        (scale[r] * (acc[0][m][2 * r] + acc[0][m][2 * r + 1]));
+                        (scale[r] *
+                         fmaf(acc[0][m][2 * r + 1], 1.f / kRestUp<T>, acc[0][m][2 * r]));
         }
         __syncwarp();
         at += hi - lo;

@@ -95,9 +95,9 @@ int sgemm_experts_combine_grad(int type, int T, int k, int E, int H, const void 
  * an expert twice); weights: T x k fp32, NULL means 1 everywhere.  Rows of W1
  * and W2 start on 16-byte boundaries (bases, leading dimensions and strides).
  * T * k <= 512, H and F <= 65536.
- * Products are exact where weights are 8-bit; sums are fp32; h is kept as the
- * sum of two values of the row type between the products (an fp16 h beyond 65504
- * is an infinity);
+ * Products are exact where weights are 8-bit; sums are fp32; h is kept in two
+ * values of the row type between the products, to twice its digits (fp16: to
+ * 2^-36 at the least, and an h beyond 65504 is an infinity);
  * out is summed over the experts in fp32, in an order fixed by ids and the
  * sizes, and rounded once.  Only experts that a kept choice names are read.  A
  * token without kept choices gets zeros.  out may not overlap x.

@@ -174,10 +174,11 @@ def product4(a, sa, b, sb):
 
 # ------------------------------------------------------- few-token expert layer
 
-def experts_layer(x, ids, weights, W1, s1, W2, s2, u):
+def experts_layer(x, ids, weights, W1, s1, W2, s2, u, least=2.0 ** -24):
     """(out, error bound without out's own rounding) of the layer; u: half a
     unit in the last place of the row type, in which h is kept as a rounded value
-    and the rounded rest; e: of a fp32 operation."""
+    and the rounded rest; e: of a fp32 operation; least: what h may be off by however
+    small it is."""
     T, k = ids.shape
     E, F2, H = W1.shape
     F = F2 // 2
@@ -197,7 +198,7 @@ def experts_layer(x, ids, weights, W1, s1, W2, s2, u):
             h = silu * up
             # |silu'| <= 1.1; fp32 sums of H terms, a few operations for silu
             dh = u * u * np.abs(h) + e24 * ((H + 16) * (1.1 * gm * np.abs(up) + np.abs(silu) * um) +
-                                        8 * np.abs(h)) + 2.0 ** -24
+                                        8 * np.abs(h)) + least
             wt = 1.0 if weights is None else float(weights[t, j])
             out[t] += wt * (w2 @ h)
             err[t] += abs(wt) * (np.abs(w2) @ (dh + e24 * (F + k + 16) * np.abs(h)))
