@@ -558,8 +558,40 @@ template <int NF>
 constexpr int kDownWarps = NF <= 8 ? 16 : 8;
 constexpr int kDownDepth = 3;
 
+// The list of all used experts' steps, cut into `parts` of equal work: the first
+// step of part w.  A step's work is its weights and its expert's rows (two columns
+// of the matrix unit each), the weights' counted as kStepRows rows; the work before
+// expert u is then steps (first[u] + kStepRows u).  (Cut into equal numbers of steps,
+// the warp with a much-chosen expert is what the block waits for: 64 tokens, 2 of 8
+// experts of 4096 x 2048, the fullest with 50, 8 bits 219 us, so 150; 16 bits 380 and
+// 244.  With weights counted as 8 rows 156 and 258.)  Up to four tokens are one group
+// of columns: equal numbers of steps.
+constexpr int kStepRows = 4;
+static_assert((kMaxSide / 64) * (kMaxRows + kStepRows * kMaxRows) < 0x7FFFFFFF / 16, "ints of work");
+template <int NF>
+__device__ __forceinline__ int first_step(const Choices &c, int steps, int w, int parts)
+{
+    const unsigned all = static_cast<unsigned>(c.used) * static_cast<unsigned>(steps);
+    if (NF == 1 || w == parts) return static_cast<int>(all * w / parts);
+    auto before = [&](int u) {
+        return static_cast<unsigned>(steps) * static_cast<unsigned>(c.first[u] + kStepRows * u);
+    };
+    const unsigned goal = before(c.used) * w / parts;
+    int u = 0, past = c.used;  // before(u) <= goal, and < before(past) where there are steps
+    while (past - u > 1) {
+        const int mid = (u + past) / 2;
+        if (before(mid) <= goal)
+            u = mid;
+        else
+            past = mid;
+    }
+    if (all == 0u) return 0;
+    return u * steps + static_cast<int>((goal - before(u)) /
+                                        static_cast<unsigned>(c.first[u + 1] - c.first[u] + kStepRows));
+}
+
 // grid: 16 channels of out.  The steps of all used experts form one list, a
-// part of which is each warp's; a warp adds an expert's results, weighted, to
+// part of which, by work, is each warp's; a warp adds an expert's results, weighted, to
 // sums of its own, and the block adds those in the warps' order.  The two parts of
 // a row of h are neighbouring columns of the matrix unit, whose results one lane
 // holds: up to four tokens of an expert cost no more than their columns.
@@ -582,9 +614,9 @@ __global__ void __launch_bounds__(kDownWarps<NF> * 32, 1) down_kernel(const Args
     const int h0 = blockIdx.x * kCh;
     float *mine = sums + static_cast<long long>(warp) * a.T * (kCh + 1);
     for (int i = lane; i < a.T * (kCh + 1); i += 32) mine[i] = 0.f;
-    const int steps = (a.F + W::STEP - 1) / W::STEP, total = c.used * steps;
-    int at = static_cast<int>(static_cast<long long>(total) * warp / WARPS);
-    const int end = static_cast<int>(static_cast<long long>(total) * (warp + 1) / WARPS);
+    const int steps = (a.F + W::STEP - 1) / W::STEP;
+    int at = first_step<NF>(c, steps, warp, WARPS);
+    const int end = first_step<NF>(c, steps, warp + 1, WARPS);
     P ring(dyn, warp, lane);
     // the step asked for next: expert au, its rows, step as
     int ask = at, au = steps > 0 ? at / steps : 0, as = at - au * steps;
