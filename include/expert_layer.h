@@ -94,16 +94,22 @@ int sgemm_experts_combine_grad(int type, int T, int k, int E, int H, const void 
  * ids: T x k (an id outside 0 .. E-1 is a dropped choice; a token may choose
  * an expert twice); weights: T x k fp32, NULL means 1 everywhere.  Rows of W1
  * and W2 start on 16-byte boundaries (bases, leading dimensions and strides).
- * T * k <= 512, H and F <= 65536.
+ * T <= 64, T * k <= 512, H and F <= 65536.
  * Products are exact where weights are 8-bit; sums are fp32; h is kept in two
  * values of the row type between the products, to twice its digits (fp16: to
  * 2^-36 at the least, and an h beyond 65504 is an infinity);
  * out is summed over the experts in fp32, in an order fixed by ids and the
  * sizes, and rounded once.  Only experts that a kept choice names are read.  A
  * token without kept choices gets zeros.  out may not overlap x.
- * workspace: 16-byte aligned, at least the size below; a call does not read
- * what it did not write there; calls that may run at the same time need one
- * each. */
+ * workspace: 16-byte aligned, at least the size below (0 for sizes that the
+ * layer refuses, too); a call does not read what it did not write there; calls
+ * that may run at the same time need one each.
+ * For more tokens there are the calls above: sort, dispatch_i8, sgemm_i8_experts
+ * with W1, sgemm_i8_quantize_rows with SGEMM_ACT_SWIGLU, sgemm_i8_experts with W2,
+ * combine.  They also round the activations to 8 bits, and with 8-bit weights are
+ * the faster way from some nine tokens on (32 experts of 2048 x 1024, 4 a token,
+ * us: 1 token 14 here, 25 there; 8 tokens 34, 35; 16 tokens 54, 43; 64 tokens 115,
+ * 59). */
 #define SGEMM_EXPERTS_I8 0
 #define SGEMM_EXPERTS_SAME 1
 size_t sgemm_experts_layer_workspace_size(int T, int k, int H, int F);
