@@ -71,8 +71,10 @@ size_t sgemm_fp4_scales_size(int format, int rows, int K);
  * The gated activation is held in fp32, each value within 8 units of fp32's last
  * place (gates below -87, whose exponential is subnormal: 2^-141 |X[r][K + k]|
  * besides).
+ *  - A zero's code has the value's sign (0 or 8).
  *  - NV: a row whose largest magnitude is below 2^-100 (zeros among them) gets
- *    row scale 0, block scales 0 and codes 0.
+ *    row scale 0, block scales 0 and codes of zeros; so does a block whose scale
+ *    rounds to 0.
  *  - A row that holds an infinity or NaN, or whose gated activation leaves
  *    fp32's range, gets row scale NaN, block scales 0 and codes 0.
  * Codes from K to the next multiple of 8, and block scales from the last block
