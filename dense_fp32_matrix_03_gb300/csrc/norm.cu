@@ -40,6 +40,7 @@ struct Args {
     long long px, pr, ps, py;  // row pitches in bytes
     unsigned char *q;          // few bits: codes, bytes per row
     long long pq;
+    bool whole_codes;  // 8 bits: a vector's codes on a boundary of theirs
     unsigned char *sf;
     long long sf_tiles;
     float *scale;
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(256, 3) norm_kernel(const Args a)
 #pragma unroll
             for (int i = 0; i < EV; ++i)
                 c[i] = some ? __float_as_uint(__fadd_rn(__fmul_rn(f[i] * g[i], inv), kRound)) : 0u;
-            if (LB == VB && a.sf_tiles != 0) {  // (8 bits: codes on boundaries of a vector's)
+            if (LB == VB && a.whole_codes) {
 #pragma unroll
                 for (int i = 0; i < EV; i += 4)
                     c[i / 4] = __byte_perm(__byte_perm(c[i], c[i + 1], 0x0040),
@@ -311,7 +312,7 @@ struct Launch {
         constexpr int EV = Words<T, VB>::N;
         Args a = args;
         a.nvec = vectors<T, VB, LB, OUT == kRow || OUT == kI8>(a.H);
-        if (OUT == kI8) a.sf_tiles = rows::aligned_to(a.q, EV) && a.pq % EV == 0;
+        a.whole_codes = OUT == kI8 && rows::aligned_to(a.q, EV) && a.pq % EV == 0;
         const int held = a.M <= num_sms ? 1 : kHeld;  // few rows: more threads on each
         const int tx = rows::pow2_threads((a.nvec + held - 1) / held, 32, 256), ty = 256 / tx;
         const dim3 block(static_cast<unsigned>(tx), static_cast<unsigned>(ty));

@@ -1,6 +1,7 @@
 // rows.cuh -- rows of bf16, fp16 or fp32 values moved in vectors of 2 to 16
 // bytes, and the host-side choice of the vector: shared by the row kernels
-// (experts.cu, quant.cu); the expert operators' limits.
+// (experts.cu, quant.cu: Vec; norm.cu, fp4_quant.cu: Words) and the products of
+// few bits; the expert operators' limits.
 #pragma once
 
 #include <cstdint>
