@@ -19,11 +19,13 @@
 // without registers or barriers.
 //
 // Measured on GB300, both kernels: one token, 4 of 32 experts of 2048 x 2048, 8 bits
-// (fp16 rows) 18.7 us (their 50 MB take 7.4), 16 bits 24.6; 16 tokens, 4 of 32 experts of
-// 2048 x 1024, 16 bits 66 (3.9 TB/s), 8 bits 54; 32 tokens, 4 of 64, 8 bits 126.  Few
-// tokens are bound by latency: ids, weights and sums in sequence, twice; more by
-// the loads in flight and, in 8 bits, by widening: weights are widened once for
-// each eight tokens of an expert (down: four, in two columns each).
+// (fp16 rows) 18.8 us (their 50 MB take 7.4), 16 bits 24.6; 16 tokens, 4 of 32 experts of
+// 2048 x 1024 (21 of them chosen), 16 bits 63 (4.2 TB/s), 8 bits 53; 32 tokens, 4 of 64
+// (40 chosen), 16 bits 114, 8 bits 94; 64 tokens, 2 of 8 of 4096 x 2048, 16 bits 249,
+// 8 bits 152.  Few tokens are bound by latency: ids, weights and sums in sequence,
+// twice; more by the loads in flight, those of the tokens among them, and, in 8 bits,
+// by widening: both recur for each eight tokens of an expert (down: four, in two
+// columns each).
 #include <type_traits>
 
 #include "../../include/expert_layer.h"
@@ -75,7 +77,7 @@ struct Choices {
 };
 
 // Fills `c` (all threads of the block call; WARPS: of them).  The loads pass L1
-// by: the down kernel is here while the up kernel still runs.
+// by: the down kernel may be here while blocks of the up kernel still run.
 template <int WARPS>
 __device__ __forceinline__ void find_choices(const Args &a, Choices &c)
 {
@@ -424,15 +426,18 @@ __device__ __forceinline__ void multiply(float (&acc)[CF][NF][4], const uint4 (&
 
 // ---------------------------------------------------------------------- up
 
-// Two blocks of eight warps a multiprocessor, two steps of 4 KB a warp on their way
-// (three leave room for one block: one token 24 us instead of 19).
+// Two steps of 4 KB a warp on their way (three leave room for one block of eight
+// warps: one token 20.0 us instead of 18.8).
 constexpr int kUpWarps = 8, kUpDepth = 2;
 template <class T, bool I8, int NF>
 struct Up {
     using P = Pieces<T, I8, 2, kUpDepth>;
     static constexpr int TK = 8 * NF, RING = kUpWarps * P::BYTES;
     static constexpr int SMEM = RING + kUpWarps * TK * (2 * kCh + 4) * 4;
-    static constexpr int BLOCKS = NF <= 4 ? 2 : 1;  // of a multiprocessor
+    // Blocks of a multiprocessor: one where the sums and the widened weights do not fit
+    // in half the registers (8 bits, 17 to 32 tokens: 94 us against 116 with two, which
+    // spill, for 32 tokens, 4 of 64 experts of 2048 x 1024).
+    static constexpr int BLOCKS = NF <= (I8 ? 2 : 4) ? 2 : 1;
 };
 
 // A unit is 16 rows of G and of U of one used expert; a block takes every
@@ -552,7 +557,8 @@ __global__ void __launch_bounds__(kUpWarps * 32, Up<T, I8, NF>::BLOCKS) up_kerne
 
 // -------------------------------------------------------------------- down
 
-// (eight warps with twice the steps on their way: 16 tokens 69 us instead of 61)
+// (eight warps with twice the steps on their way: 16 tokens in 16 bits 72 us instead
+// of 62, 32 tokens 133 instead of 114)
 // (sixteen groups of columns: their sums take the registers of half the threads)
 template <int NF>
 constexpr int kDownWarps = NF <= 8 ? 16 : 8;
@@ -607,7 +613,8 @@ __global__ void __launch_bounds__(kDownWarps<NF> * 32, 1) down_kernel(const Args
     dependent_release();
     // The up kernel releases its dependents after its own wait, so what it found
     // complete, ids and weights among it, is complete here too, and is read while
-    // it still runs.  (F == 0: there is no up kernel.)
+    // it still runs: on multiprocessors that its blocks have left, as a block of this
+    // kernel does not fit beside them.  (F == 0: there is no up kernel.)
     if (a.F == 0) dependent_wait();
     find_choices<WARPS>(a, c);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
