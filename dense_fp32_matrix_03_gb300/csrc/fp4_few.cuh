@@ -19,7 +19,7 @@
 // block share the steps of k of a few such channels and add their sums in order.
 //
 // Bound by instructions, about four a weight: one token through 1024 x 1024 2.8 us
-// (the tensor-core kernel 3.7), 2048 x 2048 3.6 (4.8), 4096 x 4096 8.1 (5.8).
+// (the tensor-core kernel 3.7), 2048 x 2048 3.7 (4.8), 4096 x 4096 8.1 (5.8).
 #pragma once
 
 #include "fp4_tc.cuh"

@@ -124,9 +124,9 @@ int run(const Args &a, cudaStream_t st)
             }
         }
     }
-    // us, narrow / wide: 128 x 4096 x 4096 8.2 / 9.6, 512 9.3 / 10.9, 1024 (256 tiles of the
-    // narrow kernel) 14.2 / 11.3, 512 x 8192 x 8192 23.2 / 17.2, 2048 x 2048 x 1024 8.0 /
-    // 7.3, 1024 x 4092 x 256 7.1 / 6.7: one wave of narrow tiles, or wide ones
+    // us, narrow / wide: 128 x 4096 x 4096 8.2 / 9.9, 512 9.3 / 11.0, 1024 (256 tiles of the
+    // narrow kernel) 14.2 / 11.5, 512 x 8192 x 8192 23.2 / 17.4, 2048 x 2048 x 1024 8.0 /
+    // 7.4, 1024 x 4092 x 256 7.1 / 6.7: one wave of narrow tiles, or wide ones
     if (kernel == SGEMM_FP4_KERNEL_AUTO)
         kernel = tiles > a.num_sms ? SGEMM_FP4_KERNEL_WIDE : SGEMM_FP4_KERNEL_NARROW;
     if (kernel == SGEMM_FP4_KERNEL_NARROW) split = shared_k<Narrow>(a, tiles);

@@ -6,8 +6,8 @@
 // values spans two to eight lanes, which find its maximum by shuffles.
 //
 // Bound by instructions, not HBM: some 25 a value, among them NV's division for
-// every block.  Measured on GB300, bf16: 8192 x 4096 22.9 us (NV; its bytes take
-// 12.6) and 20.3 (MX), gated 43.8 (43.1), one row 1.8.
+// every block.  Measured on GB300, bf16: 8192 x 4096 22.4 us (NV; its bytes take
+// 12.6) and 20.1 (MX), gated 43.7 (43.1), one row 1.8.
 #include "../../include/fp4_gemm.h"
 #include "dependent.cuh"
 #include "fp4.cuh"

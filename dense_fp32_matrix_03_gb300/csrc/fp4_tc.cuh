@@ -26,12 +26,13 @@
 // first weights (one CTA), then the epilogue (tensor memory -> scales -> result type -> staging -> C).  Every wait
 // is bounded.
 //
-// Measured on GB300, bf16 results: 8192 x 8192 x 4096 96 to 103 us (NV, 5300 to 5700
-// TFLOP/s, by box), x 8192 179 (MX 176), 4096^3 29, 1024 x 4096 x 4096 11.3; narrow 128 x 4096 x 4096 8.2; slim
-// 1 to 32 tokens x 4096 x 4096 5.8 to 6.4.  What bounds the wide form: at 8192^3 the
-// multiplies alone take 135 us and the loads alone 134 (19 TB/s out of L2, all five
-// stages on their way); together they share the multiprocessor's memory.  Four
-// stages cost 5%, three 20%.  What bounds the others: latency; a stage of k is
+// Measured on GB300, bf16 results: 8192 x 8192 x 4096 101 to 104 us (NV, 5300 to 5400
+// TFLOP/s, by box; in 32 bits 115), x 8192 183 to 188 (MX 180 to 184), 4096^3 30, 1024 x
+// 4096 x 4096 11.5; narrow 128 x 4096 x 4096 8.2; slim 1 to 32 tokens x 4096 x 4096 5.8
+// to 6.4.  What bounds the wide form: at 8192^3 the multiplies alone take 135 us and
+// the loads alone as long (19 TB/s out of L2, all five stages on their way; 134 us
+// with a pair's token scales loaded once); together they share the multiprocessor's
+// memory.  Four stages cost 5%, three 20%.  What bounds the others: latency; a stage of k is
 // 0.3 us, and a tile without any takes 2.5.
 #pragma once
 

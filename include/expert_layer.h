@@ -107,7 +107,7 @@ int sgemm_experts_combine_grad(int type, int T, int k, int E, int H, const void 
  * For more tokens there are the calls above: sort, dispatch_i8, sgemm_i8_experts
  * with W1, sgemm_i8_quantize_rows with SGEMM_ACT_SWIGLU, sgemm_i8_experts with W2,
  * combine.  They also round the activations to 8 bits, and with 8-bit weights are
- * the faster way from some nine tokens on (32 experts of 2048 x 1024, 4 a token,
+ * the faster way from some eight tokens on (32 experts of 2048 x 1024, 4 a token,
  * us: 1 token 14 here, 25 there; 8 tokens 34, 35; 16 tokens 54, 43; 64 tokens 115,
  * 59). */
 #define SGEMM_EXPERTS_I8 0
