@@ -336,7 +336,7 @@ struct Launch {
 // partial row, which the second kernel adds in the blocks' order.  (Columns
 // past the registers' are added up in the partial row itself.)  With two vectors a
 // thread, the next rows are on their way while these are reduced: two blocks of
-// 256 threads a multiprocessor, 8192 x 4096 bf16 50.9 us (5.3 TB/s; without the rows
+// 256 threads a multiprocessor, 8192 x 4096 bf16 51.4 us (5.2 TB/s; without the rows
 // ahead 64, on three blocks, whose registers spill, 77, with one vector on 512
 // threads 72).
 
@@ -461,7 +461,10 @@ __global__ void __launch_bounds__(256, 2) grad_kernel(const GradArgs a)
         }
         const float n = static_cast<float>(a.H);
         const float rho = rsqrtf(__fdiv_rn(square, n) + a.eps);
-        const float c = rho * rho * __fdiv_rn(inner, n);
+        // (where the squares leave the range, so may s dy and its sum: rho 0 takes them
+        // out by s, not by a product that is an infinity already)
+        const float c = rho == 0.f ? 0.f : rho * rho * __fdiv_rn(inner, n);
+        const float one = rho == 0.f ? 0.f : 1.f;
         auto put = [&](unsigned v, const Words<T, VB> &x, const Words<T, VB> &g, const Words<T, VB> &wv,
                        const Words<T, VB> &d, float (&dyx)[EV]) {
             float fx[EV], fg[EV], f[EV], fd[EV];
@@ -472,7 +475,7 @@ __global__ void __launch_bounds__(256, 2) grad_kernel(const GradArgs a)
 #pragma unroll
             for (int i = 0; i < EV; ++i) {
                 f[i] = fmaf(rho, f[i] * fg[i] - fx[i] * c, fd[i]);
-                dyx[i] = fg[i] * fx[i];
+                dyx[i] = fg[i] * (fx[i] * one);
             }
             Words<T, VB> o;
             o.pack(f);

@@ -35,7 +35,8 @@
  * overlap inputs or each other.
  *
  * Arithmetic: fp32, one rounding to the row type; the sum of squares is held
- * in fp32, and where it leaves fp32's range (4096 values of 2^58) rho is 0.  dweight's sums
+ * in fp32, and where it leaves fp32's range (4096 values of 2^58) rho is 0: y
+ * is zeros, dx is dsum, and the row adds nothing to dweight.  dweight's sums
  * run in an order fixed by the sizes and the alignment: repeated calls give the
  * same bits.  eps must be a normal positive fp32 number.
  *
